@@ -533,6 +533,127 @@ bl_path bitlinear_select_path(int64_t M, int64_t K, int64_t N,
  */
 bl_status bitlinear_device_error(int32_t* code, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Backward pass and adapters.
+ *
+ * The backward pass is the pages' straight-through estimator ([Production]
+ * WeightQuantizerSTE and ActivationQuantizerSTE: the gradient passes the
+ * rounding unchanged), so with W^ = gamma W~ and x^ = x~ eta / 127
+ *   dx = dy W^        dW = dy^T x^
+ * The 8-bit tokens (x~, eta) that the forward pass made are all it keeps of
+ * its activations; the latent weights are not read.
+ *
+ * Conventions beside those above, for every call of this part:
+ *   - dy, dn (gradients coming in) and the gradients going out are fp32 or
+ *     bf16, row-major and dense.  Sums are held in fp32 (or finer); an
+ *     output is rounded once.  Unlike the forward pass the results are
+ *     floating-point sums: not bit-identical to an oracle's, but the same on
+ *     every run (no atomics).
+ *   - Big operands are 16-byte aligned (BL_ERR_ALIGNMENT otherwise): dy,
+ *     xq, packed, A, B, y, dx, dW, dA, dB; the workspace is 256-byte
+ *     aligned.  Sizes are free (any M, N, K, r).
+ *   - workspace: device scratch of at least the size its query returns (0
+ *     from the query also for sizes that the call refuses; a call whose
+ *     size is 0 takes NULL).  Overwritten; calls that may overlap on the
+ *     GPU, captured graphs that may replay at the same time among them,
+ *     need one each.
+ *   - M = 0 gives zero weight and adapter gradients and no other output.
+ *   - Errors: BL_ERR_INVALID_ARG for null pointers, sizes below 1 (M below
+ *     0), unknown dtypes or a workspace smaller than the query says;
+ *     BL_ERR_UNSUPPORTED for M or N of 2^30 and more, 127 K >= 2^31, N K or
+ *     M max(N, K) above 2^40.
+ */
+
+/*
+ * Input gradient dx = gamma (dy W~) through the packed weights.
+ *   dy      in   M x N, fp32 or bf16.
+ *   packed, gamma   in   as written by bitlinear_pack_weights for N x K.
+ *   dx      out  M x K, fp32 or bf16.
+ */
+size_t bitlinear_grad_input_workspace_bytes(int64_t M, int64_t N, int64_t K, bl_dtype dydt);
+bl_status bitlinear_grad_input(const void* dy, bl_dtype dydt, int64_t M, int64_t N, const uint8_t* packed,
+                               const float* gamma, int64_t K, void* dx, bl_dtype dxdt, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of the latent weights dW[n,k] = sum_m dy[m,n] x~[m,k] eta_m / 127
+ * from the 8-bit tokens.
+ *   dy        in   M x N, fp32 or bf16.
+ *   xq, eta   in   as written by bitlinear_quant_act or
+ *                  bitlinear_rmsnorm_quant_act (M x K, M).
+ *   dw        out  N x K, fp32 or bf16.
+ */
+size_t bitlinear_grad_weight_workspace_bytes(int64_t M, int64_t N, int64_t K, bl_dtype dydt, bl_dtype dwdt);
+bl_status bitlinear_grad_weight(const void* dy, bl_dtype dydt, const int8_t* xq, const float* eta, int64_t M,
+                                int64_t N, int64_t K, void* dw, bl_dtype dwdt, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * bitlinear_rmsnorm_quant_act that also writes rstd (fp32, M): the factor r
+ * each row was multiplied by, which bitlinear_rmsnorm_grad needs.
+ */
+bl_status bitlinear_rmsnorm_quant_act_rstd(const void* x, bl_dtype xdt, int64_t M, int64_t K, int8_t* xq,
+                                           float* eta, int32_t* xsum, float* rstd, void* stream);
+
+/*
+ * Backward pass of the normalisation from the 8-bit tokens: with
+ * n = x~ eta / 127 standing for the normalised row,
+ *   dx = rstd (dn - n mean_k(n dn)).
+ *   dn        in   M x K, fp32 or bf16: the gradient of the normalised rows
+ *                  (what bitlinear_grad_input returns).
+ *   xq, eta, rstd   in   as written by bitlinear_rmsnorm_quant_act_rstd.
+ *   dx        out  M x K, fp32 or bf16; may be dn itself when the types are
+ *                  the same.
+ * 1 <= K <= 2^24; any alignment of dn, xq and dx to their element size.
+ */
+bl_status bitlinear_rmsnorm_grad(const void* dn, bl_dtype dndt, const int8_t* xq, const float* eta,
+                                 const float* rstd, int64_t M, int64_t K, void* dx, bl_dtype dxdt,
+                                 void* stream);
+
+/*
+ * Low-rank adapters of many requests beside one ternary projection: token m
+ * uses adapter a = ids[m],
+ *   y = x^ W^T + scale_a (x^ A_a^T) B_a^T
+ * (the projection alone where ids[m] is outside [0, L), -1 by convention).
+ * The adapters read the same 8-bit tokens as the projection.  No counterpart
+ * on the pages.
+ *   xq, eta, xsum, packed, gamma, flags   in   as for bitlinear_forward_path.
+ *   A       in   bf16, L x r x K.
+ *   B       in   bf16, L x N x r.
+ *   scale   in   fp32, L (commonly alpha / r).
+ *   ids     in   int32, M, on the device; in any order.
+ *   L, r    in   1 <= L <= 65535, 1 <= r <= 128 (adapters of smaller rank:
+ *                zero rows of A); L r max(N, K) <= 2^40.
+ *   y       out  M x N, fp32 or bf16; the sum is rounded once.
+ * BL_FLAG_WEIGHTS_STATIC speaks of packed, gamma, A, B and scale.
+ */
+size_t bitlinear_forward_adapters_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r);
+bl_status bitlinear_forward_adapters(const int8_t* xq, const float* eta, const int32_t* xsum, int64_t M,
+                                     int64_t K, const uint8_t* packed, const float* gamma, int64_t N,
+                                     const void* A, const void* B, const float* scale, const int32_t* ids,
+                                     int64_t L, int64_t r, void* y, bl_dtype ydt, void* workspace,
+                                     size_t workspace_bytes, unsigned flags, void* stream);
+
+/*
+ * Backward pass of bitlinear_forward_adapters from the 8-bit tokens (the
+ * projection frozen): with v = scale_a dy B_a and u = scale_a x^ A_a^T,
+ *   dx   = dy W^ + v A_a                      M x K
+ *   dA_a = sum over the tokens of a: v^T x^   L x r x K
+ *   dB_a = sum over the tokens of a: dy^T u   L x N x r
+ * An adapter that no token uses gets zeros.  dx may be NULL (not computed;
+ * packed and gamma may then be NULL too), and so may dA and dB together.
+ *   dabdt   in   type of dA and dB, fp32 or bf16.
+ *   other arguments as for bitlinear_forward_adapters and
+ *   bitlinear_grad_input.
+ */
+size_t bitlinear_adapters_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t r,
+                                               bl_dtype dydt);
+bl_status bitlinear_adapters_grad(const void* dy, bl_dtype dydt, const int8_t* xq, const float* eta, int64_t M,
+                                  int64_t N, int64_t K, const uint8_t* packed, const float* gamma,
+                                  const void* A, const void* B, const float* scale, const int32_t* ids,
+                                  int64_t L, int64_t r, void* dx, bl_dtype dxdt, void* dA, void* dB,
+                                  bl_dtype dabdt, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Library version as "major.minor.patch" (static storage). */
 const char* bitlinear_version(void);
 

@@ -19,6 +19,7 @@ BL_FLAG_WEIGHTS_STATIC = 1
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I = ctypes.c_int
+_SZ = ctypes.c_size_t
 SIGNATURES = {
     "bitlinear_status_str": (ctypes.c_char_p, [_I]),
     "bitlinear_version": (ctypes.c_char_p, []),
@@ -51,6 +52,18 @@ SIGNATURES = {
     "bitlinear_packed3_stride": (_I64, [_I64]),
     "bitlinear_pack_weights3": (_I, [_P, _I64, _I64, _P, _P, _P, _P]),
     "bitlinear_forward3": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _I64, _P, _I, _P, _P]),
+    "bitlinear_grad_input_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I]),
+    "bitlinear_grad_input": (_I, [_P, _I, _I64, _I64, _P, _P, _I64, _P, _I, _P, _SZ, _P]),
+    "bitlinear_grad_weight_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I, _I]),
+    "bitlinear_grad_weight": (_I, [_P, _I, _P, _P, _I64, _I64, _I64, _P, _I, _P, _SZ, _P]),
+    "bitlinear_rmsnorm_quant_act_rstd": (_I, [_P, _I, _I64, _I64, _P, _P, _P, _P, _P]),
+    "bitlinear_rmsnorm_grad": (_I, [_P, _I, _P, _P, _P, _I64, _I64, _P, _I, _P]),
+    "bitlinear_forward_adapters_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "bitlinear_forward_adapters": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P, _I64, _I64,
+                                        _P, _I, _P, _SZ, ctypes.c_uint, _P]),
+    "bitlinear_adapters_grad_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I]),
+    "bitlinear_adapters_grad": (_I, [_P, _I, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64,
+                                     _P, _I, _P, _P, _I, _P, _SZ, _P]),
 }
 
 _lib = None

@@ -5,6 +5,7 @@ CUDA stream; every step of the layer runs in the library's CUDA kernels.
 Names follow the C entry points: ``pack_weights``, ``quant_act``,
 ``forward`` (plus ``BitLinear``, a small holder of one packed matrix).
 """
+import contextlib
 import ctypes
 
 import torch
@@ -122,10 +123,11 @@ def quant_act(x, stream=None, out=None):
     return xq, eta, xsum
 
 
-def rmsnorm_quant_act(x, stream=None, out=None):
+def rmsnorm_quant_act(x, stream=None, out=None, want_rstd=False):
     """RMSNorm (no affine, eps 1e-6) fused with the per-token quantiser.
     Activations (M x K, bf16, CUDA) -> (xq int8 M x K, eta fp32 M, xsum int32 M)
-    of the normalised rows."""
+    of the normalised rows; with want_rstd also rstd (fp32 M), the factor each
+    row was multiplied by (what rmsnorm_grad needs)."""
     _require_cuda(x)
     if x.dim() != 2 or x.dtype != torch.bfloat16:
         raise ValueError("x must be a 2-D bfloat16 tensor")
@@ -136,6 +138,12 @@ def rmsnorm_quant_act(x, stream=None, out=None):
                torch.empty(M, dtype=torch.float32, device=dev),
                torch.empty(M, dtype=torch.int32, device=dev))
     xq, eta, xsum = out
+    if want_rstd:
+        rstd = torch.empty(M, dtype=torch.float32, device=dev)
+        check(_lib.lib().bitlinear_rmsnorm_quant_act_rstd(
+            _ptr(x), _DTYPES[x.dtype], M, K, _ptr(xq), _ptr(eta), _ptr(xsum), _ptr(rstd),
+            _stream(stream)), "bitlinear_rmsnorm_quant_act_rstd")
+        return xq, eta, xsum, rstd
     check(_lib.lib().bitlinear_rmsnorm_quant_act(_ptr(x), _DTYPES[x.dtype], M, K, _ptr(xq),
                                                  _ptr(eta), _ptr(xsum), _stream(stream)),
           "bitlinear_rmsnorm_quant_act")
@@ -341,6 +349,206 @@ def forward3(xq, eta, xsum, packed3, gamma, N, out_dtype=torch.float32, want_int
                                         N, _ptr(y), _DTYPES[y.dtype], _ptr(y_int), _stream(stream)),
           "bitlinear_forward3")
     return (y, y_int) if want_int else y
+
+
+# ------------------------------------------------------------ backward pass, adapters
+
+_HERE = contextlib.nullcontext()
+
+
+def _place(stream, *ts):
+    """A context that makes the tensors' device, and `stream` where one is
+    given, the current ones, so that scratch and outputs belong to the stream
+    that the kernels run on.  All tensors have to be on one CUDA device (and
+    the stream on it) and contiguous."""
+    _require_cuda(*ts)
+    index = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != index:
+            raise ValueError("tensors must be on one device")
+    if stream is not None:
+        if stream.device.index != index:
+            raise ValueError("stream must be on the tensors' device")
+        return torch.cuda.stream(stream)
+    return _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+
+def _al16(t):
+    """The tensor itself, or a copy where its data does not start on 16 bytes
+    (a slice of a ragged tensor)."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _check(name, t, shape, *dtypes):
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
+        raise ValueError("%s must be %s of shape %s, not %s of %s" % (
+            name, " or ".join(str(d).replace("torch.", "") for d in dtypes), tuple(shape),
+            str(t.dtype).replace("torch.", ""), tuple(t.shape)))
+
+
+def _out(out, shape, dtype, dev, name="out"):
+    """The caller's output, checked, or a new one."""
+    if dtype not in _DTYPES:
+        raise ValueError("%s must be float32 or bfloat16" % name)
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _check(name, out, shape, *_DTYPES)
+    if not out.is_cuda or out.device != dev or not out.is_contiguous() or out.data_ptr() % 16:
+        raise ValueError("%s must be contiguous, on the inputs' device and 16-byte aligned" % name)
+    return out
+
+
+def _scratch(nbytes, dev):
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+
+
+def _codes(xq, eta, M):
+    if xq.dim() != 2 or xq.shape[0] != M:
+        raise ValueError("xq must be int8 with %d rows" % M)
+    _check("xq", xq, xq.shape, torch.int8)
+    _check("eta", eta, (M,), torch.float32)
+
+
+def _packed(packed, gamma, N, K):
+    _check("packed", packed, (N, (K + 3) // 4), torch.uint8)
+    _check("gamma", gamma, (1,), torch.float32)
+
+
+def _adapters(A, B, scale, ids, M, N, K):
+    """(L, r) of an adapter set whose shapes fit."""
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A must be L x r x K and B L x N x r")
+    L, r = A.shape[:2]
+    _check("A", A, (L, r, K), torch.bfloat16)
+    _check("B", B, (L, N, r), torch.bfloat16)
+    _check("scale", scale, (L,), torch.float32)
+    _check("ids", ids, (M,), torch.int32)
+    return L, r
+
+
+def grad_input(dy, packed, gamma, K, out_dtype=torch.bfloat16, stream=None, out=None):
+    """Input gradient dx = gamma (dy W~) (M x K) of the layer's output gradient
+    dy (M x N, fp32 or bf16), through the packed weights."""
+    if dy.dim() != 2 or dy.dtype not in _DTYPES:
+        raise ValueError("dy must be a 2-D float32 or bfloat16 tensor")
+    M, N = dy.shape
+    _packed(packed, gamma, N, K)
+    with _place(stream, dy, packed, gamma):
+        dx = _out(out, (M, K), out_dtype, dy.device)
+        L = _lib.lib()
+        dt = _DTYPES[dy.dtype]
+        nws = L.bitlinear_grad_input_workspace_bytes(M, N, K, dt)
+        ws = _scratch(nws, dy.device)
+        dy, packed = _al16(dy), _al16(packed)
+        check(L.bitlinear_grad_input(_ptr(dy), dt, M, N, _ptr(packed), _ptr(gamma), K, _ptr(dx),
+                                     _DTYPES[dx.dtype], _ptr(ws), nws, _stream(None)), "bitlinear_grad_input")
+    return dx
+
+
+def grad_weight(dy, xq, eta, out_dtype=torch.float32, stream=None, out=None):
+    """Gradient of the latent weights dW = dy^T (x~ eta / 127) (N x K) from the
+    8-bit tokens that the forward pass kept."""
+    if dy.dim() != 2 or dy.dtype not in _DTYPES:
+        raise ValueError("dy must be a 2-D float32 or bfloat16 tensor")
+    M, N = dy.shape
+    _codes(xq, eta, M)
+    K = xq.shape[1]
+    with _place(stream, dy, xq, eta):
+        dw = _out(out, (N, K), out_dtype, dy.device)
+        L = _lib.lib()
+        dt, wt = _DTYPES[dy.dtype], _DTYPES[dw.dtype]
+        nws = L.bitlinear_grad_weight_workspace_bytes(M, N, K, dt, wt)
+        ws = _scratch(nws, dy.device)
+        dy, xq = _al16(dy), _al16(xq)
+        check(L.bitlinear_grad_weight(_ptr(dy), dt, _ptr(xq), _ptr(eta), M, N, K, _ptr(dw), wt, _ptr(ws), nws,
+                                      _stream(None)), "bitlinear_grad_weight")
+    return dw
+
+
+def rmsnorm_grad(dn, xq, eta, rstd, out_dtype=torch.bfloat16, stream=None, out=None):
+    """Input gradient of the RMSNorm from the 8-bit tokens: dn (M x K, fp32 or
+    bf16) is the gradient of the normalised rows, xq, eta and rstd as
+    rmsnorm_quant_act(want_rstd=True) returned them."""
+    if dn.dim() != 2 or dn.dtype not in _DTYPES:
+        raise ValueError("dn must be a 2-D float32 or bfloat16 tensor")
+    M, K = dn.shape
+    _codes(xq, eta, M)
+    _check("xq", xq, (M, K), torch.int8)
+    _check("rstd", rstd, (M,), torch.float32)
+    with _place(stream, dn, xq, eta, rstd):
+        dx = _out(out, (M, K), out_dtype, dn.device)
+        check(_lib.lib().bitlinear_rmsnorm_grad(_ptr(dn), _DTYPES[dn.dtype], _ptr(xq), _ptr(eta), _ptr(rstd),
+                                                M, K, _ptr(dx), _DTYPES[dx.dtype], _stream(None)),
+              "bitlinear_rmsnorm_grad")
+    return dx
+
+
+def forward_adapters(xq, eta, xsum, packed, gamma, N, A, B, scale, ids, out_dtype=torch.bfloat16,
+                     weights_static=False, stream=None, out=None):
+    """The projection plus each token's own low-rank adapter, from the 8-bit
+    tokens: y = x^ W^T + scale_a (x^ A_a^T) B_a^T with a = ids[m] (none where
+    ids[m] is outside [0, L)).  A bf16 L x r x K, B bf16 L x N x r, scale fp32
+    L, ids int32 M."""
+    if xq.dim() != 2:
+        raise ValueError("xq must be 2-D")
+    M, K = xq.shape
+    _codes(xq, eta, M)
+    _check("xsum", xsum, (M,), torch.int32)
+    _packed(packed, gamma, N, K)
+    n_ad, r = _adapters(A, B, scale, ids, M, N, K)
+    with _place(stream, xq, eta, xsum, packed, gamma, A, B, scale, ids):
+        y = _out(out, (M, N), out_dtype, xq.device)
+        L = _lib.lib()
+        nws = L.bitlinear_forward_adapters_workspace_bytes(M, K, N, n_ad, r)
+        ws = _scratch(nws, xq.device)
+        xq, packed, A, B = _al16(xq), _al16(packed), _al16(A), _al16(B)
+        check(L.bitlinear_forward_adapters(
+            _ptr(xq), _ptr(eta), _ptr(xsum), M, K, _ptr(packed), _ptr(gamma), N, _ptr(A), _ptr(B),
+            _ptr(scale), _ptr(ids), n_ad, r, _ptr(y), _DTYPES[y.dtype], _ptr(ws), nws,
+            _lib.BL_FLAG_WEIGHTS_STATIC if weights_static else 0, _stream(None)), "bitlinear_forward_adapters")
+    return y
+
+
+def linear_adapters(x, packed, gamma, N, A, B, scale, ids, out_dtype=torch.bfloat16, rmsnorm=False,
+                    weights_static=False, stream=None, out=None):
+    """forward_adapters on tokens it quantises itself: x (M x K, fp32 or bf16),
+    RMS-normalised first with rmsnorm (bf16)."""
+    with _place(stream, x):
+        xq, eta, xsum = (rmsnorm_quant_act if rmsnorm else quant_act)(x)
+        return forward_adapters(xq, eta, xsum, packed, gamma, N, A, B, scale, ids, out_dtype=out_dtype,
+                                weights_static=weights_static, out=out)
+
+
+def adapters_grad(dy, xq, eta, packed, gamma, A, B, scale, ids, out_dtype=torch.bfloat16,
+                  grad_dtype=torch.bfloat16, want_dx=True, want_dab=True, stream=None):
+    """Backward pass of forward_adapters from the 8-bit tokens, the projection
+    frozen: (dx, dA, dB).  dx has out_dtype, dA and dB grad_dtype; what is not
+    wanted is None (packed and gamma may be None without dx)."""
+    if dy.dim() != 2 or dy.dtype not in _DTYPES:
+        raise ValueError("dy must be a 2-D float32 or bfloat16 tensor")
+    if not (want_dx or want_dab):
+        raise ValueError("nothing is wanted")
+    M, N = dy.shape
+    _codes(xq, eta, M)
+    K = xq.shape[1]
+    if want_dx:
+        _packed(packed, gamma, N, K)
+    n_ad, r = _adapters(A, B, scale, ids, M, N, K)
+    with _place(stream, dy, xq, eta, packed, gamma, A, B, scale, ids):
+        dev = dy.device
+        dx = _out(None, (M, K), out_dtype, dev) if want_dx else None
+        dA = _out(None, A.shape, grad_dtype, dev) if want_dab else None
+        dB = _out(None, B.shape, grad_dtype, dev) if want_dab else None
+        L = _lib.lib()
+        dt = _DTYPES[dy.dtype]
+        nws = L.bitlinear_adapters_grad_workspace_bytes(M, N, K, n_ad, r, dt)
+        ws = _scratch(nws, dev)
+        dy, xq, packed, A, B = _al16(dy), _al16(xq), _al16(packed), _al16(A), _al16(B)
+        check(L.bitlinear_adapters_grad(
+            _ptr(dy), dt, _ptr(xq), _ptr(eta), M, N, K, _ptr(packed), _ptr(gamma), _ptr(A), _ptr(B),
+            _ptr(scale), _ptr(ids), n_ad, r, _ptr(dx), _DTYPES[out_dtype], _ptr(dA), _ptr(dB),
+            _DTYPES[grad_dtype], _ptr(ws), nws, _stream(None)), "bitlinear_adapters_grad")
+    return dx, dA, dB
 
 
 def select_path(M, K, N, xq, packed, y, y_int=None):

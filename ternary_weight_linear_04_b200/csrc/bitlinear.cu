@@ -27,6 +27,9 @@
 #include "quant.cuh"
 #include "rmsnorm_rows.cuh"
 #include "rmsnorm.cuh"
+#include "grad.cuh"
+#include "rmsnorm_grad.cuh"
+#include "adapters.cuh"
 
 namespace {
 
@@ -821,8 +824,8 @@ bool rows_stream_geometry(int64_t M, int64_t K, int sms, RowsGeom* g) {
 // CTAs than are resident at once.
 template <typename Kern>
 bl_status launch_rows_stream(Kern kern, int* done, const __nv_bfloat16* x, int64_t M, int64_t K,
-                             int8_t* xq, float* eta, int32_t* xsum, const RowsGeom& g, int sms,
-                             cudaStream_t s) {
+                             int8_t* xq, float* eta, int32_t* xsum, float* rstd, const RowsGeom& g,
+                             int sms, cudaStream_t s) {
   if (!ensure_smem(kern, g.smem, done)) return BL_ERR_CUDA;
   int per_sm = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, bl::kRowsThreads, g.smem) !=
@@ -834,7 +837,7 @@ bl_status launch_rows_stream(Kern kern, int* done, const __nv_bfloat16* x, int64
   const int64_t cap = static_cast<int64_t>(sms) * per_sm;
   const int64_t grid = g.grid < cap ? g.grid : cap;
   return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(bl::kRowsThreads), g.smem, s, x,
-                    M, K, g.stages, xq, eta, xsum);
+                    M, K, g.stages, xq, eta, xsum, rstd);
 }
 
 // bf16 rows with 16-byte vectors.  A few rows (decode, latency): one
@@ -858,6 +861,37 @@ bl_status launch_quant_bf16(const __nv_bfloat16* x, int64_t M, int64_t K, int8_t
   if (K <= 8192) return launch_quant_bf16_nt<256, 4>(x, M, K, xq, eta, xsum, grid, s);
   if (K <= 16384) return launch_quant_bf16_nt<512, 4>(x, M, K, xq, eta, xsum, grid, s);
   return launch_quant_bf16_nt<1024, 4>(x, M, K, xq, eta, xsum, grid, s);
+}
+
+// bitlinear_rmsnorm_quant_act, with the reciprocal root mean square of each
+// row written too where rstd is given.
+bl_status rmsnorm_quant_impl(const void* x, bl_dtype xdt, int64_t M, int64_t K, int8_t* xq, float* eta,
+                             int32_t* xsum, float* rstd, void* stream) {
+  if (M < 0 || K < 1 || (xdt != BL_F32 && xdt != BL_BF16)) return BL_ERR_INVALID_ARG;
+  if (M == 0) return BL_OK;
+  if (!x || !xq || !eta || !xsum) return BL_ERR_INVALID_ARG;
+  if (xdt != BL_BF16) return BL_ERR_UNSUPPORTED;  // the exact sum of squares needs bf16 inputs
+  if (K > (int64_t{1} << 24)) return BL_ERR_UNSUPPORTED;  // keeps xsum within int32
+  if (!aligned(x, 2) || !aligned(eta, 4) || !aligned(xsum, 4)) return BL_ERR_ALIGNMENT;
+  int sms = 148;
+  bl_status st = device_info(&sms);
+  if (st != BL_OK) return st;
+  const int vec = (K % 8 == 0 && aligned(x, 16) && aligned(xq, 8)) ? 1 : 0;
+  // Rows with 16-byte vectors up to K = 51200: streamed through shared
+  // memory, the sum of squares in fp64 with a proof (k_rmsnorm_rows); the
+  // rest: one CTA per row, the sum of squares exact (k_rmsnorm_quant).
+  RowsGeom g;
+  if (vec && rows_stream_geometry(M, K, sms, &g)) {
+    static int done_rows[kMaxDevices] = {0};
+    return launch_rows_stream(bl::k_rmsnorm_rows, done_rows, static_cast<const __nv_bfloat16*>(x), M, K,
+                              xq, eta, xsum, rstd, g, sms, as_stream(stream));
+  }
+  static int carve_done[kMaxDevices] = {0};
+  if (!ensure_smem(bl::k_rmsnorm_quant, 0, carve_done)) return BL_ERR_CUDA;
+  const int64_t ctas = M < static_cast<int64_t>(sms) * 8 ? M : static_cast<int64_t>(sms) * 8;
+  return launch_pdl(bl::k_rmsnorm_quant, dim3(static_cast<unsigned>(ctas)), dim3(256), 0,
+                    as_stream(stream), static_cast<const __nv_bfloat16*>(x), M, K, vec, xq, eta,
+                    xsum, rstd);
 }
 
 // Workspace of the single-matrix pack: the 256 exponent buckets (2048
@@ -1131,31 +1165,14 @@ bl_status bitlinear_pack_weights(const float* W, int64_t N, int64_t K, uint8_t* 
 
 bl_status bitlinear_rmsnorm_quant_act(const void* x, bl_dtype xdt, int64_t M, int64_t K,
                                       int8_t* xq, float* eta, int32_t* xsum, void* stream) {
-  if (M < 0 || K < 1 || (xdt != BL_F32 && xdt != BL_BF16)) return BL_ERR_INVALID_ARG;
-  if (M == 0) return BL_OK;
-  if (!x || !xq || !eta || !xsum) return BL_ERR_INVALID_ARG;
-  if (xdt != BL_BF16) return BL_ERR_UNSUPPORTED;  // the exact sum of squares needs bf16 inputs
-  if (K > (int64_t{1} << 24)) return BL_ERR_UNSUPPORTED;  // keeps xsum within int32
-  if (!aligned(x, 2) || !aligned(eta, 4) || !aligned(xsum, 4)) return BL_ERR_ALIGNMENT;
-  int sms = 148;
-  bl_status st = device_info(&sms);
-  if (st != BL_OK) return st;
-  const int vec = (K % 8 == 0 && aligned(x, 16) && aligned(xq, 8)) ? 1 : 0;
-  // Rows with 16-byte vectors up to K = 51200: streamed through shared
-  // memory, the sum of squares in fp64 with a proof (k_rmsnorm_rows); the
-  // rest: one CTA per row, the sum of squares exact (k_rmsnorm_quant).
-  RowsGeom g;
-  if (vec && rows_stream_geometry(M, K, sms, &g)) {
-    static int done_rows[kMaxDevices] = {0};
-    return launch_rows_stream(bl::k_rmsnorm_rows, done_rows, static_cast<const __nv_bfloat16*>(x), M, K,
-                              xq, eta, xsum, g, sms, as_stream(stream));
-  }
-  static int carve_done[kMaxDevices] = {0};
-  if (!ensure_smem(bl::k_rmsnorm_quant, 0, carve_done)) return BL_ERR_CUDA;
-  const int64_t ctas = M < static_cast<int64_t>(sms) * 8 ? M : static_cast<int64_t>(sms) * 8;
-  return launch_pdl(bl::k_rmsnorm_quant, dim3(static_cast<unsigned>(ctas)), dim3(256), 0,
-                    as_stream(stream), static_cast<const __nv_bfloat16*>(x), M, K, vec, xq, eta,
-                    xsum);
+  return rmsnorm_quant_impl(x, xdt, M, K, xq, eta, xsum, nullptr, stream);
+}
+
+bl_status bitlinear_rmsnorm_quant_act_rstd(const void* x, bl_dtype xdt, int64_t M, int64_t K, int8_t* xq,
+                                           float* eta, int32_t* xsum, float* rstd, void* stream) {
+  if (M > 0 && !rstd) return BL_ERR_INVALID_ARG;
+  if (!aligned(rstd, 4)) return BL_ERR_ALIGNMENT;
+  return rmsnorm_quant_impl(x, xdt, M, K, xq, eta, xsum, rstd, stream);
 }
 
 int64_t bitlinear_packed3_stride(int64_t K) {
@@ -1472,3 +1489,5 @@ bl_status bitlinear_device_error(int32_t* code, void* stream) {
 }
 
 }  // extern "C"
+
+#include "train_host.cuh"

@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(256) k_rmsnorm_quant(const __nv_bfloat16* __re
                                                         int64_t M, int64_t K, int vec,
                                                         int8_t* __restrict__ xq,
                                                         float* __restrict__ eta_out,
-                                                        int32_t* __restrict__ xsum_out) {
+                                                        int32_t* __restrict__ xsum_out,
+                                                        float* __restrict__ rstd_out) {
   __shared__ unsigned long long sb[kBuckets];  // terms below the register window
   __shared__ unsigned long long red_lo[8], red_hi[8];
   __shared__ float redf[8];
@@ -232,6 +233,7 @@ __global__ void __launch_bounds__(256) k_rmsnorm_quant(const __nv_bfloat16* __re
     if (tid == 0) {
       eta_out[m] = eta;
       xsum_out[m] = sum;
+      if (rstd_out) rstd_out[m] = r;
     }
     __syncthreads();  // before the next row clears the buckets
   }

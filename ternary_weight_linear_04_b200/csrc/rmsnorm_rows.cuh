@@ -85,7 +85,8 @@ __global__ void __launch_bounds__(kRowsThreads) k_rmsnorm_rows(const __nv_bfloat
                                                                     int64_t M, int64_t K, int stages,
                                                                     int8_t* __restrict__ xq,
                                                                     float* __restrict__ eta_out,
-                                                                    int32_t* __restrict__ xsum_out) {
+                                                                    int32_t* __restrict__ xsum_out,
+                                                                    float* __restrict__ rstd_out) {
   constexpr int NT = kRowsThreads;
   constexpr int NWARP = NT / 32;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -230,6 +231,7 @@ __global__ void __launch_bounds__(kRowsThreads) k_rmsnorm_rows(const __nv_bfloat
     if (tid == 0) {
       eta_out[r] = eta;
       xsum_out[r] = sum;
+      if (rstd_out) rstd_out[r] = rn;
       const int64_t rn2 = r + stages * G;
       if (rn2 < M) {
         mbar_arrive_expect_tx(&bar[s], row_bytes);

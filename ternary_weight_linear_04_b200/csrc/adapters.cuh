@@ -16,11 +16,6 @@
 
 namespace bl {
 
-__device__ __forceinline__ int adapter_of(const int32_t* ids, int64_t m, int L) {
-  const int a = ids[m];
-  return static_cast<unsigned>(a) < static_cast<unsigned>(L) ? a : -1;
-}
-
 __device__ __forceinline__ float warp_sum(float s) {
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
   return s;

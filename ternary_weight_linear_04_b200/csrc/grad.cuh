@@ -1,13 +1,21 @@
-// grad.cuh -- backward pass of the ternary layer (straight-through
-// estimator: the rounding of x and W passes gradients unchanged).
+// grad.cuh -- backward pass of the ternary layer on the tensor core.
 //
-//   dx[m,k] = gamma * sum_n dy[m,n] W~[n,k]
-//   dW[n,k] = sum_m dy[m,n] (x~[m,k] eta_m / 127)
+// The straight-through estimator passes gradients through the roundings
+// unchanged, so with W^ = gamma W~ and x^ = x~ eta / 127
 //
-// One thread per output element, fp32 sums.
+//   dx[m,k] = gamma sum_n dy[m,n] W~[n,k]          (k_grad_input)
+//   dW[n,k] = sum_m dy[m,n] x~[m,k] eta_m / 127    (k_grad_weight)
+//
+// Both are contractions of bf16 by bf16 values with fp32 accumulators
+// (tcgen05 kind::f16, accumulators in TMEM).  W~ has the values -1, 0, +1,
+// exact in bf16, so the products of dx are exact and only the sum rounds;
+// gamma is applied to the finished sum.
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
+#include "tc_bf16.cuh"
 
 namespace bl {
 
@@ -18,34 +26,659 @@ __device__ __forceinline__ float ld_f32<float>(const float* p) { return *p; }
 template <>
 __device__ __forceinline__ float ld_f32<__nv_bfloat16>(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-template <typename DyT, typename OutT>
+// The adapter of token m: ids[m], or -1 (none) when outside [0, L).
+__device__ __forceinline__ int adapter_of(const int32_t* ids, int64_t m, int L) {
+  const int a = ids[m];
+  return static_cast<unsigned>(a) < static_cast<unsigned>(L) ? a : -1;
+}
+
+// ---------------------------------------------------------------- operand copies
+
+// Rows of `bytes` bytes copied into rows of `stride` bytes (a multiple of
+// 16), the rest zero: operands whose rows do not start on 16 bytes cannot be
+// read by TMA.  One pass over the operand, small beside the product.
 __global__ void __launch_bounds__(256)
-    k_grad_input(const DyT* __restrict__ dy, int64_t M, int64_t N, const uint8_t* __restrict__ packed,
-                 const float* __restrict__ gamma, int64_t K, void* __restrict__ dx) {
-  const int64_t P = (K + 3) / 4;
-  const int64_t total = M * K;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int64_t m = i / K, k = i % K;
-    float s = 0.0f;
-    for (int64_t n = 0; n < N; ++n) {
-      const int c = (packed[n * P + (k >> 2)] >> (2 * (k & 3))) & 3;
-      s = __fmaf_rn(ld_f32(dy + m * N + n), static_cast<float>(c - 1), s);
+    k_pad_rows(const uint8_t* __restrict__ src, int64_t rows, int64_t bytes, int64_t stride,
+               uint8_t* __restrict__ dst) {
+  const int64_t chunks = stride / 16;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < rows * chunks; i += gridDim.x * 256ll) {
+    const int64_t row = i / chunks, c = (i - row * chunks) * 16;
+    const int64_t left = bytes - c;
+    const int64_t off = row * bytes + c;
+    uint32_t w[4];
+    if (off + 20 <= rows * bytes) {  // rows start anywhere: five aligned words, shifted together
+      const uint32_t* s4 = reinterpret_cast<const uint32_t*>(src + (off & ~int64_t{3}));
+      const unsigned sh = 8 * static_cast<unsigned>(off & 3);
+      uint32_t in[5];
+#pragma unroll
+      for (int j = 0; j < 5; ++j) in[j] = __ldg(s4 + j);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = __funnelshift_r(in[j], in[j + 1], sh);
+        const int64_t keep = left - 4 * j;  // bytes of this word inside the row
+        if (keep < 4) w[j] = keep <= 0 ? 0u : w[j] & (0xFFFFFFFFu >> (8 * (4 - keep)));
+      }
+    } else {  // the end of the tensor byte by byte
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (4 * j + b < left) w[j] |= static_cast<uint32_t>(src[off + 4 * j + b]) << (8 * b);
+      }
     }
-    store_out<OutT>(dx, i, __fmul_rn(s, *gamma));
+    *reinterpret_cast<uint4*>(dst + row * stride + c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-template <typename DyT, typename OutT>
+// fp32 rows as three bf16 planes (rows x cols_pad each, zero past cols) whose
+// sum is the fp32 value: 8 bits each of its 24, the differences exact.
 __global__ void __launch_bounds__(256)
-    k_grad_weight(const DyT* __restrict__ dy, const int8_t* __restrict__ xq, const float* __restrict__ eta,
-                  int64_t M, int64_t N, int64_t K, void* __restrict__ dw) {
-  const int64_t total = N * K;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int64_t n = i / K, k = i % K;
-    float s = 0.0f;
-    for (int64_t m = 0; m < M; ++m)
-      s = __fmaf_rn(ld_f32(dy + m * N + n), __fmul_rn(static_cast<float>(xq[m * K + k]), div127_rn(eta[m])), s);
-    store_out<OutT>(dw, i, s);
+    k_split_planes(const float* __restrict__ src, int64_t rows, int64_t cols, int64_t cols_pad,
+                   __nv_bfloat16* __restrict__ dst) {
+  const int64_t plane = rows * cols_pad;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < plane; i += gridDim.x * 256ll) {
+    const int64_t row = i / cols_pad, c = i - row * cols_pad;
+    const float f = c < cols ? src[row * cols + c] : 0.0f;
+    const __nv_bfloat16 a = __float2bfloat16_rn(f);
+    const float fa = __fsub_rn(f, __bfloat162float(a));
+    const __nv_bfloat16 b = __float2bfloat16_rn(fa);
+    dst[i] = a;
+    dst[plane + i] = b;
+    dst[2 * plane + i] = __float2bfloat16_rn(__fsub_rn(fa, __bfloat162float(b)));
+  }
+}
+
+// ---------------------------------------------------------------- input gradient
+//
+// Tile: 128 H tokens (TMEM lanes, H accumulators) by 256 inputs k (columns),
+// the contraction over n in steps of 64.  Per step:
+//   * the dy tile (128 H x 64, K-major, 128-byte swizzle) by TMA;
+//   * the packed tile (64 rows n x 64 bytes) by TMA through its own ring of
+//     stages, expanded by eight warps to bf16 (64 x 256, MN-major: k
+//     contiguous as in the packed rows, so nothing is transposed).  A code c
+//     in {0,1,2} becomes bits 0x4300 | c = 128 + c in bf16, minus 129: two
+//     codes a lane-instruction.  The pair in one register is (k, k + 8) of
+//     its 16, which leaves the columns of a 16-group in the order 0 8 1 9 ..
+//     7 15; the epilogue puts them back by naming registers;
+//   * eight (H = 2) MMAs 128 x 256 x 16.
+// H = 2 shares one expanded tile between two MMAs of 128 tokens; H = 1 is
+// for token counts that would leave the second half empty.
+//
+// Adapters: behind the steps over n come steps over the adapters of the
+// tile's tokens, whose operands the eight warps write: v (each token's row
+// masked to its own adapter, divided by gamma because the sum is multiplied
+// by it at the end) in two bf16 parts against A_a twice, 64 entries a step.
+
+constexpr int kGiBK = 64;    // n per step
+constexpr int kGiBN = 256;   // inputs k per tile
+constexpr int kGiWarps = 8;  // expanding warps
+constexpr int kGiThreads = 32 * (2 + kGiWarps);
+
+template <int H>
+struct GiCfg {
+  static constexpr int kStages = H == 2 ? 3 : 4;
+  static constexpr int kPStages = 6;
+  static constexpr int kABytes = H * 128 * 128;    // dy tile
+  static constexpr int kBBytes = kGiBK * kGiBN * 2;  // expanded weights
+  static constexpr int kPBytes = kGiBK * kGiBN / 4;  // packed weights
+  static constexpr int kBars = 3 * kStages + 2 * kPStages + 2;
+  static constexpr int kTail = 8 * kBars + 16 + 4 * (2 * 128 * H + 16);
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * (kABytes + kBBytes) + kPStages * kPBytes + kTail;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
+
+struct GiArgs {
+  const float* gamma;
+  int M, N, K;       // N: contraction, K: output columns
+  int planes;        // bf16 planes of dy
+  void* dx;
+  int vec;           // rows of dx take 16-byte stores
+  // adapters (v NULL: none)
+  const float* v;    // M x r
+  const __nv_bfloat16* A;  // L x r x K
+  const int32_t* ids;
+  int L, r;
+};
+
+// The distinct adapters of a tile's tokens in order of first use: s_ids[t]
+// for t < BM and s_list; returns their number.  Every thread of the block
+// calls it; BM <= 256 <= threads.
+__device__ __forceinline__ int tile_adapters(const int32_t* ids, int64_t m0, int M, int BM, int L, int* s_ids,
+                                             int* s_list, int* s_cnt) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int id = t < BM && m0 + t < M ? adapter_of(ids, m0 + t, L) : -1;
+  if (t < BM) s_ids[t] = id;
+  __syncthreads();
+  const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
+  bool first = id >= 0 && lane == __ffs(same) - 1;
+  if (first)
+    for (int j = 0; j < 32 * warp; ++j)
+      if (s_ids[j] == id) {
+        first = false;
+        break;
+      }
+  const unsigned firsts = __ballot_sync(0xFFFFFFFFu, first);
+  if (lane == 0 && warp < 8) s_cnt[warp] = __popc(firsts);
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) before += s_cnt[w];
+    total += s_cnt[w];
+  }
+  if (first) s_list[before + __popc(firsts & ((1u << lane) - 1))] = id;
+  __syncthreads();
+  return total;
+}
+
+// Sixteen bf16 of a row of the factor in the column order of the expanded
+// weights (pairs (i, i + 8)); zero past `left`.
+__device__ __forceinline__ void load16_paired(const __nv_bfloat16* p, int64_t left, bool vec, uint32_t (&o)[8]) {
+  uint32_t w[8];
+  if (left >= 16 && vec) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 8);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  } else {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[i] = (2 * i < left ? h[2 * i] : 0u) | (2 * i + 1 < left ? static_cast<uint32_t>(h[2 * i + 1]) << 16 : 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = __byte_perm(w[i >> 1], w[4 + (i >> 1)], (i & 1) ? 0x7632 : 0x5410);
+}
+
+template <int H, typename OutT>
+__global__ void __launch_bounds__(kGiThreads, 1)
+    k_grad_input(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_w, const GiArgs a) {
+  using Cfg = GiCfg<H>;
+  constexpr int S = Cfg::kStages, SP = Cfg::kPStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sA = base;
+  uint8_t* sB = sA + S * Cfg::kABytes;
+  uint8_t* sP = sB + S * Cfg::kBBytes;
+  uint64_t* full_a = reinterpret_cast<uint64_t*>(sP + SP * Cfg::kPBytes);  // dy tile in
+  uint64_t* full_b = full_a + S;      // weights expanded (8 warps)
+  uint64_t* empty = full_b + S;       // the MMAs are done with the stage
+  uint64_t* full_p = empty + S;       // packed tile in
+  uint64_t* empty_p = full_p + SP;    // packed tile read (8 warps)
+  uint64_t* accum_full = empty_p + SP;
+  uint64_t* drain = accum_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* s_ids = reinterpret_cast<int*>(tmem_slot + 4);
+  int* s_list = s_ids + 128 * H;
+  int* s_cnt = s_list + 128 * H;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ktiles = (a.K + kGiBN - 1) / kGiBN;
+  const int k0 = static_cast<int>(blockIdx.x % ktiles) * kGiBN, m0 = static_cast<int>(blockIdx.x / ktiles) * (128 * H);
+  const int steps_n = (a.N + kGiBK - 1) / kGiBK;
+  const int nst = steps_n * a.planes;
+
+  auto issue_p = [&](int i) {
+    const int s = i % SP;
+    mbar_arrive_expect_tx(full_p + s, Cfg::kPBytes);
+    tma_load_2d(sP + s * Cfg::kPBytes, &tm_w, full_p + s, k0 / 4, (i % steps_n) * kGiBK);
+  };
+  auto issue_a = [&](int i) {
+    const int s = i % S;
+    mbar_arrive_expect_tx(full_a + s, Cfg::kABytes);
+    tma_load_3d(sA + s * Cfg::kABytes, &tm_dy, full_a + s, (i % steps_n) * kGiBK, m0, i / steps_n);
+  };
+  const int a_first = nst < S ? nst : S, p_first = nst < SP ? nst : SP;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_a + s, 1);
+      mbar_init(full_b + s, kGiWarps);
+      mbar_init(empty + s, 1);
+    }
+    for (int s = 0; s < SP; ++s) {
+      mbar_init(full_p + s, 1);
+      mbar_init(empty_p + s, kGiWarps);
+    }
+    mbar_init(accum_full, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+    for (int i = 0; i < p_first; ++i) issue_p(i);
+    for (int i = 0; i < a_first; ++i) issue_a(i);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 256 * H);
+    tmem_relinquish();
+  }
+  int nadapt = 0, esteps = 0;  // adapters of the tile, steps of 64 entries for each
+  if (a.v) {
+    nadapt = tile_adapters(a.ids, m0, a.M, 128 * H, a.L, s_ids, s_list, s_cnt);
+    esteps = (2 * a.r + kGiBK - 1) / kGiBK;
+  }
+  const int nall = nst + nadapt * esteps;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_d = *tmem_slot;
+  bool epi_ok = false;
+  int issued = 0;
+
+  if (warp == 0) {
+    if (lane == 0) {  // dy tiles
+      issued = a_first;
+      for (int i = S; i < nst; ++i) {
+        if (!mbar_wait(empty + i % S, static_cast<uint32_t>(i / S - 1) & 1u, abort_flag)) break;
+        issue_a(i);
+        issued = i + 1;
+      }
+    } else if (lane == 1) {  // packed tiles
+      issued = p_first;
+      for (int i = SP; i < nst; ++i) {
+        if (!mbar_wait(empty_p + i % SP, static_cast<uint32_t>(i / SP - 1) & 1u, abort_flag)) break;
+        issue_p(i);
+        issued = i + 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = make_idesc_bf16(128, kGiBN, false, true);
+      const uint64_t a_desc0 = make_sw128_kmajor_desc(smem_u32(sA));
+      const uint64_t b_desc0 = make_sw128_mnmajor_desc(smem_u32(sB), kGiBK * 128);
+      bool ok = true;
+      for (int i = 0; i < nall; ++i) {
+        const int s = i % S;
+        const uint32_t par = static_cast<uint32_t>(i / S) & 1u;
+        ok = (i >= nst || mbar_wait(full_a + s, par, abort_flag)) && mbar_wait(full_b + s, par, abort_flag);
+        if (!ok) {
+          if (i > 0) {
+            tc_commit(drain);
+            mbar_drain(drain, 0);
+          }
+          break;
+        }
+        tc_fence_after();
+        const uint64_t ad = a_desc0 + static_cast<uint64_t>(s * (Cfg::kABytes >> 4));
+        const uint64_t bd = b_desc0 + static_cast<uint64_t>(s * (Cfg::kBBytes >> 4));
+#pragma unroll
+        for (int kk = 0; kk < kGiBK / 16; ++kk)
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            tc_mma_bf16_ss(tmem_d + 256 * h, ad + h * (16384 >> 4) + 2 * kk, bd + kk * (2048 >> 4), idesc,
+                           i != 0 || kk != 0 ? 1u : 0u);
+        tc_commit(empty + s);
+      }
+      if (ok) tc_commit(accum_full);
+    }
+  } else {
+    // ---------------- expand: thread = row n of the tile and 64 of its inputs
+    const int t = threadIdx.x - 64;
+    const int n = t & 63, q = t >> 6;
+    const uint32_t src_off = n * 64 + ((q ^ ((n >> 1) & 3)) << 4);  // 64-byte swizzle
+    uint8_t* const dst0 = sB + q * (kGiBK * 128) + (n >> 3) * 1024 + (n & 7) * 128;
+    bool ok = true;
+    for (int i = 0; i < nst; ++i) {
+      const int s = i % S, sp = i % SP;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(full_p + sp, static_cast<uint32_t>(i / SP) & 1u, abort_flag));
+      if (!ok) break;
+      const uint4 p = *reinterpret_cast<const uint4*>(sP + sp * Cfg::kPBytes + src_off);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty_p + sp);
+      if (i >= S) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + s, static_cast<uint32_t>(i / S - 1) & 1u, abort_flag));
+        if (!ok) break;
+      }
+      const uint32_t pw[4] = {p.x, p.y, p.z, p.w};
+      uint8_t* dst = dst0 + s * Cfg::kBBytes;
+#pragma unroll
+      for (int wi = 0; wi < 4; ++wi) {
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t c = ((pw[wi] >> (2 * j)) & 0x00030003u) | 0x43004300u;  // 128 + code
+          const __nv_bfloat162 d = __hsub2(reinterpret_cast<const __nv_bfloat162&>(c),
+                                           __nv_bfloat162(__float2bfloat16(129.0f), __float2bfloat16(129.0f)));
+          o[j] = reinterpret_cast<const uint32_t&>(d);
+        }
+        *reinterpret_cast<uint4*>(dst + (((2 * wi) ^ (n & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + (((2 * wi + 1) ^ (n & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full_b + s);
+    }
+    // ---------------- adapters: entry e of 2 r is v's first part (e < r) or its rest
+    const float inv_gamma = nall > nst ? __frcp_rn(*a.gamma) : 0.0f;
+    const bool avec = (a.K & 7) == 0;
+    for (int i = nst; ok && i < nall; ++i) {
+      const int s = i % S;
+      if (i >= S) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + s, static_cast<uint32_t>(i / S - 1) & 1u, abort_flag));
+        if (!ok) break;
+      }
+      const int ad = s_list[(i - nst) / esteps], e0 = (i - nst) % esteps * kGiBK;
+      if (t < 128 * H) {  // this token's row of v
+        const bool mine = s_ids[t] == ad;
+        const float* vr = a.v + static_cast<int64_t>(m0 + t) * a.r;
+        uint8_t* row = sA + s * Cfg::kABytes + (t >> 3) * 1024 + (t & 7) * 128;
+#pragma unroll 2
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float f[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const int e = e0 + 8 * c + 2 * j + b;
+              float x = 0.0f;
+              if (mine && e < 2 * a.r) {
+                x = __fmul_rn(vr[e < a.r ? e : e - a.r], inv_gamma);
+                if (e >= a.r) x = __fsub_rn(x, __bfloat162float(__float2bfloat16_rn(x)));
+              }
+              f[b] = x;
+            }
+            o[j] = pack_bf16(f[0], f[1]);
+          }
+          *reinterpret_cast<uint4*>(row + ((c ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      const int e = e0 + n;
+      const __nv_bfloat16* ar = a.A + (static_cast<int64_t>(ad) * a.r + (e < a.r ? e : e - a.r)) * a.K;
+      uint8_t* dst = dst0 + s * Cfg::kBBytes;
+#pragma unroll 1
+      for (int wi = 0; wi < 4; ++wi) {
+        uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        const int k = k0 + 64 * q + 16 * wi;
+        if (e < 2 * a.r && k < a.K) load16_paired(ar + k, a.K - k, avec, o);
+        *reinterpret_cast<uint4*>(dst + (((2 * wi) ^ (n & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + (((2 * wi + 1) ^ (n & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full_b + s);
+    }
+    if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(accum_full, 0, abort_flag));
+    epi_ok = ok && __all_sync(0xFFFFFFFFu, *abort_flag == 0);
+  }
+
+  // After an abort the producers wait (bounded) for the loads that can still
+  // be in flight, so none lands in shared memory freed at exit.
+  __syncwarp();
+  __syncthreads();
+  if (warp == 0 && lane < 2 && *abort_flag) {
+    uint64_t* bars = lane == 0 ? full_a : full_p;
+    const int ring = lane == 0 ? S : SP;
+    for (int i = issued > ring ? issued - ring : 0; i < issued; ++i)
+      mbar_drain(bars + i % ring, static_cast<uint32_t>(i / ring) & 1u);
+  }
+
+  // ---------------- epilogue: one TMEM lane = one token
+  if (warp >= 2 && epi_ok) {
+    tc_fence_after();
+    const float gamma = *a.gamma;
+    const int qd = warp & 3, part = (warp - 2) >> 2;
+    // H = 2: the two warps of a lane quarter take one half of the tokens
+    // each; H = 1: half of the columns each
+    const int h = H == 2 ? part : 0;
+    const int c_begin = H == 2 ? 0 : part * 128, c_end = H == 2 ? 256 : c_begin + 128;
+    const int64_t m = static_cast<int64_t>(m0) + 128 * h + 32 * qd + lane;
+    const uint32_t trow = tmem_d + 256 * h + (static_cast<uint32_t>(qd * 32) << 16);
+#pragma unroll 1
+    for (int c = c_begin; c < c_end; c += 32) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(trow + c, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float f[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          f[j] = __fmul_rn(__uint_as_float(v[16 * g + 2 * j]), gamma);
+          f[8 + j] = __fmul_rn(__uint_as_float(v[16 * g + 2 * j + 1]), gamma);
+        }
+        if (m < a.M) store16<OutT>(a.dx, m * a.K, k0 + c + 16 * g, a.K, f, a.vec);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_d, 256 * H);
+  }
+}
+
+// ---------------------------------------------------------------- weight gradient
+//
+// Tile: 128 H outputs n (TMEM lanes) by 256 inputs k (columns), the
+// contraction over the tokens in steps of 32.  Both operands lie with the
+// contraction outermost, as the tensors do (MN-major): the dy tile comes by
+// TMA, the token codes through a ring of their own and eight warps that
+// multiply them by eta / 127 and write bf16.  PL = 2 keeps 16 bits of each
+// value in two bf16 tiles (fp32 results: the rounding of one bf16 factor,
+// 2^-9 relative, would show in them); PL = 1 rounds it once (bf16 results,
+// whose own rounding is as large).
+
+constexpr int kGwBM = 32;    // tokens per step
+constexpr int kGwBN = 256;   // inputs k per tile
+constexpr int kGwWarps = 8;
+constexpr int kGwThreads = 32 * (2 + kGwWarps);
+
+template <int H, int PL>
+struct GwCfg {
+  static constexpr int kStages = PL == 2 ? 4 : 5;
+  static constexpr int kXStages = 4;
+  static constexpr int kABytes = H * 128 * kGwBM * 2;
+  static constexpr int kBBytes = PL * kGwBN * kGwBM * 2;
+  static constexpr int kXBytes = kGwBN * kGwBM;
+  static constexpr int kBars = 3 * kStages + 2 * kXStages + 2;
+  static constexpr int kTail = 8 * kBars + 16;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * (kABytes + kBBytes) + kXStages * kXBytes + kTail;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
+
+template <int H, int PL, typename OutT>
+__global__ void __launch_bounds__(kGwThreads, 1)
+    k_grad_weight(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_x,
+                  const float* __restrict__ eta, int M, int N, int K, int planes, void* __restrict__ dw, int vec) {
+  using Cfg = GwCfg<H, PL>;
+  constexpr int S = Cfg::kStages, SX = Cfg::kXStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sA = base;
+  uint8_t* sB = sA + S * Cfg::kABytes;
+  uint8_t* sX = sB + S * Cfg::kBBytes;
+  uint64_t* full_a = reinterpret_cast<uint64_t*>(sX + SX * Cfg::kXBytes);
+  uint64_t* full_b = full_a + S;
+  uint64_t* empty = full_b + S;
+  uint64_t* full_x = empty + S;
+  uint64_t* empty_x = full_x + SX;
+  uint64_t* accum_full = empty_x + SX;
+  uint64_t* drain = accum_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ktiles = (K + kGwBN - 1) / kGwBN;
+  const int k0 = static_cast<int>(blockIdx.x % ktiles) * kGwBN, n0 = static_cast<int>(blockIdx.x / ktiles) * (128 * H);
+  const int steps_m = (M + kGwBM - 1) / kGwBM;
+  const int nst = steps_m * planes;
+
+  auto issue_x = [&](int i) {
+    const int s = i % SX, m = (i % steps_m) * kGwBM;
+    mbar_arrive_expect_tx(full_x + s, Cfg::kXBytes);
+    for (int j = 0; j < 2; ++j)
+      tma_load_2d(sX + s * Cfg::kXBytes + j * (128 * kGwBM), &tm_x, full_x + s, k0 + 128 * j, m);
+  };
+  auto issue_a = [&](int i) {
+    const int s = i % S, m = (i % steps_m) * kGwBM;
+    mbar_arrive_expect_tx(full_a + s, Cfg::kABytes);
+    for (int j = 0; j < 2 * H; ++j)
+      tma_load_3d(sA + s * Cfg::kABytes + j * (128 * kGwBM), &tm_dy, full_a + s, n0 + 64 * j, m, i / steps_m);
+  };
+  const int a_first = nst < S ? nst : S, x_first = nst < SX ? nst : SX;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_a + s, 1);
+      mbar_init(full_b + s, kGwWarps);
+      mbar_init(empty + s, 1);
+    }
+    for (int s = 0; s < SX; ++s) {
+      mbar_init(full_x + s, 1);
+      mbar_init(empty_x + s, kGwWarps);
+    }
+    mbar_init(accum_full, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+    for (int i = 0; i < x_first; ++i) issue_x(i);
+    for (int i = 0; i < a_first; ++i) issue_a(i);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 256 * H);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_d = *tmem_slot;
+  bool epi_ok = false;
+  int issued = 0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      issued = a_first;
+      for (int i = S; i < nst; ++i) {
+        if (!mbar_wait(empty + i % S, static_cast<uint32_t>(i / S - 1) & 1u, abort_flag)) break;
+        issue_a(i);
+        issued = i + 1;
+      }
+    } else if (lane == 1) {
+      issued = x_first;
+      for (int i = SX; i < nst; ++i) {
+        if (!mbar_wait(empty_x + i % SX, static_cast<uint32_t>(i / SX - 1) & 1u, abort_flag)) break;
+        issue_x(i);
+        issued = i + 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = make_idesc_bf16(128, kGwBN, true, true);
+      const uint64_t a_desc0 = make_sw128_mnmajor_desc(smem_u32(sA), kGwBM * 128);
+      const uint64_t b_desc0 = make_sw128_mnmajor_desc(smem_u32(sB), kGwBM * 128);
+      bool ok = true;
+      for (int i = 0; i < nst; ++i) {
+        const int s = i % S;
+        const uint32_t par = static_cast<uint32_t>(i / S) & 1u;
+        ok = mbar_wait(full_a + s, par, abort_flag) && mbar_wait(full_b + s, par, abort_flag);
+        if (!ok) {
+          if (i > 0) {
+            tc_commit(drain);
+            mbar_drain(drain, 0);
+          }
+          break;
+        }
+        tc_fence_after();
+        const uint64_t ad = a_desc0 + static_cast<uint64_t>(s * (Cfg::kABytes >> 4));
+        const uint64_t bd = b_desc0 + static_cast<uint64_t>(s * (Cfg::kBBytes >> 4));
+#pragma unroll
+        for (int kk = 0; kk < kGwBM / 16; ++kk)
+#pragma unroll
+          for (int p = 0; p < PL; ++p)
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+              tc_mma_bf16_ss(tmem_d + 256 * h, ad + h * ((2 * 128 * kGwBM) >> 4) + kk * (2048 >> 4),
+                             bd + p * ((kGwBN * kGwBM * 2) >> 4) + kk * (2048 >> 4), idesc,
+                             i != 0 || kk != 0 || p != 0 ? 1u : 0u);
+        tc_commit(empty + s);
+      }
+      if (ok) tc_commit(accum_full);
+    }
+  } else {
+    // ---------------- tokens to bf16: lane = token of the step, warp = 32 inputs
+    const int u = warp - 2;
+    const uint8_t* src0 = sX + (u >> 2) * (128 * kGwBM) + lane * 128;
+    uint8_t* const dst0 = sB + (u >> 1) * (128 * kGwBM) + (lane >> 3) * 1024 + (lane & 7) * 128;
+    bool ok = true;
+    for (int i = 0; i < nst; ++i) {
+      const int s = i % S, sx = i % SX;
+      const int m = (i % steps_m) * kGwBM + lane;
+      const float f = m < M ? div127_rn(__ldg(eta + m)) : 0.0f;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(full_x + sx, static_cast<uint32_t>(i / SX) & 1u, abort_flag));
+      if (!ok) break;
+      uint4 xv[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        xv[c] = *reinterpret_cast<const uint4*>(src0 + sx * Cfg::kXBytes + ((((u & 3) * 2 + c) ^ (lane & 7)) << 4));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty_x + sx);
+      if (i >= S) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + s, static_cast<uint32_t>(i / S - 1) & 1u, abort_flag));
+        if (!ok) break;
+      }
+      uint8_t* dst = dst0 + s * Cfg::kBBytes;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {  // 8 values each
+        const uint4& x4 = xv[c >> 1];
+        const uint32_t w2[2] = {(c & 1) ? x4.z : x4.x, (c & 1) ? x4.w : x4.y};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t ub = w2[j >> 1] ^ 0x80808080u;  // code + 128
+          // 2^23 + (code + 128) as bits, minus 2^23 + 128: the code, exact
+          const float v0 = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(ub, 0x4B000000u, (j & 1) ? 0x7442 : 0x7440)), 8388736.0f), f);
+          const float v1 = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(ub, 0x4B000000u, (j & 1) ? 0x7443 : 0x7441)), 8388736.0f), f);
+          hi[j] = pack_bf16(v0, v1);
+          if (PL == 2) lo[j] = pack_bf16_rest(v0, v1, hi[j]);
+        }
+        const uint32_t off = (((u & 1) * 4 + c) ^ (lane & 7)) << 4;
+        *reinterpret_cast<uint4*>(dst + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (PL == 2)
+          *reinterpret_cast<uint4*>(dst + kGwBN * kGwBM * 2 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full_b + s);
+    }
+    if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(accum_full, 0, abort_flag));
+    epi_ok = ok && __all_sync(0xFFFFFFFFu, *abort_flag == 0);
+  }
+
+  __syncwarp();
+  __syncthreads();
+  if (warp == 0 && lane < 2 && *abort_flag) {
+    uint64_t* bars = lane == 0 ? full_a : full_x;
+    const int ring = lane == 0 ? S : SX;
+    for (int i = issued > ring ? issued - ring : 0; i < issued; ++i)
+      mbar_drain(bars + i % ring, static_cast<uint32_t>(i / ring) & 1u);
+  }
+
+  // ---------------- epilogue: one TMEM lane = one output n
+  if (warp >= 2 && epi_ok) {
+    tc_fence_after();
+    const int qd = warp & 3, part = (warp - 2) >> 2;
+    const int h = H == 2 ? part : 0;
+    const int c_begin = H == 2 ? 0 : part * 128, c_end = H == 2 ? 256 : c_begin + 128;
+    const int64_t n = static_cast<int64_t>(n0) + 128 * h + 32 * qd + lane;
+    const uint32_t trow = tmem_d + 256 * h + (static_cast<uint32_t>(qd * 32) << 16);
+#pragma unroll 1
+    for (int c = c_begin; c < c_end; c += 32) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(trow + c, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float f[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[16 * g + j]);
+        if (n < N) store16<OutT>(dw, n * K, k0 + c + 16 * g, K, f, vec);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_d, 256 * H);
   }
 }
 

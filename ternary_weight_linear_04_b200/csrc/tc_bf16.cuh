@@ -1,0 +1,104 @@
+// tc_bf16.cuh -- tcgen05 kind::f16 (bf16 operands, fp32 accumulator) pieces
+// of the backward-pass kernels, from the public PTX ISA.
+#pragma once
+
+#include "common.cuh"
+
+namespace bl {
+
+// Instruction descriptor, kind::f16: fp32 accumulator (bits 4-5 = 1), A and B
+// bf16 (bits 7-9 and 10-12 = 1), A / B MN-major (bits 15 / 16), N >> 3 in
+// 17-22, M >> 4 in 24-28.
+__host__ __device__ constexpr uint32_t make_idesc_bf16(uint32_t M, uint32_t N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// D[tmem] (+)= A[smem] B[smem], kind::f16, one CTA.
+__device__ __forceinline__ void tc_mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Shared-memory descriptor of an MN-major operand in the 128-byte swizzle:
+// atoms of 8 rows of the contraction by 64 bf16 (128 bytes), the 16-byte
+// chunk index XORed with the row's index in its atom; atoms that follow one
+// another along the contraction lie 1024 bytes apart (stride byte offset),
+// along M or N `lbo` bytes apart (leading byte offset).
+__device__ __forceinline__ uint64_t make_sw128_mnmajor_desc(uint32_t smem_addr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(lbo >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* tmap, uint64_t* bar, int32_t c0,
+                                            int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// 32 lanes x 32 bit, 32 consecutive columns per thread.
+__device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]),
+        "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Two fp32 rounded to a bf16 pair (lo in the low half).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return reinterpret_cast<const uint32_t&>(p);
+}
+
+// (lo, hi) minus their bf16 pair, rounded to a bf16 pair: what the first
+// rounding left (the difference is exact), so that pair + rest hold 16 bits.
+__device__ __forceinline__ uint32_t pack_bf16_rest(float lo, float hi, uint32_t pair) {
+  return pack_bf16(__fsub_rn(lo, __uint_as_float(pair << 16)), __fsub_rn(hi, __uint_as_float(pair & 0xFFFF0000u)));
+}
+
+// Sixteen values of one output row at `col`, to fp32 or bf16; `vec`: 16-byte
+// stores are aligned and the sixteen are inside the row, else one by one up
+// to `cols`.
+template <typename OutT>
+__device__ __forceinline__ void store16(void* out, int64_t row_off, int64_t col, int64_t cols, const float (&v)[16],
+                                        bool vec) {
+  if (vec && col + 16 <= cols) {
+    if constexpr (sizeof(OutT) == 4) {
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + row_off + col);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+      uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + row_off + col);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        p[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                          pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (col + i < cols) store_out<OutT>(out, row_off + col + i, v[i]);
+  }
+}
+
+}  // namespace bl

@@ -47,13 +47,101 @@ inline unsigned grid_for(int64_t items, int64_t per, int sms) {
   return static_cast<unsigned>(g < 1 ? 1 : g);
 }
 
-template <typename DyT>
-bl_status launch_grad_input(const void* dy, int64_t M, int64_t N, const uint8_t* packed, const float* gamma,
-                            int64_t K, void* dx, bl_dtype dxdt, int sms, cudaStream_t s) {
-  const auto* d = static_cast<const DyT*>(dy);
-  const unsigned g = grid_for(M * K, 256, sms);
-  if (dxdt == BL_F32) bl::k_grad_input<DyT, float><<<g, 256, 0, s>>>(d, M, N, packed, gamma, K, dx);
-  else bl::k_grad_input<DyT, __nv_bfloat16><<<g, 256, 0, s>>>(d, M, N, packed, gamma, K, dx);
+// Row-major matrix (planes of it) of elem-byte values for TMA: cols of rows
+// of `stride` bytes, box of box_cols x box_rows; out-of-bounds values read as
+// zero.
+bool make_tmap(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, uint64_t cols, uint64_t rows,
+               uint64_t planes, uint64_t stride, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  auto enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {cols, rows, planes ? planes : 1};
+  const cuuint64_t strides[2] = {stride, stride * rows};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, type, planes ? 3 : 2, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An operand as TMA can read it: the caller's own rows when they start on 16
+// bytes, else a copy in the workspace (taken from it in either case of a
+// null base, so that queries and calls agree).
+struct Rows {
+  const void* p;
+  int64_t stride;  // bytes
+  int planes;
+};
+
+inline bl_status pad_rows(const void* src, int64_t rows, int64_t bytes, Scratch* ws, Rows* out, int sms,
+                          cudaStream_t s) {
+  *out = {src, bytes, 1};
+  if (bytes % 16 == 0) return BL_OK;
+  out->stride = round_up(bytes, 16);
+  void* dst = ws->take(static_cast<size_t>(rows * out->stride));
+  out->p = dst;
+  if (!ws->base || rows == 0) return BL_OK;
+  bl::k_pad_rows<<<grid_for(rows * (out->stride / 16), 256, sms), 256, 0, s>>>(
+      static_cast<const uint8_t*>(src), rows, bytes, out->stride, static_cast<uint8_t*>(dst));
+  return launch_status();
+}
+
+// dy as bf16 planes: one, or three of an fp32 dy.
+inline bl_status dy_rows(const void* dy, bl_dtype dydt, int64_t M, int64_t N, Scratch* ws, Rows* out, int sms,
+                         cudaStream_t s) {
+  if (dydt == BL_BF16) return pad_rows(dy, M, 2 * N, ws, out, sms, s);
+  const int64_t cols = round_up(N, 8);
+  void* dst = ws->take(static_cast<size_t>(3 * M * cols * 2));
+  *out = {dst, 2 * cols, 3};
+  if (!ws->base || M == 0) return BL_OK;
+  bl::k_split_planes<<<grid_for(M * cols, 256, sms), 256, 0, s>>>(static_cast<const float*>(dy), M, N, cols,
+                                                                   static_cast<__nv_bfloat16*>(dst));
+  return launch_status();
+}
+
+// Whether rows of `cols` values of type dt take 16-byte stores.
+inline int vec_rows(int64_t cols, bl_dtype dt) { return cols % (16 / dtype_bytes(dt)) == 0 ? 1 : 0; }
+
+template <int H, typename OutT>
+bl_status launch_gi(const CUtensorMap& tdy, const CUtensorMap& tw, const bl::GiArgs& a, cudaStream_t s) {
+  static int done[kMaxDevices] = {0};
+  auto kern = bl::k_grad_input<H, OutT>;
+  constexpr size_t smem = bl::GiCfg<H>::kSmem;
+  if (!ensure_smem(kern, smem, done)) return BL_ERR_CUDA;
+  const int64_t tiles = ((a.K + bl::kGiBN - 1) / bl::kGiBN) * ((int64_t{a.M} + 128 * H - 1) / (128 * H));
+  if (tiles > INT32_MAX) return BL_ERR_UNSUPPORTED;
+  kern<<<static_cast<unsigned>(tiles), bl::kGiThreads, smem, s>>>(tdy, tw, a);
+  return launch_status();
+}
+
+// dx = gamma dy W~ (+ v A where a.v is given); the operands' copies come out of ws.
+bl_status run_grad_input(const Rows& dy, const uint8_t* packed, bl_dtype dxdt, bl::GiArgs a, Scratch* ws, int sms,
+                         cudaStream_t s) {
+  Rows w;
+  bl_status st = pad_rows(packed, a.N, (a.K + 3) / 4, ws, &w, sms, s);
+  if (st != BL_OK) return st;
+  const int H = a.M > 128 ? 2 : 1;
+  CUtensorMap tdy, tw;
+  if (!make_tmap(&tdy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy.p, a.N, a.M, dy.planes, dy.stride, bl::kGiBK, 128 * H,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.p, (a.K + 3) / 4, a.N, 0, w.stride, bl::kGiBN / 4,
+                 bl::kGiBK, CU_TENSOR_MAP_SWIZZLE_64B))
+    return BL_ERR_CUDA;
+  a.planes = dy.planes;
+  a.vec = vec_rows(a.K, dxdt);
+  if (H == 2) return dxdt == BL_F32 ? launch_gi<2, float>(tdy, tw, a, s) : launch_gi<2, __nv_bfloat16>(tdy, tw, a, s);
+  return dxdt == BL_F32 ? launch_gi<1, float>(tdy, tw, a, s) : launch_gi<1, __nv_bfloat16>(tdy, tw, a, s);
+}
+
+template <int H, int PL, typename OutT>
+bl_status launch_gw(const CUtensorMap& tdy, const CUtensorMap& tx, const float* eta, int M, int N, int K, int planes,
+                    void* dw, int vec, cudaStream_t s) {
+  static int done[kMaxDevices] = {0};
+  auto kern = bl::k_grad_weight<H, PL, OutT>;
+  constexpr size_t smem = bl::GwCfg<H, PL>::kSmem;
+  if (!ensure_smem(kern, smem, done)) return BL_ERR_CUDA;
+  const int64_t tiles = ((K + bl::kGwBN - 1) / bl::kGwBN) * ((int64_t{N} + 128 * H - 1) / (128 * H));
+  if (tiles > INT32_MAX) return BL_ERR_UNSUPPORTED;
+  kern<<<static_cast<unsigned>(tiles), bl::kGwThreads, smem, s>>>(tdy, tx, eta, M, N, K, planes, dw, vec);
   return launch_status();
 }
 
@@ -89,7 +177,11 @@ extern "C" {
 
 size_t bitlinear_grad_input_workspace_bytes(int64_t M, int64_t N, int64_t K, bl_dtype dydt) {
   if (train_sizes(M, N, K) != BL_OK || !dtype_ok(dydt)) return 0;
-  return 0;
+  Scratch ws(nullptr);
+  Rows r;
+  dy_rows(nullptr, dydt, M, N, &ws, &r, 1, nullptr);
+  pad_rows(nullptr, N, (K + 3) / 4, &ws, &r, 1, nullptr);
+  return ws.used;
 }
 
 bl_status bitlinear_grad_input(const void* dy, bl_dtype dydt, int64_t M, int64_t N, const uint8_t* packed,
@@ -107,13 +199,21 @@ bl_status bitlinear_grad_input(const void* dy, bl_dtype dydt, int64_t M, int64_t
   int sms = 148;
   if ((st = device_info(&sms)) != BL_OK) return st;
   const cudaStream_t s = as_stream(stream);
-  return dydt == BL_F32 ? launch_grad_input<float>(dy, M, N, packed, gamma, K, dx, dxdt, sms, s)
-                        : launch_grad_input<__nv_bfloat16>(dy, M, N, packed, gamma, K, dx, dxdt, sms, s);
+  Scratch ws(workspace);
+  Rows rdy;
+  if ((st = dy_rows(dy, dydt, M, N, &ws, &rdy, sms, s)) != BL_OK) return st;
+  bl::GiArgs a = {};
+  a.gamma = gamma; a.M = static_cast<int>(M); a.N = static_cast<int>(N); a.K = static_cast<int>(K); a.dx = dx;
+  return run_grad_input(rdy, packed, dxdt, a, &ws, sms, s);
 }
 
 size_t bitlinear_grad_weight_workspace_bytes(int64_t M, int64_t N, int64_t K, bl_dtype dydt, bl_dtype dwdt) {
   if (train_sizes(M, N, K) != BL_OK || !dtype_ok(dydt) || !dtype_ok(dwdt)) return 0;
-  return 0;
+  Scratch ws(nullptr);
+  Rows r;
+  dy_rows(nullptr, dydt, M, N, &ws, &r, 1, nullptr);
+  pad_rows(nullptr, M, K, &ws, &r, 1, nullptr);
+  return ws.used;
 }
 
 bl_status bitlinear_grad_weight(const void* dy, bl_dtype dydt, const int8_t* xq, const float* eta, int64_t M,
@@ -131,17 +231,28 @@ bl_status bitlinear_grad_weight(const void* dy, bl_dtype dydt, const int8_t* xq,
   int sms = 148;
   if ((st = device_info(&sms)) != BL_OK) return st;
   const cudaStream_t s = as_stream(stream);
-  const unsigned g = grid_for(N * K, 256, sms);
-  if (dydt == BL_F32) {
-    const auto* d = static_cast<const float*>(dy);
-    if (dwdt == BL_F32) bl::k_grad_weight<float, float><<<g, 256, 0, s>>>(d, xq, eta, M, N, K, dw);
-    else bl::k_grad_weight<float, __nv_bfloat16><<<g, 256, 0, s>>>(d, xq, eta, M, N, K, dw);
-  } else {
-    const auto* d = static_cast<const __nv_bfloat16*>(dy);
-    if (dwdt == BL_F32) bl::k_grad_weight<__nv_bfloat16, float><<<g, 256, 0, s>>>(d, xq, eta, M, N, K, dw);
-    else bl::k_grad_weight<__nv_bfloat16, __nv_bfloat16><<<g, 256, 0, s>>>(d, xq, eta, M, N, K, dw);
+  if (M == 0) {
+    if (cudaMemsetAsync(dw, 0, static_cast<size_t>(N * K * dtype_bytes(dwdt)), s) == cudaSuccess) return BL_OK;
+    (void)cudaGetLastError();
+    return BL_ERR_CUDA;
   }
-  return launch_status();
+  Scratch ws(workspace);
+  Rows rdy, rx;
+  if ((st = dy_rows(dy, dydt, M, N, &ws, &rdy, sms, s)) != BL_OK) return st;
+  if ((st = pad_rows(xq, M, K, &ws, &rx, sms, s)) != BL_OK) return st;
+  CUtensorMap tdy, tx;
+  if (!make_tmap(&tdy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rdy.p, N, M, rdy.planes, rdy.stride, 64, bl::kGwBM,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, rx.p, K, M, 0, rx.stride, 128, bl::kGwBM,
+                 CU_TENSOR_MAP_SWIZZLE_128B))
+    return BL_ERR_CUDA;
+  const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
+  const int vec = vec_rows(K, dwdt);
+  if (dwdt == BL_F32)
+    return N > 128 ? launch_gw<2, 2, float>(tdy, tx, eta, m, n, k, rdy.planes, dw, vec, s)
+                   : launch_gw<1, 2, float>(tdy, tx, eta, m, n, k, rdy.planes, dw, vec, s);
+  return N > 128 ? launch_gw<2, 1, __nv_bfloat16>(tdy, tx, eta, m, n, k, rdy.planes, dw, vec, s)
+                 : launch_gw<1, 1, __nv_bfloat16>(tdy, tx, eta, m, n, k, rdy.planes, dw, vec, s);
 }
 
 bl_status bitlinear_rmsnorm_grad(const void* dn, bl_dtype dndt, const int8_t* xq, const float* eta,
@@ -221,7 +332,9 @@ size_t bitlinear_adapters_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, 
   Scratch ws(nullptr);
   ws.take(static_cast<size_t>(M) * r * 4);  // u
   ws.take(static_cast<size_t>(M) * r * 4);  // v
-  ws.take(static_cast<size_t>(M) * K * 4);  // the projection's input gradient in fp32
+  Rows rows;
+  dy_rows(nullptr, dydt, M, N, &ws, &rows, 1, nullptr);
+  pad_rows(nullptr, N, (K + 3) / 4, &ws, &rows, 1, nullptr);
   return ws.used;
 }
 
@@ -249,20 +362,18 @@ bl_status bitlinear_adapters_grad(const void* dy, bl_dtype dydt, const int8_t* x
   Scratch ws(workspace);
   float* u = static_cast<float*>(ws.take(static_cast<size_t>(M) * r * 4));
   float* v = static_cast<float*>(ws.take(static_cast<size_t>(M) * r * 4));
-  float* base = static_cast<float*>(ws.take(static_cast<size_t>(M) * K * 4));
   const AdapterSet ad = {static_cast<const __nv_bfloat16*>(A), static_cast<const __nv_bfloat16*>(B), scale, ids,
                          static_cast<int>(L), static_cast<int>(r)};
   st = dydt == BL_F32
            ? launch_adapters_grad<float>(dy, xq, eta, M, K, N, ad, dA, dB, dabdt, u, v, sms, s)
            : launch_adapters_grad<__nv_bfloat16>(dy, xq, eta, M, K, N, ad, dA, dB, dabdt, u, v, sms, s);
   if (st != BL_OK || !dx || M == 0) return st;
-  st = dydt == BL_F32 ? launch_grad_input<float>(dy, M, N, packed, gamma, K, base, BL_F32, sms, s)
-                      : launch_grad_input<__nv_bfloat16>(dy, M, N, packed, gamma, K, base, BL_F32, sms, s);
-  if (st != BL_OK) return st;
-  const unsigned g = grid_for(M * K, 256, sms);
-  if (dxdt == BL_F32) bl::k_adapter_add<float><<<g, 256, 0, s>>>(base, M, K, v, ad.A, 1, K, ids, ad.L, ad.r, dx);
-  else bl::k_adapter_add<__nv_bfloat16><<<g, 256, 0, s>>>(base, M, K, v, ad.A, 1, K, ids, ad.L, ad.r, dx);
-  return launch_status();
+  Rows rdy;
+  if ((st = dy_rows(dy, dydt, M, N, &ws, &rdy, sms, s)) != BL_OK) return st;
+  bl::GiArgs g = {};
+  g.gamma = gamma; g.M = static_cast<int>(M); g.N = static_cast<int>(N); g.K = static_cast<int>(K); g.dx = dx;
+  g.v = v; g.A = ad.A; g.ids = ids; g.L = ad.L; g.r = ad.r;
+  return run_grad_input(rdy, packed, dxdt, g, &ws, sms, s);
 }
 
 }  // extern "C"

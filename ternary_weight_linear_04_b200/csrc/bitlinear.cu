@@ -28,6 +28,7 @@
 #include "rmsnorm_rows.cuh"
 #include "rmsnorm.cuh"
 #include "grad.cuh"
+#include "grad_weight.cuh"
 #include "rmsnorm_grad.cuh"
 #include "adapters.cuh"
 

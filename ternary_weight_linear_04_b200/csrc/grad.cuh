@@ -4,12 +4,13 @@
 // unchanged, so with W^ = gamma W~ and x^ = x~ eta / 127
 //
 //   dx[m,k] = gamma sum_n dy[m,n] W~[n,k]          (k_grad_input)
-//   dW[n,k] = sum_m dy[m,n] x~[m,k] eta_m / 127    (k_grad_weight)
+//   dW[n,k] = sum_m dy[m,n] x~[m,k] eta_m / 127    (grad_weight.cuh)
 //
-// Both are contractions of bf16 by bf16 values with fp32 accumulators
-// (tcgen05 kind::f16, accumulators in TMEM).  W~ has the values -1, 0, +1,
-// exact in bf16, so the products of dx are exact and only the sum rounds;
-// gamma is applied to the finished sum.
+// k_grad_input (here) contracts bf16 with bf16 values into fp32 accumulators
+// (tcgen05 kind::f16, accumulators in TMEM): W~ has the values -1, 0, +1,
+// exact in bf16, so the products are exact and only the sum rounds; gamma is
+// applied to the finished sum.  k_grad_weight (grad_weight.cuh) contracts
+// integers.
 #pragma once
 
 #include <cuda.h>
@@ -436,241 +437,6 @@ __global__ void __launch_bounds__(kGiThreads, 1)
           f[8 + j] = __fmul_rn(__uint_as_float(v[16 * g + 2 * j + 1]), gamma);
         }
         if (m < a.M) store16<OutT>(a.dx, m * a.K, k0 + c + 16 * g, a.K, f, a.vec);
-      }
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem_d, 256 * H);
-  }
-}
-
-// ---------------------------------------------------------------- weight gradient
-//
-// Tile: 128 H outputs n (TMEM lanes) by 256 inputs k (columns), the
-// contraction over the tokens in steps of 32.  Both operands lie with the
-// contraction outermost, as the tensors do (MN-major): the dy tile comes by
-// TMA, the token codes through a ring of their own and eight warps that
-// multiply them by eta / 127 and write bf16.  PL = 2 keeps 16 bits of each
-// value in two bf16 tiles (fp32 results: the rounding of one bf16 factor,
-// 2^-9 relative, would show in them); PL = 1 rounds it once (bf16 results,
-// whose own rounding is as large).
-
-constexpr int kGwBM = 32;    // tokens per step
-constexpr int kGwBN = 256;   // inputs k per tile
-constexpr int kGwWarps = 8;
-constexpr int kGwThreads = 32 * (2 + kGwWarps);
-
-template <int H, int PL>
-struct GwCfg {
-  static constexpr int kStages = PL == 2 ? 4 : 5;
-  static constexpr int kXStages = 4;
-  static constexpr int kABytes = H * 128 * kGwBM * 2;
-  static constexpr int kBBytes = PL * kGwBN * kGwBM * 2;
-  static constexpr int kXBytes = kGwBN * kGwBM;
-  static constexpr int kBars = 3 * kStages + 2 * kXStages + 2;
-  static constexpr int kTail = 8 * kBars + 16;
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * (kABytes + kBBytes) + kXStages * kXBytes + kTail;
-  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-};
-
-template <int H, int PL, typename OutT>
-__global__ void __launch_bounds__(kGwThreads, 1)
-    k_grad_weight(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_x,
-                  const float* __restrict__ eta, int M, int N, int K, int planes, void* __restrict__ dw, int vec) {
-  using Cfg = GwCfg<H, PL>;
-  constexpr int S = Cfg::kStages, SX = Cfg::kXStages;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* sA = base;
-  uint8_t* sB = sA + S * Cfg::kABytes;
-  uint8_t* sX = sB + S * Cfg::kBBytes;
-  uint64_t* full_a = reinterpret_cast<uint64_t*>(sX + SX * Cfg::kXBytes);
-  uint64_t* full_b = full_a + S;
-  uint64_t* empty = full_b + S;
-  uint64_t* full_x = empty + S;
-  uint64_t* empty_x = full_x + SX;
-  uint64_t* accum_full = empty_x + SX;
-  uint64_t* drain = accum_full + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ktiles = (K + kGwBN - 1) / kGwBN;
-  const int k0 = static_cast<int>(blockIdx.x % ktiles) * kGwBN, n0 = static_cast<int>(blockIdx.x / ktiles) * (128 * H);
-  const int steps_m = (M + kGwBM - 1) / kGwBM;
-  const int nst = steps_m * planes;
-
-  auto issue_x = [&](int i) {
-    const int s = i % SX, m = (i % steps_m) * kGwBM;
-    mbar_arrive_expect_tx(full_x + s, Cfg::kXBytes);
-    for (int j = 0; j < 2; ++j)
-      tma_load_2d(sX + s * Cfg::kXBytes + j * (128 * kGwBM), &tm_x, full_x + s, k0 + 128 * j, m);
-  };
-  auto issue_a = [&](int i) {
-    const int s = i % S, m = (i % steps_m) * kGwBM;
-    mbar_arrive_expect_tx(full_a + s, Cfg::kABytes);
-    for (int j = 0; j < 2 * H; ++j)
-      tma_load_3d(sA + s * Cfg::kABytes + j * (128 * kGwBM), &tm_dy, full_a + s, n0 + 64 * j, m, i / steps_m);
-  };
-  const int a_first = nst < S ? nst : S, x_first = nst < SX ? nst : SX;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(full_a + s, 1);
-      mbar_init(full_b + s, kGwWarps);
-      mbar_init(empty + s, 1);
-    }
-    for (int s = 0; s < SX; ++s) {
-      mbar_init(full_x + s, 1);
-      mbar_init(empty_x + s, kGwWarps);
-    }
-    mbar_init(accum_full, 1);
-    mbar_init(drain, 1);
-    *abort_flag = 0;
-    mbar_init_fence();
-    for (int i = 0; i < x_first; ++i) issue_x(i);
-    for (int i = 0; i < a_first; ++i) issue_a(i);
-  }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, 256 * H);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_d = *tmem_slot;
-  bool epi_ok = false;
-  int issued = 0;
-
-  if (warp == 0) {
-    if (lane == 0) {
-      issued = a_first;
-      for (int i = S; i < nst; ++i) {
-        if (!mbar_wait(empty + i % S, static_cast<uint32_t>(i / S - 1) & 1u, abort_flag)) break;
-        issue_a(i);
-        issued = i + 1;
-      }
-    } else if (lane == 1) {
-      issued = x_first;
-      for (int i = SX; i < nst; ++i) {
-        if (!mbar_wait(empty_x + i % SX, static_cast<uint32_t>(i / SX - 1) & 1u, abort_flag)) break;
-        issue_x(i);
-        issued = i + 1;
-      }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = make_idesc_bf16(128, kGwBN, true, true);
-      const uint64_t a_desc0 = make_sw128_mnmajor_desc(smem_u32(sA), kGwBM * 128);
-      const uint64_t b_desc0 = make_sw128_mnmajor_desc(smem_u32(sB), kGwBM * 128);
-      bool ok = true;
-      for (int i = 0; i < nst; ++i) {
-        const int s = i % S;
-        const uint32_t par = static_cast<uint32_t>(i / S) & 1u;
-        ok = mbar_wait(full_a + s, par, abort_flag) && mbar_wait(full_b + s, par, abort_flag);
-        if (!ok) {
-          if (i > 0) {
-            tc_commit(drain);
-            mbar_drain(drain, 0);
-          }
-          break;
-        }
-        tc_fence_after();
-        const uint64_t ad = a_desc0 + static_cast<uint64_t>(s * (Cfg::kABytes >> 4));
-        const uint64_t bd = b_desc0 + static_cast<uint64_t>(s * (Cfg::kBBytes >> 4));
-#pragma unroll
-        for (int kk = 0; kk < kGwBM / 16; ++kk)
-#pragma unroll
-          for (int p = 0; p < PL; ++p)
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-              tc_mma_bf16_ss(tmem_d + 256 * h, ad + h * ((2 * 128 * kGwBM) >> 4) + kk * (2048 >> 4),
-                             bd + p * ((kGwBN * kGwBM * 2) >> 4) + kk * (2048 >> 4), idesc,
-                             i != 0 || kk != 0 || p != 0 ? 1u : 0u);
-        tc_commit(empty + s);
-      }
-      if (ok) tc_commit(accum_full);
-    }
-  } else {
-    // ---------------- tokens to bf16: lane = token of the step, warp = 32 inputs
-    const int u = warp - 2;
-    const uint8_t* src0 = sX + (u >> 2) * (128 * kGwBM) + lane * 128;
-    uint8_t* const dst0 = sB + (u >> 1) * (128 * kGwBM) + (lane >> 3) * 1024 + (lane & 7) * 128;
-    bool ok = true;
-    for (int i = 0; i < nst; ++i) {
-      const int s = i % S, sx = i % SX;
-      const int m = (i % steps_m) * kGwBM + lane;
-      const float f = m < M ? div127_rn(__ldg(eta + m)) : 0.0f;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(full_x + sx, static_cast<uint32_t>(i / SX) & 1u, abort_flag));
-      if (!ok) break;
-      uint4 xv[2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        xv[c] = *reinterpret_cast<const uint4*>(src0 + sx * Cfg::kXBytes + ((((u & 3) * 2 + c) ^ (lane & 7)) << 4));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty_x + sx);
-      if (i >= S) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + s, static_cast<uint32_t>(i / S - 1) & 1u, abort_flag));
-        if (!ok) break;
-      }
-      uint8_t* dst = dst0 + s * Cfg::kBBytes;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {  // 8 values each
-        const uint4& x4 = xv[c >> 1];
-        const uint32_t w2[2] = {(c & 1) ? x4.z : x4.x, (c & 1) ? x4.w : x4.y};
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t ub = w2[j >> 1] ^ 0x80808080u;  // code + 128
-          // 2^23 + (code + 128) as bits, minus 2^23 + 128: the code, exact
-          const float v0 = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(ub, 0x4B000000u, (j & 1) ? 0x7442 : 0x7440)), 8388736.0f), f);
-          const float v1 = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(ub, 0x4B000000u, (j & 1) ? 0x7443 : 0x7441)), 8388736.0f), f);
-          hi[j] = pack_bf16(v0, v1);
-          if (PL == 2) lo[j] = pack_bf16_rest(v0, v1, hi[j]);
-        }
-        const uint32_t off = (((u & 1) * 4 + c) ^ (lane & 7)) << 4;
-        *reinterpret_cast<uint4*>(dst + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (PL == 2)
-          *reinterpret_cast<uint4*>(dst + kGwBN * kGwBM * 2 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full_b + s);
-    }
-    if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(accum_full, 0, abort_flag));
-    epi_ok = ok && __all_sync(0xFFFFFFFFu, *abort_flag == 0);
-  }
-
-  __syncwarp();
-  __syncthreads();
-  if (warp == 0 && lane < 2 && *abort_flag) {
-    uint64_t* bars = lane == 0 ? full_a : full_x;
-    const int ring = lane == 0 ? S : SX;
-    for (int i = issued > ring ? issued - ring : 0; i < issued; ++i)
-      mbar_drain(bars + i % ring, static_cast<uint32_t>(i / ring) & 1u);
-  }
-
-  // ---------------- epilogue: one TMEM lane = one output n
-  if (warp >= 2 && epi_ok) {
-    tc_fence_after();
-    const int qd = warp & 3, part = (warp - 2) >> 2;
-    const int h = H == 2 ? part : 0;
-    const int c_begin = H == 2 ? 0 : part * 128, c_end = H == 2 ? 256 : c_begin + 128;
-    const int64_t n = static_cast<int64_t>(n0) + 128 * h + 32 * qd + lane;
-    const uint32_t trow = tmem_d + 256 * h + (static_cast<uint32_t>(qd * 32) << 16);
-#pragma unroll 1
-    for (int c = c_begin; c < c_end; c += 32) {
-      uint32_t v[32];
-      tmem_ld_32x32b_x32(trow + c, v);
-      tmem_ld_wait();
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        float f[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[16 * g + j]);
-        if (n < N) store16<OutT>(dw, n * K, k0 + c + 16 * g, K, f, vec);
       }
     }
   }

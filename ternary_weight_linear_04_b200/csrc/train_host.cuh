@@ -132,17 +132,45 @@ bl_status run_grad_input(const Rows& dy, const uint8_t* packed, bl_dtype dxdt, b
   return dxdt == BL_F32 ? launch_gi<1, float>(tdy, tw, a, s) : launch_gi<1, __nv_bfloat16>(tdy, tw, a, s);
 }
 
-template <int H, int PL, typename OutT>
-bl_status launch_gw(const CUtensorMap& tdy, const CUtensorMap& tx, const float* eta, int M, int N, int K, int planes,
-                    void* dw, int vec, cudaStream_t s) {
+template <typename DyT, int ND>
+bl_status launch_gw_digits(const void* dy, const float* eta, int64_t M, int64_t N, int64_t Mp, uint8_t* digits,
+                           float* scale, cudaStream_t s) {
   static int done[kMaxDevices] = {0};
-  auto kern = bl::k_grad_weight<H, PL, OutT>;
-  constexpr size_t smem = bl::GwCfg<H, PL>::kSmem;
+  auto kern = bl::k_gw_digits<DyT, ND>;
+  constexpr size_t smem = ND * 32 * (bl::kGwChunk + 4);
   if (!ensure_smem(kern, smem, done)) return BL_ERR_CUDA;
-  const int64_t tiles = ((K + bl::kGwBN - 1) / bl::kGwBN) * ((int64_t{N} + 128 * H - 1) / (128 * H));
-  if (tiles > INT32_MAX) return BL_ERR_UNSUPPORTED;
-  kern<<<static_cast<unsigned>(tiles), bl::kGwThreads, smem, s>>>(tdy, tx, eta, M, N, K, planes, dw, vec);
+  const int64_t blocks = ((N + 31) / 32) * ((M + bl::kGwChunk - 1) / bl::kGwChunk);
+  if (blocks > INT32_MAX) return BL_ERR_UNSUPPORTED;
+  kern<<<static_cast<unsigned>(blocks), 256, smem, s>>>(static_cast<const DyT*>(dy), eta, M, N, Mp, digits, scale);
   return launch_status();
+}
+
+template <int ND, typename OutT>
+bl_status launch_gw(const CUtensorMap& td, const CUtensorMap& tx, const float* scale, int M, int N, int K, void* dw,
+                    int vec, int sms, cudaStream_t s) {
+  static int done[kMaxDevices] = {0};
+  auto kern = bl::k_grad_weight<ND, OutT>;
+  if (!ensure_smem(kern, bl::kGwSmem, done)) return BL_ERR_CUDA;
+  const int64_t tiles = ((int64_t{K} + bl::kGwBN - 1) / bl::kGwBN) * ((int64_t{N} + 127) / 128);
+  const int64_t grid = tiles < sms ? tiles : sms;
+  kern<<<static_cast<unsigned>(grid), bl::kGwThreads, bl::kGwSmem, s>>>(td, tx, scale, M, N, K, dw, vec);
+  return launch_status();
+}
+
+// Workspace of grad_weight: the digit planes, their exponents, the codes.
+struct GwScratch {
+  int64_t Mp;
+  uint8_t *digits, *codes;
+  float* scale;
+};
+
+inline GwScratch gw_scratch(int64_t M, int64_t N, int64_t K, int nd, Scratch* ws) {
+  GwScratch g;
+  g.Mp = round_up(M, 16);
+  g.digits = static_cast<uint8_t*>(ws->take(static_cast<size_t>(nd * N * g.Mp)));
+  g.codes = static_cast<uint8_t*>(ws->take(static_cast<size_t>(K * g.Mp)));
+  g.scale = static_cast<float*>(ws->take(static_cast<size_t>((M + bl::kGwChunk - 1) / bl::kGwChunk * N * 4)));
+  return g;
 }
 
 struct AdapterSet {
@@ -210,9 +238,7 @@ bl_status bitlinear_grad_input(const void* dy, bl_dtype dydt, int64_t M, int64_t
 size_t bitlinear_grad_weight_workspace_bytes(int64_t M, int64_t N, int64_t K, bl_dtype dydt, bl_dtype dwdt) {
   if (train_sizes(M, N, K) != BL_OK || !dtype_ok(dydt) || !dtype_ok(dwdt)) return 0;
   Scratch ws(nullptr);
-  Rows r;
-  dy_rows(nullptr, dydt, M, N, &ws, &r, 1, nullptr);
-  pad_rows(nullptr, M, K, &ws, &r, 1, nullptr);
+  gw_scratch(M, N, K, dwdt == BL_F32 ? 3 : 2, &ws);
   return ws.used;
 }
 
@@ -237,22 +263,29 @@ bl_status bitlinear_grad_weight(const void* dy, bl_dtype dydt, const int8_t* xq,
     return BL_ERR_CUDA;
   }
   Scratch ws(workspace);
-  Rows rdy, rx;
-  if ((st = dy_rows(dy, dydt, M, N, &ws, &rdy, sms, s)) != BL_OK) return st;
-  if ((st = pad_rows(xq, M, K, &ws, &rx, sms, s)) != BL_OK) return st;
-  CUtensorMap tdy, tx;
-  if (!make_tmap(&tdy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rdy.p, N, M, rdy.planes, rdy.stride, 64, bl::kGwBM,
+  const int nd = dwdt == BL_F32 ? 3 : 2;
+  const GwScratch g = gw_scratch(M, N, K, nd, &ws);
+  if (dydt == BL_F32)
+    st = nd == 3 ? launch_gw_digits<float, 3>(dy, eta, M, N, g.Mp, g.digits, g.scale, s)
+                 : launch_gw_digits<float, 2>(dy, eta, M, N, g.Mp, g.digits, g.scale, s);
+  else
+    st = nd == 3 ? launch_gw_digits<__nv_bfloat16, 3>(dy, eta, M, N, g.Mp, g.digits, g.scale, s)
+                 : launch_gw_digits<__nv_bfloat16, 2>(dy, eta, M, N, g.Mp, g.digits, g.scale, s);
+  if (st != BL_OK) return st;
+  const int64_t blocks = ((K + 63) / 64) * ((M + 127) / 128);
+  if (blocks > INT32_MAX) return BL_ERR_UNSUPPORTED;
+  bl::k_gw_codes<<<static_cast<unsigned>(blocks), 256, 0, s>>>(xq, M, K, g.Mp, g.codes);
+  if ((st = launch_status()) != BL_OK) return st;
+  CUtensorMap td, tx;
+  if (!make_tmap(&td, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.digits, g.Mp, N, nd, g.Mp, bl::kGwBM, 128,
                  CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, rx.p, K, M, 0, rx.stride, 128, bl::kGwBM,
+      !make_tmap(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.codes, g.Mp, K, 0, g.Mp, bl::kGwBM, bl::kGwBN,
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return BL_ERR_CUDA;
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
   const int vec = vec_rows(K, dwdt);
-  if (dwdt == BL_F32)
-    return N > 128 ? launch_gw<2, 2, float>(tdy, tx, eta, m, n, k, rdy.planes, dw, vec, s)
-                   : launch_gw<1, 2, float>(tdy, tx, eta, m, n, k, rdy.planes, dw, vec, s);
-  return N > 128 ? launch_gw<2, 1, __nv_bfloat16>(tdy, tx, eta, m, n, k, rdy.planes, dw, vec, s)
-                 : launch_gw<1, 1, __nv_bfloat16>(tdy, tx, eta, m, n, k, rdy.planes, dw, vec, s);
+  return nd == 3 ? launch_gw<3, float>(td, tx, g.scale, m, n, k, dw, vec, sms, s)
+                 : launch_gw<2, __nv_bfloat16>(td, tx, g.scale, m, n, k, dw, vec, sms, s);
 }
 
 bl_status bitlinear_rmsnorm_grad(const void* dn, bl_dtype dndt, const int8_t* xq, const float* eta,

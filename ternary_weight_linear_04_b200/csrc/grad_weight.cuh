@@ -27,6 +27,7 @@
 #include <cuda.h>
 
 #include "common.cuh"
+#include "decode.cuh"
 #include "grad.cuh"
 #include "tc_bf16.cuh"
 
@@ -36,77 +37,139 @@ constexpr int kGwChunk = 512;  // tokens that share a column's exponent
 
 // ---------------------------------------------------------------- operands
 
-// Digits of a 32-column, 512-token tile: lane = column, a warp takes 64
-// tokens in groups of 4, whose digits fill one word.  digits: ND planes of
-// N x Mp bytes (Mp a multiple of 16, zero past M); scale[chunk * N + n] =
-// 2^-e, or NaN where the column holds an infinity or a NaN (its whole
-// gradient row is then NaN, as it would be in floating point).
+// Digits of a 64-column, 512-token tile: lane = two neighbouring columns, a
+// warp takes 32 tokens, held as they were read (two bf16 in a register)
+// between the column's maximum and the digits.  digits: ND planes of N x Mp
+// bytes (Mp a multiple of 16, zero past M); scale[chunk * N + n] = 2^-e, or
+// NaN where the column holds an infinity or a NaN (its whole gradient row is
+// then NaN, as it would be in floating point).
+//
+// Rounding and splitting use no conversion instruction (a quarter of the
+// rate of an add): adding 1.5 2^23 rounds a value below 2^22 to an integer in
+// the low bits, and the bytes of q + 0x808080 with their top bits flipped
+// are the signed digits.  2048 x 11008, three digits: 101 us with
+// conversions, bound by their pipe.
+constexpr int kGdCols = 64;
+constexpr int kGdThreads = 512;
+
+// q + 0x808080 (ND = 3) or + 0x8080 (ND = 2), q = p rounded to an integer.
+template <int ND>
+__device__ __forceinline__ uint32_t biased_round(float p) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 2^23
+  constexpr uint32_t kBits = 0x4B400000u;
+  if constexpr (ND == 2) {
+    return __float_as_uint(__fadd_rn(p, kMagic)) + (0x8080u - kBits);
+  } else {  // |p| passes 2^22: a multiple of 4096 first, the rest is exact
+    const float h = __fmaf_rn(p, 0x1p-12f, kMagic);
+    const float l = __fadd_rn(__fmaf_rn(__fsub_rn(h, kMagic), -4096.0f, p), kMagic);
+    return __float_as_uint(h) * 4096u + (__float_as_uint(l) + (0x808080u - 4097u * kBits));
+  }
+}
+
 template <typename DyT, int ND>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
     k_gw_digits(const DyT* __restrict__ dy, const float* __restrict__ eta, int64_t M, int64_t N, int64_t Mp,
-                uint8_t* __restrict__ digits, float* __restrict__ scale) {
-  constexpr int kPitch = kGwChunk + 4;  // bytes: 129 words, so 32 columns lie in 32 banks
+                int pairs, uint8_t* __restrict__ digits, float* __restrict__ scale) {
   constexpr float kTop = ND == 3 ? 8355711.0f : 32639.0f;  // 127 (1 + 256 (+ 65536)): the largest q
   constexpr int kBits = ND == 3 ? 22 : 14;
-  extern __shared__ uint8_t smem[];  // ND x 32 x kPitch
-  __shared__ uint32_t s_max[8][32];
+  constexpr int kRegs = sizeof(DyT) == 2 ? 1 : 2;
+  extern __shared__ __align__(16) uint8_t smem[];  // ND x 64 columns x 512 bytes, words XORed with the lane
+  __shared__ uint32_t s_max[16][kGdCols];
+  __shared__ float s_f[kGwChunk];
+  uint32_t* words = reinterpret_cast<uint32_t*>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t ntiles = (N + 31) / 32;
+  const int64_t ntiles = (N + kGdCols - 1) / kGdCols;
   const int64_t chunk = blockIdx.x / ntiles;
-  const int64_t n0 = (blockIdx.x % ntiles) * 32, n = n0 + lane;
-  const int64_t mc = chunk * kGwChunk, mw = mc + warp * 64;
-  float g[64];
-  uint32_t mx = 0;
+  const int64_t n0 = (blockIdx.x % ntiles) * kGdCols, n = n0 + 2 * lane;
+  const int64_t mc = chunk * kGwChunk;
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
+  uint32_t raw[32][kRegs];
+  const int rows = static_cast<int>(min(static_cast<int64_t>(32), M - mc - 32 * warp));  // of this warp, may be < 1
+  const DyT* src = dy + (mc + 32 * warp) * N + n;
+  const bool in0 = n < N, in1 = n + 1 < N;
+  if (pairs) {
 #pragma unroll
-  for (int i = 0; i < 64; ++i) {
-    const int64_t m = mw + i;
-    g[i] = n < N && m < M ? ld_f32(dy + m * N + n) : 0.0f;
-  }
-#pragma unroll
-  for (int i = 0; i < 64; ++i) {
-    const int64_t m = mw + i;
-    if (m < M) g[i] = __fmul_rn(g[i], div127_rn(__ldg(eta + m)));
-    mx = max(mx, __float_as_uint(g[i]) & 0x7FFFFFFFu);  // orders magnitudes, infinities and NaN last
-  }
-  s_max[warp][lane] = mx;
-  __syncthreads();
-  for (int w = 0; w < 8; ++w) mx = max(mx, s_max[w][lane]);
-  // 2^e with the largest |g| 2^e in [2^kBits, 2^(kBits+1)), one less if that
-  // passes kTop; kept where 2^e and 2^-e are normal numbers
-  int e = kBits + 127 - static_cast<int>(mx >> 23);
-  e = min(max(e, -113), 120);
-  if (__fmul_rn(__uint_as_float(mx), __uint_as_float(static_cast<uint32_t>(e + 127) << 23)) > kTop) --e;
-  const bool finite = mx < 0x7F800000u;
-  const float up = finite ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 0.0f;
-  if (warp == 0 && n < N)
-    scale[chunk * N + n] = finite ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : __uint_as_float(0x7FC00000u);
-#pragma unroll
-  for (int i = 0; i < 64; i += 4) {
-    uint32_t w[ND];
-#pragma unroll
-    for (int j = 0; j < ND; ++j) w[j] = 0;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      int q = finite ? __float2int_rn(__fmul_rn(g[i + b], up)) : 0;
-#pragma unroll
-      for (int j = 0; j < ND; ++j) {  // low digit first; d in [-128, 127]
-        const int d = static_cast<int>(static_cast<int8_t>(q & 0xFF));
-        w[j] |= static_cast<uint32_t>(d & 0xFF) << (8 * b);
-        q = (q - d) >> 8;
+    for (int i = 0; i < 32; ++i, src += N) {
+      if constexpr (kRegs == 1) {
+        raw[i][0] = in0 && i < rows ? __ldg(reinterpret_cast<const unsigned*>(src)) : 0u;
+      } else {
+        const uint2 v = in0 && i < rows ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0, 0);
+        raw[i][0] = v.x;
+        raw[i][kRegs - 1] = v.y;
       }
     }
+  } else {
 #pragma unroll
-    for (int j = 0; j < ND; ++j)
-      *reinterpret_cast<uint32_t*>(smem + (j * 32 + lane) * kPitch + warp * 64 + i) = w[j];
+    for (int i = 0; i < 32; ++i, src += N) {
+      if constexpr (kRegs == 1) {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
+        raw[i][0] = (in0 && i < rows ? static_cast<uint32_t>(__ldg(h)) : 0u) |
+                    (in1 && i < rows ? static_cast<uint32_t>(__ldg(h + 1)) << 16 : 0u);
+      } else {
+        const uint32_t* h = reinterpret_cast<const uint32_t*>(src);
+        raw[i][0] = in0 && i < rows ? __ldg(h) : 0u;
+        raw[i][kRegs - 1] = in1 && i < rows ? __ldg(h + 1) : 0u;
+      }
+    }
+  }
+  {
+    const int64_t m = mc + threadIdx.x;
+    s_f[threadIdx.x] = m < M ? div127_rn(__ldg(eta + m)) : 0.0f;
+  }
+  __syncthreads();
+  auto g_of = [&](int i, int c) {  // dy f of the warp's token i, column c
+    const uint32_t u = kRegs == 2 ? raw[i][kRegs == 2 ? c : 0] : c ? raw[i][0] & 0xFFFF0000u : raw[i][0] << 16;
+    return __fmul_rn(__uint_as_float(u), s_f[32 * warp + i]);
+  };
+  uint32_t mx[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    mx[0] = max(mx[0], __float_as_uint(g_of(i, 0)) & 0x7FFFFFFFu);  // orders magnitudes, infinities and NaN last
+    mx[1] = max(mx[1], __float_as_uint(g_of(i, 1)) & 0x7FFFFFFFu);
+  }
+  *reinterpret_cast<uint2*>(&s_max[warp][2 * lane]) = make_uint2(mx[0], mx[1]);
+  __syncthreads();
+  float up[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+#pragma unroll
+    for (int w = 0; w < 16; ++w) mx[c] = max(mx[c], s_max[w][2 * lane + c]);
+    // 2^e with the largest |g| 2^e in [2^kBits, 2^(kBits+1)), one less if that
+    // passes kTop; kept where 2^e and 2^-e are normal numbers
+    int e = kBits + 127 - static_cast<int>(mx[c] >> 23);
+    e = min(max(e, -113), 120);
+    if (__fmul_rn(__uint_as_float(mx[c]), __uint_as_float(static_cast<uint32_t>(e + 127) << 23)) > kTop) --e;
+    const bool finite = mx[c] < 0x7F800000u;
+    up[c] = finite ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 0.0f;
+    if (warp == 0 && n + c < N)
+      scale[chunk * N + n + c] = finite ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : __uint_as_float(0x7FC00000u);
+  }
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) asm volatile("" : "+r"(raw[i + b][0]));  // keep dy, not the products
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t u[4], o[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) u[b] = up[c] != 0.0f ? biased_round<ND>(__fmul_rn(g_of(i + b, c), up[c])) : 0x808080u;
+      transpose4x4_bytes(u[0], u[1], u[2], u[3], o[0], o[1], o[2], o[3]);
+#pragma unroll
+      for (int j = 0; j < ND; ++j)
+        words[(j * kGdCols + 2 * lane + c) * 128 + ((8 * warp + i / 4) ^ lane)] = o[j] ^ 0x80808080u;
+    }
   }
   __syncthreads();
   // out: a warp writes one column's 512 bytes at a time
-  for (int c = warp; c < 32 * ND; c += 8) {
-    const int j = c >> 5, col = c & 31;
+  for (int r = warp; r < kGdCols * ND; r += 16) {
+    const int j = r / kGdCols, col = r % kGdCols, x = col >> 1;  // x: the lane that wrote the column
     const int64_t m = mc + lane * 16;
     if (n0 + col < N && m < Mp) {
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(smem + (j * 32 + col) * kPitch) + lane * 4;
-      *reinterpret_cast<uint4*>(digits + (j * N + n0 + col) * Mp + m) = make_uint4(src[0], src[1], src[2], src[3]);
+      uint4 v = *reinterpret_cast<const uint4*>(words + r * 128 + ((4 * lane) ^ (x & ~3)));
+      if (x & 1) v = make_uint4(v.y, v.x, v.w, v.z);
+      if (x & 2) v = make_uint4(v.z, v.w, v.x, v.y);
+      *reinterpret_cast<uint4*>(digits + (j * N + n0 + col) * Mp + m) = v;
     }
   }
 }
@@ -121,6 +184,8 @@ __global__ void __launch_bounds__(256)
   const int64_t k0 = (blockIdx.x % ktiles) * 64, m0 = (blockIdx.x / ktiles) * 128;
   const int kq = threadIdx.x & 15, mq = threadIdx.x >> 4;
   const bool words = (K & 3) == 0;
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
 #pragma unroll
   for (int it = 0; it < 2; ++it) {
     const int64_t k = k0 + 4 * kq, m = m0 + 4 * (mq + 16 * it);
@@ -190,6 +255,26 @@ struct Ring {
   }
 };
 
+// acc += v sc for 16 sums of a pass.  Sums below 2^22 (all but freak ones;
+// the bound is 2^23) become fp32 by adding the bits of 1.5 2^23 and taking it
+// off again, two adds instead of a conversion at a quarter of their rate.
+__device__ __forceinline__ void add_pass(const uint32_t (&v)[16], float sc, float* acc) {
+  int hi = static_cast<int>(v[0]), lo = hi;
+#pragma unroll
+  for (int x = 1; x < 16; ++x) {
+    hi = max(hi, static_cast<int>(v[x]));
+    lo = min(lo, static_cast<int>(v[x]));
+  }
+  if (__any_sync(0xFFFFFFFFu, hi >= (1 << 22) || lo < -(1 << 22))) {
+#pragma unroll
+    for (int x = 0; x < 16; ++x) acc[x] = __fmaf_rn(__int2float_rn(static_cast<int>(v[x])), sc, acc[x]);
+  } else {
+#pragma unroll
+    for (int x = 0; x < 16; ++x)
+      acc[x] = __fmaf_rn(__fsub_rn(__uint_as_float(v[x] + 0x4B400000u), 12582912.0f), sc, acc[x]);
+  }
+}
+
 template <int ND, typename OutT>
 __global__ void __launch_bounds__(kGwThreads, 1)
     k_grad_weight(const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_x,
@@ -236,6 +321,8 @@ __global__ void __launch_bounds__(kGwThreads, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -330,9 +417,7 @@ __global__ void __launch_bounds__(kGwThreads, 1)
             uint32_t v[16];
             tmem_ld_32x32b_x16(trow + 256 * pass.s + i, v);
             tmem_ld_wait();
-#pragma unroll
-            for (int x = 0; x < 16; ++x)
-              acc[i + x] = __fmaf_rn(__int2float_rn(static_cast<int32_t>(v[x])), sc, acc[i + x]);
+            add_pass(v, sc, acc + i);
           }
           tc_fence_before();
           __syncwarp();

@@ -137,12 +137,12 @@ bl_status launch_gw_digits(const void* dy, const float* eta, int64_t M, int64_t 
                            float* scale, cudaStream_t s) {
   static int done[kMaxDevices] = {0};
   auto kern = bl::k_gw_digits<DyT, ND>;
-  constexpr size_t smem = ND * 32 * (bl::kGwChunk + 4);
+  constexpr size_t smem = ND * bl::kGdCols * bl::kGwChunk;
   if (!ensure_smem(kern, smem, done)) return BL_ERR_CUDA;
-  const int64_t blocks = ((N + 31) / 32) * ((M + bl::kGwChunk - 1) / bl::kGwChunk);
+  const int64_t blocks = ((N + bl::kGdCols - 1) / bl::kGdCols) * ((M + bl::kGwChunk - 1) / bl::kGwChunk);
   if (blocks > INT32_MAX) return BL_ERR_UNSUPPORTED;
-  kern<<<static_cast<unsigned>(blocks), 256, smem, s>>>(static_cast<const DyT*>(dy), eta, M, N, Mp, digits, scale);
-  return launch_status();
+  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(bl::kGdThreads), smem, s,
+                    static_cast<const DyT*>(dy), eta, M, N, Mp, N % 2 == 0 ? 1 : 0, digits, scale);
 }
 
 template <int ND, typename OutT>
@@ -153,8 +153,8 @@ bl_status launch_gw(const CUtensorMap& td, const CUtensorMap& tx, const float* s
   if (!ensure_smem(kern, bl::kGwSmem, done)) return BL_ERR_CUDA;
   const int64_t tiles = ((int64_t{K} + bl::kGwBN - 1) / bl::kGwBN) * ((int64_t{N} + 127) / 128);
   const int64_t grid = tiles < sms ? tiles : sms;
-  kern<<<static_cast<unsigned>(grid), bl::kGwThreads, bl::kGwSmem, s>>>(td, tx, scale, M, N, K, dw, vec);
-  return launch_status();
+  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(bl::kGwThreads), bl::kGwSmem, s, td, tx, scale, M, N,
+                    K, dw, vec);
 }
 
 // Workspace of grad_weight: the digit planes, their exponents, the codes.
@@ -171,6 +171,18 @@ inline GwScratch gw_scratch(int64_t M, int64_t N, int64_t K, int nd, Scratch* ws
   g.codes = static_cast<uint8_t*>(ws->take(static_cast<size_t>(K * g.Mp)));
   g.scale = static_cast<float*>(ws->take(static_cast<size_t>((M + bl::kGwChunk - 1) / bl::kGwChunk * N * 4)));
   return g;
+}
+
+// One CTA per row, of as many warps as hold the row at kRgHeld chunks a thread.
+template <typename DnT, typename OutT>
+bl_status launch_rg(const void* dn, const int8_t* xq, const float* eta, const float* rstd, int64_t M, int64_t K,
+                    void* dx, bool vec, int sms, cudaStream_t s) {
+  const int64_t per_warp = 32 * 8 * bl::kRgHeld, warps = (K + per_warp - 1) / per_warp;
+  const bool held = warps <= bl::kRgMaxThreads / 32;
+  const auto* d = static_cast<const DnT*>(dn);
+  const dim3 grid(grid_for(M, 1, sms)), block(static_cast<unsigned>(held ? 32 * warps : bl::kRgMaxThreads));
+  if (held) return launch_pdl(bl::k_rmsnorm_grad<DnT, OutT, true>, grid, block, 0, s, d, xq, eta, rstd, M, K, dx, vec ? 1 : 0);
+  return launch_pdl(bl::k_rmsnorm_grad<DnT, OutT, false>, grid, block, 0, s, d, xq, eta, rstd, M, K, dx, vec ? 1 : 0);
 }
 
 struct AdapterSet {
@@ -274,8 +286,9 @@ bl_status bitlinear_grad_weight(const void* dy, bl_dtype dydt, const int8_t* xq,
   if (st != BL_OK) return st;
   const int64_t blocks = ((K + 63) / 64) * ((M + 127) / 128);
   if (blocks > INT32_MAX) return BL_ERR_UNSUPPORTED;
-  bl::k_gw_codes<<<static_cast<unsigned>(blocks), 256, 0, s>>>(xq, M, K, g.Mp, g.codes);
-  if ((st = launch_status()) != BL_OK) return st;
+  if ((st = launch_pdl(bl::k_gw_codes, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, xq, M, K, g.Mp, g.codes)) !=
+      BL_OK)
+    return st;
   CUtensorMap td, tx;
   if (!make_tmap(&td, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.digits, g.Mp, N, nd, g.Mp, bl::kGwBM, 128,
                  CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -300,17 +313,12 @@ bl_status bitlinear_rmsnorm_grad(const void* dn, bl_dtype dndt, const int8_t* xq
   const bl_status st = device_info(&sms);
   if (st != BL_OK) return st;
   const cudaStream_t s = as_stream(stream);
-  const unsigned g = grid_for(M, 1, sms);
-  if (dndt == BL_F32) {
-    const auto* d = static_cast<const float*>(dn);
-    if (dxdt == BL_F32) bl::k_rmsnorm_grad<float, float><<<g, 256, 0, s>>>(d, xq, eta, rstd, M, K, dx);
-    else bl::k_rmsnorm_grad<float, __nv_bfloat16><<<g, 256, 0, s>>>(d, xq, eta, rstd, M, K, dx);
-  } else {
-    const auto* d = static_cast<const __nv_bfloat16*>(dn);
-    if (dxdt == BL_F32) bl::k_rmsnorm_grad<__nv_bfloat16, float><<<g, 256, 0, s>>>(d, xq, eta, rstd, M, K, dx);
-    else bl::k_rmsnorm_grad<__nv_bfloat16, __nv_bfloat16><<<g, 256, 0, s>>>(d, xq, eta, rstd, M, K, dx);
-  }
-  return launch_status();
+  const bool vec = K % 8 == 0 && aligned(dn, 16) && aligned(xq, 8) && aligned(dx, 16);
+  if (dndt == BL_F32)
+    return dxdt == BL_F32 ? launch_rg<float, float>(dn, xq, eta, rstd, M, K, dx, vec, sms, s)
+                          : launch_rg<float, __nv_bfloat16>(dn, xq, eta, rstd, M, K, dx, vec, sms, s);
+  return dxdt == BL_F32 ? launch_rg<__nv_bfloat16, float>(dn, xq, eta, rstd, M, K, dx, vec, sms, s)
+                        : launch_rg<__nv_bfloat16, __nv_bfloat16>(dn, xq, eta, rstd, M, K, dx, vec, sms, s);
 }
 
 size_t bitlinear_forward_adapters_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r) {

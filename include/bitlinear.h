@@ -259,6 +259,8 @@ bl_status bitlinear_forward(const int8_t* xq, const float* eta, const int32_t* x
  * are always read only after it has finished.
  */
 #define BL_FLAG_WEIGHTS_STATIC 1u
+/* bitlinear_linear_adapters only: RMS-normalise the tokens first. */
+#define BL_FLAG_RMSNORM 2u
 
 /*
  * bitlinear_forward with the accumulate kernel and flags chosen by the
@@ -615,8 +617,12 @@ bl_status bitlinear_rmsnorm_grad(const void* dn, bl_dtype dndt, const int8_t* xq
  * uses adapter a = ids[m],
  *   y = x^ W^T + scale_a (x^ A_a^T) B_a^T
  * (the projection alone where ids[m] is outside [0, L), -1 by convention).
- * The adapters read the same 8-bit tokens as the projection.  No counterpart
- * on the pages.
+ * The adapters read the same 8-bit tokens as the projection; x^ A^T is
+ * summed in fp32, and enters the second product as it is (up to 16 tokens),
+ * as three bf16 parts that hold all of it (fp32 y), or as two that hold 16
+ * bits of it (bf16 y).  A token's output depends on no other token's adapter,
+ * whatever that one holds (infinities and NaN too).  No counterpart on the
+ * pages.
  *   xq, eta, xsum, packed, gamma, flags   in   as for bitlinear_forward_path.
  *   A       in   bf16, L x r x K.
  *   B       in   bf16, L x N x r.
@@ -633,6 +639,22 @@ bl_status bitlinear_forward_adapters(const int8_t* xq, const float* eta, const i
                                      const void* A, const void* B, const float* scale, const int32_t* ids,
                                      int64_t L, int64_t r, void* y, bl_dtype ydt, void* workspace,
                                      size_t workspace_bytes, unsigned flags, void* stream);
+
+/*
+ * bitlinear_forward_adapters on tokens that the call quantises itself.
+ *   x       in   M x K, fp32 or bf16 (bf16 with BL_FLAG_RMSNORM, which
+ *                normalises the tokens first as bitlinear_rmsnorm_quant_act
+ *                does; BL_ERR_UNSUPPORTED for fp32), any alignment to its
+ *                element size.
+ * Up to 16 bf16 tokens with K a multiple of 8 (at most 16384) take two
+ * launches: the quantiser runs inside the one that computes x^ A^T.
+ */
+size_t bitlinear_linear_adapters_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r);
+bl_status bitlinear_linear_adapters(const void* x, bl_dtype xdt, int64_t M, int64_t K, const uint8_t* packed,
+                                    const float* gamma, int64_t N, const void* A, const void* B,
+                                    const float* scale, const int32_t* ids, int64_t L, int64_t r, void* y,
+                                    bl_dtype ydt, void* workspace, size_t workspace_bytes, unsigned flags,
+                                    void* stream);
 
 /*
  * Backward pass of bitlinear_forward_adapters from the 8-bit tokens (the

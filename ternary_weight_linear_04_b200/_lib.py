@@ -14,6 +14,7 @@ BL_OK, BL_ERR_INVALID_ARG, BL_ERR_UNSUPPORTED, BL_ERR_ALIGNMENT, BL_ERR_CUDA, BL
 BL_F32, BL_BF16 = 0, 1
 BL_PATH_AUTO, BL_PATH_GEMV, BL_PATH_TCGEN05, BL_PATH_GENERIC = range(4)
 BL_FLAG_WEIGHTS_STATIC = 1
+BL_FLAG_RMSNORM = 2
 
 # name -> (restype, argtypes); every symbol include/bitlinear.h declares.
 _P = ctypes.c_void_p
@@ -61,6 +62,9 @@ SIGNATURES = {
     "bitlinear_forward_adapters_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
     "bitlinear_forward_adapters": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P, _I64, _I64,
                                         _P, _I, _P, _SZ, ctypes.c_uint, _P]),
+    "bitlinear_linear_adapters_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "bitlinear_linear_adapters": (_I, [_P, _I, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _I, _P,
+                                       _SZ, ctypes.c_uint, _P]),
     "bitlinear_adapters_grad_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I]),
     "bitlinear_adapters_grad": (_I, [_P, _I, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64,
                                      _P, _I, _P, _P, _I, _P, _SZ, _P]),

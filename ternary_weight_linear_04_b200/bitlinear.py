@@ -20,12 +20,12 @@ _DTYPES = {torch.float32: _lib.BL_F32, torch.bfloat16: _lib.BL_BF16}
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    # the raw handle: building a Stream object costs as much as a launch
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
 
 
 def _require_cuda(*ts):
@@ -361,11 +361,17 @@ def _place(stream, *ts):
     given, the current ones, so that scratch and outputs belong to the stream
     that the kernels run on.  All tensors have to be on one CUDA device (and
     the stream on it) and contiguous."""
-    _require_cuda(*ts)
-    index = ts[0].get_device()
+    index = -1
     for t in ts:
-        if t is not None and t.get_device() != index:
-            raise ValueError("tensors must be on one device")
+        if t is None:
+            continue
+        if not (t.is_cuda and t.is_contiguous()):
+            raise ValueError("tensors must be contiguous CUDA tensors")
+        at = t.get_device()
+        if at != index:
+            if index >= 0:
+                raise ValueError("tensors must be on one device")
+            index = at
     if stream is not None:
         if stream.device.index != index:
             raise ValueError("stream must be on the tensors' device")
@@ -380,7 +386,7 @@ def _al16(t):
 
 
 def _check(name, t, shape, *dtypes):
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
+    if t.shape != shape or t.dtype not in dtypes:
         raise ValueError("%s must be %s of shape %s, not %s of %s" % (
             name, " or ".join(str(d).replace("torch.", "") for d in dtypes), tuple(shape),
             str(t.dtype).replace("torch.", ""), tuple(t.shape)))
@@ -513,10 +519,22 @@ def linear_adapters(x, packed, gamma, N, A, B, scale, ids, out_dtype=torch.bfloa
                     weights_static=False, stream=None, out=None):
     """forward_adapters on tokens it quantises itself: x (M x K, fp32 or bf16),
     RMS-normalised first with rmsnorm (bf16)."""
-    with _place(stream, x):
-        xq, eta, xsum = (rmsnorm_quant_act if rmsnorm else quant_act)(x)
-        return forward_adapters(xq, eta, xsum, packed, gamma, N, A, B, scale, ids, out_dtype=out_dtype,
-                                weights_static=weights_static, out=out)
+    if x.dim() != 2 or x.dtype not in _DTYPES:
+        raise ValueError("x must be a 2-D float32 or bfloat16 tensor")
+    M, K = x.shape
+    _packed(packed, gamma, N, K)
+    n_ad, r = _adapters(A, B, scale, ids, M, N, K)
+    with _place(stream, x, packed, gamma, A, B, scale, ids):
+        y = _out(out, (M, N), out_dtype, x.device)
+        L = _lib.lib()
+        nws = L.bitlinear_linear_adapters_workspace_bytes(M, K, N, n_ad, r)
+        ws = _scratch(nws, x.device)
+        packed, A, B = _al16(packed), _al16(A), _al16(B)
+        flags = (_lib.BL_FLAG_WEIGHTS_STATIC if weights_static else 0) | (_lib.BL_FLAG_RMSNORM if rmsnorm else 0)
+        check(L.bitlinear_linear_adapters(
+            _ptr(x), _DTYPES[x.dtype], M, K, _ptr(packed), _ptr(gamma), N, _ptr(A), _ptr(B), _ptr(scale), _ptr(ids),
+            n_ad, r, _ptr(y), _DTYPES[y.dtype], _ptr(ws), nws, flags, _stream(None)), "bitlinear_linear_adapters")
+    return y
 
 
 def adapters_grad(dy, xq, eta, packed, gamma, A, B, scale, ids, out_dtype=torch.bfloat16,

@@ -1,0 +1,109 @@
+// adapter_add.cuh -- what the accumulate kernels need to add a low-rank
+// adapter to their outputs (adapters.cuh holds the rest).
+//
+// Token m uses adapter a = ids[m] (none when outside [0, L)); with u[m,:]
+// given, output n gains sum_j u[m,j] B_a[n,j], added to the rescaled integer
+// sum in fp32, so that the output is rounded once.
+#pragma once
+
+#include "common.cuh"
+
+namespace bl {
+
+struct AdapterAdd {
+  const float* u;  // M x r; NULL: no adapters
+  const __nv_bfloat16* B;  // L x N x r
+  const int32_t* ids;
+  int L, r;
+};
+
+// The adapter of token m: ids[m], or -1 (none) when outside [0, L).
+__device__ __forceinline__ int adapter_of(const int32_t* ids, int64_t m, int L) {
+  const int a = ids[m];
+  return static_cast<unsigned>(a) < static_cast<unsigned>(L) ? a : -1;
+}
+
+// base + sum_j u[m,j] B_a[n,j] for one output of the decode kernels, which
+// call it where they store (out of line: it costs them no registers).
+__device__ __noinline__ float adapter_add(const float* u, const __nv_bfloat16* B, const int32_t* ids, int L, int r, int m,
+                                          int n, int N, float base) {
+  const int a = adapter_of(ids, m, L);
+  if (a < 0) return base;
+  const __nv_bfloat16* b = B + (static_cast<int64_t>(a) * N + n) * r;
+  u += static_cast<int64_t>(m) * r;
+  float s = 0.0f;
+  int j = 0;
+  if ((r & 7) == 0) {
+    for (; j < r; j += 8) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(b + j));
+      const float4 p = *reinterpret_cast<const float4*>(u + j), q = *reinterpret_cast<const float4*>(u + j + 4);
+      s = __fmaf_rn(p.x, __uint_as_float(v.x << 16), s);
+      s = __fmaf_rn(p.y, __uint_as_float(v.x & 0xFFFF0000u), s);
+      s = __fmaf_rn(p.z, __uint_as_float(v.y << 16), s);
+      s = __fmaf_rn(p.w, __uint_as_float(v.y & 0xFFFF0000u), s);
+      s = __fmaf_rn(q.x, __uint_as_float(v.z << 16), s);
+      s = __fmaf_rn(q.y, __uint_as_float(v.z & 0xFFFF0000u), s);
+      s = __fmaf_rn(q.z, __uint_as_float(v.w << 16), s);
+      s = __fmaf_rn(q.w, __uint_as_float(v.w & 0xFFFF0000u), s);
+    }
+  }
+  for (; j < r; ++j) s = __fmaf_rn(u[j], __bfloat162float(b[j]), s);
+  return __fadd_rn(base, s);
+}
+
+// The distinct adapters of a tile's tokens in order of first use: s_ids[t]
+// for t < BM and s_list; returns their number.  Every thread of the block
+// calls it; BM <= 256 and BM <= threads.
+__device__ __forceinline__ int tile_adapters(const int32_t* ids, int64_t m0, int64_t M, int BM, int L, int* s_ids,
+                                             int* s_list, int* s_cnt) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, groups = (BM + 31) >> 5;
+  const int id = t < BM && m0 + t < M ? adapter_of(ids, m0 + t, L) : -1;
+  if (t < BM) s_ids[t] = id;
+  __syncthreads();
+  const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
+  bool first = id >= 0 && lane == __ffs(same) - 1;
+  if (first)
+    for (int j = 0; j < 32 * warp; ++j)
+      if (s_ids[j] == id) {
+        first = false;
+        break;
+      }
+  const unsigned firsts = __ballot_sync(0xFFFFFFFFu, first);
+  if (lane == 0 && warp < groups) s_cnt[warp] = __popc(firsts);
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int w = 0; w < groups; ++w) {
+    if (w < warp) before += s_cnt[w];
+    total += s_cnt[w];
+  }
+  if (first) s_list[before + __popc(firsts & ((1u << lane) - 1))] = id;
+  __syncthreads();
+  return total;
+}
+
+// Part p of the bf16 values x0 + x1 + x2 that hold an fp32 (8 bits each, the
+// differences exact).
+template <int P>
+__device__ __forceinline__ float bf16_part(float x, int p) {
+#pragma unroll
+  for (int i = 1; i < P; ++i)
+    if (p >= i) {
+      const float h = __bfloat162float(__float2bfloat16_rn(x));
+      x = __fsub_rn(h, h) == 0.0f ? __fsub_rn(x, h) : 0.0f;  // an infinity has no rest
+    }
+  return x;  // to be rounded to bf16
+}
+
+// Whether a pair of bf16 holds an infinity or a NaN.  The tensor-core kernels
+// multiply a factor of one adapter by the zeros that stand for the tokens of
+// the others; zero times infinity is not zero, so such factors are replaced
+// by zeros there and the outputs taken from plain sums over each token's own
+// adapter instead (slow, and only then).
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
+  return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+__device__ __forceinline__ bool nonfinite8(const uint4& v) {
+  return (nonfinite2(v.x) | nonfinite2(v.y) | nonfinite2(v.z) | nonfinite2(v.w)) != 0;
+}
+
+}  // namespace bl

@@ -8,104 +8,710 @@
 //   dA_a     = sum_{m of a} v[m,:]^T (eta_m / 127) x~[m,:]
 //   dB_a     = sum_{m of a} dy[m,:]^T u[m,:]
 //
-// A is L x r x K, B is L x N x r (bf16); sums in fp32.
+// A is L x r x K, B is L x N x r (bf16); sums in fp32.  Here: u and v, and
+// the two gradients.  y's sum over j sits in the accumulate kernels
+// (adapter_add.cuh, gemm_tc.cuh), dx's in grad.cuh.
 #pragma once
 
+#include <type_traits>
+
+#include "adapter_add.cuh"
 #include "common.cuh"
 #include "grad.cuh"
+#include "quant.cuh"
+#include "rmsnorm_grad.cuh"
 
 namespace bl {
 
-__device__ __forceinline__ float warp_sum(float s) {
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  return s;
+// ---------------------------------------------------------------- small pieces
+
+__device__ __forceinline__ void mma_bf16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One warp per (token, rank index).
-__global__ void __launch_bounds__(256)
-    k_adapter_u(const int8_t* __restrict__ xq, const float* __restrict__ eta, int64_t M, int64_t K,
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&d)[4], const void* row) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+               : "r"(smem_u32(row))
+               : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+// The codes in bytes 0 and 2 of w as a bf16 pair: the low seven bits on 128
+// (one step of bf16 there is one), minus 128 or, for a negative code, 256.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
+  const uint32_t low = (w & 0x007F007Fu) | 0x43004300u, off = (w & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 d = __hsub2(reinterpret_cast<const __nv_bfloat162&>(low), reinterpret_cast<const __nv_bfloat162&>(off));
+  return reinterpret_cast<const uint32_t&>(d);
+}
+
+// Four values of a row as two bf16 pairs (0, 1) and (2, 3): part p of fp32.
+template <typename T>
+__device__ __forceinline__ uint2 load4_bf16(const T* p, int64_t left, bool vec, int part) {
+  if constexpr (sizeof(T) == 2) {
+    if (vec) return left > 0 ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < left ? __ldg(h + i) : 0u;
+    return make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+  } else {
+    float f[4];
+    if (vec) {
+      const float4 v = left > 0 ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(0, 0, 0, 0);
+      f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = i < left ? __ldg(p + i) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = bf16_part<3>(f[i], part);
+    return make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+  }
+}
+
+// ---------------------------------------------------------------- u of up to 16 tokens
+//
+// Few tokens: every (token, rank index) is a dot product over K that reads
+// its own row of A, so the time is that of reading the adapters in use (and
+// a launch).  One CTA per token and group of rank indices; a thread holds its
+// chunks of the token's codes.  FUSE: the CTA quantises the token itself
+// (the exact rule of the quantiser kernels) and the first group's CTA
+// writes x~, eta and xsum, which saves the quantiser's launch.
+
+constexpr int kAuThreads = 256;
+constexpr int kAuChunks = 8;  // chunks of 8 codes a thread: K <= 16384
+
+template <bool FUSE>
+__global__ void __launch_bounds__(kAuThreads)
+    k_adapter_u(const __nv_bfloat16* __restrict__ x, int8_t* xq, float* eta, int32_t* xsum, int K,
                 const __nv_bfloat16* __restrict__ A, const float* __restrict__ scale,
-                const int32_t* __restrict__ ids, int L, int r, float* __restrict__ u) {
-  const int lane = threadIdx.x & 31;
-  for (int64_t i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < M * r; i += gridDim.x * 8ll) {
-    const int64_t m = i / r, j = i % r;
-    const int a = adapter_of(ids, m, L);
-    float s = 0.0f;
-    if (a >= 0) {
-      const __nv_bfloat16* row = A + (static_cast<int64_t>(a) * r + j) * K;
-      for (int64_t k = lane; k < K; k += 32)
-        s = __fmaf_rn(static_cast<float>(xq[m * K + k]), __bfloat162float(row[k]), s);
-      s = __fmul_rn(__fmul_rn(warp_sum(s), div127_rn(eta[m])), scale[a]);
+                const int32_t* __restrict__ ids, int L, int r, int group, float* __restrict__ u) {
+  __shared__ float s_red[2][kAuThreads / 32];
+  __shared__ int32_t s_sum[kAuThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t m = blockIdx.y;
+  const int nch = K >> 3;
+  pdl_wait();
+  if (tid == 0) pdl_trigger();
+  const int a = adapter_of(ids, m, L);
+  const bool writes = FUSE && xq != nullptr && blockIdx.x == 0;
+  if (a < 0) {
+    for (int j = blockIdx.x * group + tid; j < min(r, static_cast<int>(blockIdx.x + 1) * group); j += kAuThreads)
+      u[m * r + j] = 0.0f;
+    if (!writes) return;
+  }
+  uint2 q[kAuChunks];
+  float e;
+  if constexpr (FUSE) {
+    const uint4* row = reinterpret_cast<const uint4*>(x + m * K);
+    uint4 v[kAuChunks];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < kAuChunks; ++i) {
+      const int c = tid + kAuThreads * i;
+      v[i] = c < nch ? __ldg(row + c) : make_uint4(0, 0, 0, 0);
     }
-    if (lane == 0) u[i] = s;
+#pragma unroll
+    for (int i = 0; i < kAuChunks; ++i) {
+      const uint32_t w4[4] = {v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu, v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) amax = max(amax, max(w4[k] << 16, w4[k] & 0xFFFF0000u));
+    }
+    amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+    if (lane == 0) s_red[0][warp] = __uint_as_float(amax);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAuThreads / 32; ++w) amax = max(amax, __float_as_uint(s_red[0][w]));
+    e = fmaxf(__uint_as_float(amax), 1e-5f);
+    const float rr = rcp_approx(e), qs = __fmul_rn(127.0f, rr), heta = __fmul_rn(0.5f, e);
+    const bool eta_bf16 = is_bf16_value(e);  // else eta is the 1e-5 floor: exact quotients
+    int32_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < kAuChunks; ++i) {
+      const int c = tid + kAuThreads * i;
+      q[i] = make_uint2(0, 0);
+      if (c < nch) {
+        q[i] = eta_bf16 ? codes8_bf16<4>(v[i], e, heta, qs, rr) : codes8_exact(v[i], e);
+        if (writes) {
+          sum = __dp4a(static_cast<int>(q[i].x), 0x01010101, sum);
+          sum = __dp4a(static_cast<int>(q[i].y), 0x01010101, sum);
+          *reinterpret_cast<uint2*>(xq + m * K + 8 * c) = q[i];
+        }
+      }
+    }
+    if (writes) {
+      sum = __reduce_add_sync(0xFFFFFFFFu, sum);
+      if (lane == 0) s_sum[warp] = sum;
+      __syncthreads();
+      if (tid == 0) {
+        sum = 0;
+        for (int w = 0; w < kAuThreads / 32; ++w) sum += s_sum[w];
+        eta[m] = e;
+        xsum[m] = sum;
+      }
+      if (a < 0) return;
+    }
+  } else {
+    e = eta[m];
+    const uint2* row = reinterpret_cast<const uint2*>(xq + m * K);
+#pragma unroll
+    for (int i = 0; i < kAuChunks; ++i) {
+      const int c = tid + kAuThreads * i;
+      q[i] = c < nch ? row[c] : make_uint2(0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kAuChunks; ++i) q[i] = make_uint2(q[i].x ^ 0x80808080u, q[i].y ^ 0x80808080u);
+  const float f = div127_rn(e), sc = __ldg(scale + a);
+  for (int jj = 0; jj < group; ++jj) {
+    const int j = blockIdx.x * group + jj;
+    if (j >= r) break;
+    const uint4* row = reinterpret_cast<const uint4*>(A + (static_cast<int64_t>(a) * r + j) * K);
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kAuChunks; ++i) {
+      const int c = tid + kAuThreads * i;
+      if (c < nch) {
+        const uint4 v = __ldg(row + c);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s = __fmaf_rn(code_f32(q[i], 2 * k), __uint_as_float(w[k] << 16), s);
+          s = __fmaf_rn(code_f32(q[i], 2 * k + 1), __uint_as_float(w[k] & 0xFFFF0000u), s);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (lane == 0) s_red[(jj & 1) ^ 1][warp] = s;
+    __syncthreads();
+    if (tid == 0) {
+      s = 0.0f;
+      for (int w = 0; w < kAuThreads / 32; ++w) s += s_red[(jj & 1) ^ 1][w];
+      u[m * r + j] = __fmul_rn(__fmul_rn(s, f), sc);
+    }
   }
 }
 
+// ---------------------------------------------------------------- u and v of many tokens
+//
+// One CTA per 16 RT tokens and part of the contraction (a cluster splits it
+// and adds the parts through distributed shared memory); the four warps take
+// its steps of 64 in turn, each for all the tokens, so every factor is read
+// once per CTA.  Products on mma.sync m16n8k16: bf16 by bf16, fp32 sums; x~ is
+// exact in bf16, an fp32 dy goes in as three parts.  (tcgen05 would need its
+// operands in shared memory: the work is small beside reading dy, and these
+// fragments come straight from global memory.)  The order of the contraction
+// is free, so lane q of a row reads 16 consecutive codes, and A's row the
+// same 16; for v, B's rows lie across the contraction and pass through shared
+// memory (ldmatrix.trans).  A row's fragment is zeroed for the adapters that
+// are not its own.
+
+struct UvSide {
+  int is_v;                // u: x = codes, F = A; v: x = dy, F = B
+  const void* x;           // M x C
+  int64_t C;               // contraction
+  const __nv_bfloat16* F;
+  const float* eta;        // u
+  float* out;              // M x r
+  int vec;                 // rows of x (and of A) can be read in vectors
+};
+
+struct UvArgs {
+  UvSide side[2];
+  const float* scale;
+  const int32_t* ids;
+  int64_t M;
+  int L, r;
+};
+
+constexpr int kUvThreads = 128;
+constexpr int kUvPitch = 40;  // bf16 of a staged row of B: 32 and 8 that spread the banks
+
+// The plain sum for one output, where a factor is not finite.
 template <typename DyT>
-__global__ void __launch_bounds__(256)
-    k_adapter_v(const DyT* __restrict__ dy, int64_t M, int64_t N, const __nv_bfloat16* __restrict__ B,
-                const float* __restrict__ scale, const int32_t* __restrict__ ids, int L, int r,
-                float* __restrict__ v) {
-  const int lane = threadIdx.x & 31;
-  for (int64_t i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < M * r; i += gridDim.x * 8ll) {
-    const int64_t m = i / r, j = i % r;
-    const int a = adapter_of(ids, m, L);
-    float s = 0.0f;
-    if (a >= 0) {
-      for (int64_t n = lane; n < N; n += 32)
-        s = __fmaf_rn(ld_f32(dy + m * N + n), __bfloat162float(B[(a * N + n) * r + j]), s);
-      s = __fmul_rn(warp_sum(s), scale[a]);
+__device__ __noinline__ float uv_plain(const UvArgs& g, const UvSide& s, int64_t m, int a, int j) {
+  float t = 0.0f;
+  for (int64_t c = 0; c < s.C; ++c) {
+    const float x = s.is_v ? ld_f32(static_cast<const DyT*>(s.x) + m * s.C + c)
+                           : static_cast<float>(static_cast<const int8_t*>(s.x)[m * s.C + c]);
+    const int64_t at = s.is_v ? (a * s.C + c) * g.r + j : (static_cast<int64_t>(a) * g.r + j) * s.C + c;
+    t = __fmaf_rn(x, __bfloat162float(s.F[at]), t);
+  }
+  return t;
+}
+
+// DyT void: u.  smem: the four warps' partial sums (16 RT x 32 each) or
+// their staged rows of B (64 x kUvPitch).
+template <typename XT, int RT>
+__device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_t* smem, const int* s_ids,
+                                        const int* s_list, int nad, volatile int* s_bad) {
+  constexpr bool V = sizeof(XT) > 1;
+  constexpr int T = 16 * RT, PX = sizeof(XT) == 4 ? 3 : 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, q = lane & 3;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * T;
+  const int CS = static_cast<int>(cluster_nctarank()), z = CS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t C = s.C, nst = (C + 63) >> 6;
+  const int64_t lo = nst * z / CS, hi = nst * (z + 1) / CS;
+  const int r = g.r;
+  const bool vec = s.vec != 0, bvec = (r & 7) == 0;
+  float* red = reinterpret_cast<float*>(smem);
+  __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(smem) + warp * 64 * kUvPitch;
+  int id[RT][2];
+  const XT* row[RT][2];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int m = 16 * t + 8 * h + gr;
+      id[t][h] = s_ids[m];
+      row[t][h] = static_cast<const XT*>(s.x) + min(m0 + m, g.M - 1) * C;  // rows past M repeat the last, unused
     }
-    if (lane == 0) v[i] = s;
-  }
-}
-
-// out[m,n] = base[m,n] + sum_j u[m,j] B_a[n,j]; jstride/nstride address the
-// factor so that the same kernel adds v A (factor A_a[j,k]).
-template <typename OutT>
-__global__ void __launch_bounds__(256)
-    k_adapter_add(const float* __restrict__ base, int64_t M, int64_t N, const float* __restrict__ u,
-                  const __nv_bfloat16* __restrict__ F, int64_t nstride, int64_t jstride,
-                  const int32_t* __restrict__ ids, int L, int r, void* __restrict__ out) {
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < M * N; i += gridDim.x * 256ll) {
-    const int64_t m = i / N, n = i % N;
-    const int a = adapter_of(ids, m, L);
-    float s = base[i];
-    if (a >= 0) {
-      const __nv_bfloat16* f = F + static_cast<int64_t>(a) * r * N + n * nstride;
-      float t = 0.0f;
-      for (int j = 0; j < r; ++j) t = __fmaf_rn(u[m * r + j], __bfloat162float(f[j * jstride]), t);
-      s = __fadd_rn(s, t);
+  for (int jb = 0; jb < r; jb += 32) {
+    const int nt = min(4, (r - jb + 7) >> 3);
+    float acc[RT][4][4];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][n][i] = 0.0f;
+    bool bad = false;
+    for (int64_t st = lo + warp; nad && st < hi; st += 4) {
+      const int64_t k0 = st << 6;
+#pragma unroll 1
+      for (int part = 0; part < PX; ++part) {
+        uint32_t xf[RT][4][4];
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if constexpr (!V) {
+              const int64_t k = k0 + 16 * q;
+              uint32_t w[4] = {0, 0, 0, 0};
+              if (vec) {
+                if (k < C) {
+                  const uint4 v = __ldg(reinterpret_cast<const uint4*>(row[t][h] + k));
+                  w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (k + i < C) w[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(row[t][h][k + i])) << (8 * (i & 3));
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                xf[t][i][h] = codes_bf16(w[i]);           // codes 0, 2 of the four
+                xf[t][i][2 + h] = codes_bf16(w[i] >> 8);  // 1, 3
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int64_t k = k0 + 16 * i + 4 * q;
+                const uint2 w = load4_bf16(row[t][h] + k, C - k, vec, part);
+                xf[t][i][h] = w.x;
+                xf[t][i][2 + h] = w.y;
+              }
+            }
+          }
+        for (int li = 0; li < nad; ++li) {
+          const int a = s_list[li];
+          uint32_t b[4][4][2];  // [MMA][8 rank indices][register]
+          if constexpr (!V) {
+            const int64_t k = k0 + 16 * q;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              if (n >= nt) continue;
+              uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+              const int j = jb + 8 * n + gr;
+              const __nv_bfloat16* f = s.F + (static_cast<int64_t>(a) * r + j) * C + k;
+              if (j < r && k < C) {
+                if (vec) {
+                  w[0] = __ldg(reinterpret_cast<const uint4*>(f));
+                  w[1] = __ldg(reinterpret_cast<const uint4*>(f) + 1);
+                } else {
+                  uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                  for (int i = 0; i < 16; ++i)
+                    if (k + i < C)
+                      e[i >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(f) + i)) << (16 * (i & 1));
+                  w[0] = make_uint4(e[0], e[1], e[2], e[3]);
+                  w[1] = make_uint4(e[4], e[5], e[6], e[7]);
+                }
+              }
+              if (nonfinite8(w[0]) || nonfinite8(w[1])) {
+                bad = true;
+                w[0] = w[1] = make_uint4(0, 0, 0, 0);
+              }
+              const uint32_t e[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                b[i][n][0] = __byte_perm(e[2 * i], e[2 * i + 1], 0x5410);
+                b[i][n][1] = __byte_perm(e[2 * i], e[2 * i + 1], 0x7632);
+              }
+            }
+          } else {
+            const __nv_bfloat16* f = s.F + (a * C + k0) * r + jb;
+            __syncwarp();
+            if (bvec) {
+              for (int i = lane; i < 64 * nt; i += 32) {
+                const int n = i / nt, c = i - n * nt;
+                uint4 w = k0 + n < C ? __ldg(reinterpret_cast<const uint4*>(f + static_cast<int64_t>(n) * r) + c)
+                                     : make_uint4(0, 0, 0, 0);
+                if (nonfinite8(w)) {
+                  bad = true;
+                  w = make_uint4(0, 0, 0, 0);
+                }
+                *reinterpret_cast<uint4*>(stage + n * kUvPitch + 8 * c) = w;
+              }
+            } else {
+              const int cols = 8 * nt;
+              for (int i = lane; i < 64 * cols; i += 32) {
+                const int n = i / cols, j = i - n * cols;
+                uint16_t w = k0 + n < C && jb + j < r
+                                 ? __ldg(reinterpret_cast<const uint16_t*>(f) + static_cast<int64_t>(n) * r + j) : 0;
+                if (nonfinite2(w)) {
+                  bad = true;
+                  w = 0;
+                }
+                reinterpret_cast<uint16_t*>(stage)[n * kUvPitch + j] = w;
+              }
+            }
+            __syncwarp();
+            // matrix lane / 8: rows of the contraction 0 1 4 5 .. (registers
+            // 0) or 2 3 6 7 .. (1), rank indices 0-7 or 8-15 of the pair
+            const int mat = lane >> 3, kk = lane & 7;
+            const __nv_bfloat16* at = stage + (4 * (kk >> 1) + (kk & 1) + 2 * (mat & 1)) * kUvPitch + 8 * (mat >> 1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int n = 0; n < 4; n += 2) {
+                if (n >= nt) continue;
+                uint32_t d[4];
+                ldmatrix_x4_trans(d, at + 16 * i * kUvPitch + 8 * n);  // an odd nt: the second half is not used
+                b[i][n][0] = d[0];
+                b[i][n][1] = d[1];
+                b[i][n + 1][0] = d[2];
+                b[i][n + 1][1] = d[3];
+              }
+          }
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            const bool m0own = id[t][0] == a, m1own = id[t][1] == a;
+            if (!__any_sync(0xFFFFFFFFu, m0own || m1own)) continue;
+            const uint32_t k0m = m0own ? 0xFFFFFFFFu : 0u, k1m = m1own ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              if (n >= nt) continue;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma_bf16_16816(acc[t][n], xf[t][i][0] & k0m, xf[t][i][1] & k1m, xf[t][i][2] & k0m, xf[t][i][3] & k1m,
+                               b[i][n][0], b[i][n][1]);
+            }
+          }
+        }
+      }
     }
-    store_out<OutT>(out, i, s);
+    if (bad) *s_bad = 1;
+    __syncthreads();  // the staged rows are read
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float2*>(red + (warp * T + 16 * t + 8 * h + gr) * 32 + 8 * n + 2 * q) =
+              make_float2(acc[t][n][2 * h], acc[t][n][2 * h + 1]);
+    __syncthreads();
+    for (int e = tid; e < T * 32; e += kUvThreads)
+      red[e] = __fadd_rn(__fadd_rn(red[e], red[T * 32 + e]), __fadd_rn(red[2 * T * 32 + e], red[3 * T * 32 + e]));
+    if (CS > 1) cluster_sync_all();
+    else __syncthreads();
+    int any = *s_bad;
+    for (int c = 0; CS > 1 && c < CS; ++c) any |= __float_as_int(ld_cluster_f32(cluster_map(const_cast<int*>(s_bad), c)));
+    for (int e = z * kUvThreads + tid; e < T * 32; e += CS * kUvThreads) {
+      const int m = e >> 5, j = jb + (e & 31), a = s_ids[m];
+      if (j >= r || m0 + m >= g.M) continue;
+      float v = 0.0f;
+      if (a >= 0) {
+        if (CS > 1)
+          for (int c = 0; c < CS; ++c) v = __fadd_rn(v, ld_cluster_f32(cluster_map(red + e, c)));
+        else
+          v = red[e];
+        if (any) v = uv_plain<typename std::conditional<V, XT, float>::type>(g, s, m0 + m, a, j);
+        if constexpr (!V) v = __fmul_rn(v, div127_rn(s.eta[m0 + m]));
+        v = __fmul_rn(v, g.scale[a]);
+      }
+      s.out[(m0 + m) * r + j] = v;
+    }
+    if (CS > 1) cluster_sync_all();
+    else __syncthreads();
   }
 }
 
-template <typename OutT>
-__global__ void __launch_bounds__(256)
-    k_adapter_da(const float* __restrict__ v, const int8_t* __restrict__ xq, const float* __restrict__ eta,
-                 int64_t M, int64_t K, const int32_t* __restrict__ ids, int L, int r, void* __restrict__ dA) {
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < L * r * K; i += gridDim.x * 256ll) {
-    const int64_t k = i % K, aj = i / K, j = aj % r, a = aj / r;
-    float s = 0.0f;
-    for (int64_t m = 0; m < M; ++m)
-      if (ids[m] == a)
-        s = __fmaf_rn(__fmul_rn(v[m * r + j], div127_rn(eta[m])), static_cast<float>(xq[m * K + k]), s);
-    store_out<OutT>(dA, i, s);
+// Grid (tiles of 16 RT tokens, sides, CTAs of a cluster).
+template <typename DyT, int RT>
+__global__ void __launch_bounds__(kUvThreads, 2) k_adapter_uv(const __grid_constant__ UvArgs g) {
+  constexpr int T = 16 * RT;
+  constexpr int kStage = 4 * 64 * kUvPitch * 2, kRed = 4 * T * 32 * 4;
+  __shared__ __align__(16) uint8_t smem[kStage > kRed ? kStage : kRed];
+  __shared__ int s_ids[T < 32 ? 32 : T], s_list[T], s_cnt[8];
+  __shared__ int s_bad;
+  pdl_wait();
+  if (threadIdx.x == 0) {
+    pdl_trigger();
+    s_bad = 0;
   }
+  const UvSide& s = g.side[blockIdx.y];
+  const int nad = tile_adapters(g.ids, static_cast<int64_t>(blockIdx.x) * T, g.M, T, g.L, s_ids, s_list, s_cnt);
+  if (s.is_v) uv_tile<DyT, RT>(g, s, smem, s_ids, s_list, nad, &s_bad);
+  else uv_tile<int8_t, RT>(g, s, smem, s_ids, s_list, nad, &s_bad);
 }
 
-template <typename DyT, typename OutT>
-__global__ void __launch_bounds__(256)
-    k_adapter_db(const DyT* __restrict__ dy, const float* __restrict__ u, int64_t M, int64_t N,
-                 const int32_t* __restrict__ ids, int L, int r, void* __restrict__ dB) {
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < L * N * r; i += gridDim.x * 256ll) {
-    const int64_t j = i % r, an = i / r, n = an % N, a = an / N;
-    float s = 0.0f;
-    for (int64_t m = 0; m < M; ++m)
-      if (ids[m] == a) s = __fmaf_rn(ld_f32(dy + m * N + n), u[m * r + j], s);
-    store_out<OutT>(dB, i, s);
+// ---------------------------------------------------------------- dA and dB
+//
+// One CTA per adapter and 64 columns of A or B (a cluster splits the tokens
+// where there are few of these): it gathers the adapter's tokens out of ids
+// in windows, in order, then 64 of them at a time
+//   out[j][c] += coef[m][j] x[m][c],   dA: coef = v eta / 127, x = x~;
+//                                      dB: coef = u,           x = dy
+// on mma.sync, both operands transposed out of shared memory by ldmatrix.
+// The coefficients go in as P bf16 parts (two for bf16 results, three for
+// fp32 ones).
+
+struct DabSide {
+  const void* x;     // M x C: codes (dA) or dy (dB)
+  int64_t C;
+  const float* coef;  // M x r
+  void* out;
+  int vec;           // rows of x can be read in 16-byte pieces
+};
+
+struct DabArgs {
+  DabSide a, b;
+  const float* eta;
+  const int32_t* ids;
+  int64_t M;
+  int r;
+  unsigned slabs_a;  // blocks x below this: dA
+};
+
+constexpr int kDabThreads = 128;
+constexpr int kDabTokens = 64;   // a chunk
+constexpr int kDabCols = 64;
+constexpr int kDabWindow = 2048;
+constexpr int kDabXPitch = kDabCols + 8;
+
+__host__ __device__ constexpr int dab_rows(int r) { return (r + 15) / 16 * 16; }
+__host__ __device__ constexpr size_t dab_smem(int r, int parts, int xparts) {
+  const size_t tiles = static_cast<size_t>(kDabTokens) * 2 * (parts * (dab_rows(r) + 8) + xparts * kDabXPitch);
+  const size_t out = static_cast<size_t>(dab_rows(r)) * (kDabCols + 4) * 4;
+  return tiles > out ? tiles : out;
+}
+
+// JT: tiles of 16 rank indices (r <= 16 JT).
+template <typename XT, typename OutT, int JT>
+__device__ __forceinline__ void dab_tile(const DabArgs& g, const DabSide& s, int64_t c0, bool is_a, uint8_t* smem,
+                                         uint16_t* s_tok, int* s_cnt) {
+  constexpr int P = sizeof(OutT) == 4 ? 3 : 2, PX = sizeof(XT) == 4 ? 3 : 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int CS = static_cast<int>(cluster_nctarank()), z = CS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int r = g.r, rows = dab_rows(r), cpitch = rows + 8;
+  const int a = blockIdx.y;
+  __nv_bfloat16* s_coef = reinterpret_cast<__nv_bfloat16*>(smem);          // [P][token][cpitch]
+  __nv_bfloat16* s_x = s_coef + P * kDabTokens * cpitch;                   // [PX][token][kDabXPitch]
+  float acc[JT][2][4];
+#pragma unroll
+  for (int t = 0; t < JT; ++t)
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t][n][i] = 0.0f;
+
+  const int xt = tid >> 1, xh = tid & 1;  // this thread's token of a chunk and half of its 64 columns
+  int chunk0 = 0;                         // chunks of the windows before, for the turns of a cluster's CTAs
+  for (int64_t w0 = 0; w0 < g.M; w0 += kDabWindow) {
+    // the window's tokens of this adapter, in order
+    const int wn = static_cast<int>(min(static_cast<int64_t>(kDabWindow), g.M - w0));
+    constexpr int kEach = kDabWindow / kDabThreads;
+    unsigned mine = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int t = tid * kEach + i;
+      if (t < wn && __ldg(g.ids + w0 + t) == a) mine |= 1u << i;
+    }
+    const int n = __popc(mine);
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    __syncthreads();  // the list and counts of the window before are read
+    if (lane == 31) s_cnt[warp] = inc;
+    __syncthreads();
+    int at = inc - n, total = 0;
+#pragma unroll
+    for (int w = 0; w < kDabThreads / 32; ++w) {
+      if (w < warp) at += s_cnt[w];
+      total += s_cnt[w];
+    }
+    while (mine) {
+      const int i = __ffs(mine) - 1;
+      mine &= mine - 1;
+      s_tok[at++] = static_cast<uint16_t>(tid * kEach + i);
+    }
+    __syncthreads();
+    const int chunks = (total + kDabTokens - 1) / kDabTokens;
+    for (int c = 0; c < chunks; ++c) {
+      if ((chunk0 + c) % CS != z) continue;
+      const int left = total - c * kDabTokens;
+      const uint16_t* tok = s_tok + c * kDabTokens;
+      // 32 columns of a token a thread
+      {
+        const bool in = xt < left;
+        const XT* src = static_cast<const XT*>(s.x) + (w0 + (in ? tok[xt] : 0)) * s.C + c0 + 32 * xh;
+        const int64_t cols = in ? s.C - c0 - 32 * xh : 0;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(s_x + xt * kDabXPitch + 32 * xh);
+        if constexpr (sizeof(XT) == 1) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t w[4] = {0, 0, 0, 0};
+            if (s.vec) {
+              if (16 * i < cols) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+                w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+              }
+            } else {
+#pragma unroll
+              for (int b = 0; b < 16; ++b)
+                if (16 * i + b < cols) w[b >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(src[16 * i + b])) << (8 * (b & 3));
+            }
+            uint32_t o[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t e = codes_bf16(w[k]), d = codes_bf16(w[k] >> 8);  // codes 0, 2 and 1, 3
+              o[2 * k] = __byte_perm(e, d, 0x5410);
+              o[2 * k + 1] = __byte_perm(e, d, 0x7632);
+            }
+            reinterpret_cast<uint4*>(dst)[2 * i] = make_uint4(o[0], o[1], o[2], o[3]);
+            reinterpret_cast<uint4*>(dst)[2 * i + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        } else {
+#pragma unroll
+          for (int p = 0; p < PX; ++p)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint2 lo = load4_bf16(src + 8 * i, cols - 8 * i, s.vec != 0, p);
+              const uint2 hi = load4_bf16(src + 8 * i + 4, cols - 8 * i - 4, s.vec != 0, p);
+              reinterpret_cast<uint4*>(dst + p * kDabTokens * kDabXPitch / 2)[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
+        }
+      }
+      for (int i = tid; i < kDabTokens * rows; i += kDabThreads) {
+        const int t = i / rows, j = i - t * rows;
+        float f = 0.0f;
+        if (t < left && j < r) {
+          const int64_t m = w0 + tok[t];
+          f = s.coef[m * r + j];
+          if (is_a) f = __fmul_rn(f, div127_rn(__ldg(g.eta + m)));
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const __nv_bfloat16 h = __float2bfloat16_rn(f);
+          s_coef[(p * kDabTokens + t) * cpitch + j] = h;
+          f = bf16_part<2>(f, 1);
+        }
+      }
+      __syncthreads();
+      const int kk = lane & 7, mat = lane >> 3;
+#pragma unroll
+      for (int ks = 0; ks < kDabTokens / 16; ++ks) {
+        uint32_t bx[PX][4];  // columns 16 warp + 0-7 (registers 0, 1) and 8-15 (2, 3)
+#pragma unroll
+        for (int p = 0; p < PX; ++p)
+          ldmatrix_x4_trans(bx[p], s_x + (p * kDabTokens + 16 * ks + kk + 8 * (mat & 1)) * kDabXPitch + 16 * warp + 8 * (mat >> 1));
+#pragma unroll
+        for (int t = 0; t < JT; ++t) {
+          if (16 * t >= rows) continue;
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            uint32_t f[4];  // rows j 0-7, 8-15 at tokens 0-7, then at 8-15
+            ldmatrix_x4_trans(f, s_coef + (p * kDabTokens + 16 * ks + kk + 8 * (mat >> 1)) * cpitch + 16 * t + 8 * (mat & 1));
+#pragma unroll
+            for (int px = 0; px < PX; ++px) {
+              mma_bf16_16816(acc[t][0], f[0], f[1], f[2], f[3], bx[px][0], bx[px][1]);
+              mma_bf16_16816(acc[t][1], f[0], f[1], f[2], f[3], bx[px][2], bx[px][3]);
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    chunk0 += chunks;
   }
+
+  // out: the CTA's sums into shared memory, a cluster's added up by rows
+  float* s_out = reinterpret_cast<float*>(smem);
+  constexpr int kOPitch = kDabCols + 4;
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < JT; ++t) {
+    if (16 * t >= rows) continue;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2*>(s_out + (16 * t + 8 * h + (lane >> 2)) * kOPitch + 16 * warp + 8 * n + 2 * (lane & 3)) =
+            make_float2(acc[t][n][2 * h], acc[t][n][2 * h + 1]);
+  }
+  if (CS > 1) cluster_sync_all();
+  else __syncthreads();
+  const int cols = static_cast<int>(min(static_cast<int64_t>(kDabCols), s.C - c0));
+  const int64_t base = is_a ? static_cast<int64_t>(a) * r * s.C + c0 : (static_cast<int64_t>(a) * s.C + c0) * r;
+  for (int e = z * kDabThreads + tid; e < r * kDabCols; e += CS * kDabThreads) {
+    // neighbouring threads take neighbouring outputs: A is r x K, B is N x r
+    const int j = is_a ? e / kDabCols : e % r, c = is_a ? e % kDabCols : e / r;
+    if (c >= cols) continue;
+    float v = s_out[j * kOPitch + c];
+    if (CS > 1) {
+      v = 0.0f;
+      for (int k = 0; k < CS; ++k) v = __fadd_rn(v, ld_cluster_f32(cluster_map(s_out + j * kOPitch + c, k)));
+    }
+    store_out<OutT>(s.out, base + (is_a ? j * s.C + c : static_cast<int64_t>(c) * r + j), v);
+  }
+  if (CS > 1) cluster_sync_all();  // the sums stay until they are read
+}
+
+// Grid (slabs of A, then of B; adapters; CTAs of a cluster).
+template <typename DyT, typename OutT, int JT>
+__global__ void __launch_bounds__(kDabThreads) k_adapter_dab(const __grid_constant__ DabArgs g) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint16_t s_tok[kDabWindow];
+  __shared__ int s_cnt[kDabThreads / 32];
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
+  if (blockIdx.x < g.slabs_a)
+    dab_tile<int8_t, OutT, JT>(g, g.a, static_cast<int64_t>(blockIdx.x) * kDabCols, true, smem, s_tok, s_cnt);
+  else
+    dab_tile<DyT, OutT, JT>(g, g.b, static_cast<int64_t>(blockIdx.x - g.slabs_a) * kDabCols, false, smem, s_tok, s_cnt);
 }
 
 }  // namespace bl

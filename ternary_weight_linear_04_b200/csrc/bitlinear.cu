@@ -442,10 +442,10 @@ bool reg_decode_geometry(int64_t K, int64_t N, int sms, RegGeom* g) {
   return true;
 }
 
-template <int RB, int NJ>
+template <int RB, int NJ, bool AD>
 bl_status launch_decode_reg_nj(const bl::RegDecodeArgs& a, const RegGeom& g, cudaStream_t st) {
   static int done[kMaxDevices] = {0};
-  auto kern = bl::k_decode_reg<RB, NJ>;
+  auto kern = bl::k_decode_reg<RB, NJ, AD>;
   if (!ensure_smem(kern, 0, done)) return BL_ERR_CUDA;
   return launch_pdl(kern, dim3(static_cast<unsigned>(g.grid)), dim3(bl::kRegThreads),
                     static_cast<size_t>(32 * NJ * 16), st, a);
@@ -453,7 +453,7 @@ bl_status launch_decode_reg_nj(const bl::RegDecodeArgs& a, const RegGeom& g, cud
 
 bl_status launch_decode_reg(const bl::RegDecodeArgs& a, const RegGeom& g, cudaStream_t st) {
 #define BL_REG_CASE(R, J) \
-  if (g.RB == R && g.NJ == J) return launch_decode_reg_nj<R, J>(a, g, st);
+  if (g.RB == R && g.NJ == J) return a.ad.u ? launch_decode_reg_nj<R, J, true>(a, g, st) : launch_decode_reg_nj<R, J, false>(a, g, st);
   BL_REG_CASE(1, 2) BL_REG_CASE(1, 4) BL_REG_CASE(1, 7) BL_REG_CASE(1, 8) BL_REG_CASE(1, 12)
   BL_REG_CASE(1, 16) BL_REG_CASE(1, 17) BL_REG_CASE(1, 24)
   BL_REG_CASE(2, 2) BL_REG_CASE(2, 4) BL_REG_CASE(2, 7) BL_REG_CASE(2, 8) BL_REG_CASE(2, 12)
@@ -652,14 +652,15 @@ int tc_split(int64_t tiles, int64_t K, int sms) {
   return static_cast<int>(ks);
 }
 
-template <int BM, typename OutT>
+template <int BM, typename OutT, bool AD>
 bl_status launch_tc_bm(const int8_t* xq, const float* eta, const int32_t* xsum, int M, int K,
                        const uint8_t* packed, const float* gamma, int N, void* y, int32_t* y_int,
-                       int sms, int wstatic, cudaStream_t st) {
+                       int sms, int wstatic, cudaStream_t st, const bl::AdapterAdd& ad) {
   using Cfg = bl::TcCfg<BM>;
   static int smem_done[kMaxDevices] = {0};
-  auto kern = bl::k_gemm_tc<BM, OutT>;
-  if (!ensure_smem(kern, Cfg::kSmem, smem_done)) return BL_ERR_CUDA;
+  auto kern = bl::k_gemm_tc<BM, OutT, AD>;
+  constexpr size_t smem = AD ? Cfg::kSmemAdapters : Cfg::kSmem;
+  if (!ensure_smem(kern, smem, smem_done)) return BL_ERR_CUDA;
   CUtensorMap tm_x, tm_w;
   if (!make_tmap_u8(&tm_x, xq, static_cast<uint64_t>(M), static_cast<uint64_t>(K), BM, bl::kTcBK, true))
     return BL_ERR_CUDA;
@@ -670,23 +671,31 @@ bl_status launch_tc_bm(const int8_t* xq, const float* eta, const int32_t* xsum, 
   if (grid.y > 65535) return BL_ERR_UNSUPPORTED;
   const int ks = tc_split<BM>(grid.x * grid.y, K, sms);
   if (ks <= 1)
-    return launch_pdl(kern, grid, dim3(bl::kTcThreads), Cfg::kSmem, st, tm_x, tm_w, eta, xsum,
-                      gamma, M, K, N, y, y_int, 1, wstatic);
+    return launch_pdl(kern, grid, dim3(bl::kTcThreads), smem, st, tm_x, tm_w, eta, xsum,
+                      gamma, M, K, N, y, y_int, 1, wstatic, ad);
   grid.z = static_cast<unsigned>(ks);
-  return launch_pdl_cluster(kern, grid, dim3(bl::kTcThreads), Cfg::kSmem, st,
+  return launch_pdl_cluster(kern, grid, dim3(bl::kTcThreads), smem, st,
                             static_cast<unsigned>(ks), tm_x, tm_w, eta, xsum, gamma, M, K, N, y,
-                            y_int, ks, wstatic);
+                            y_int, ks, wstatic, ad);
+}
+
+template <typename OutT, bool AD>
+bl_status launch_tc_ad(const int8_t* xq, const float* eta, const int32_t* xsum, int M, int K,
+                       const uint8_t* packed, const float* gamma, int N, void* y, int32_t* y_int,
+                       int sms, int ws, cudaStream_t st, const bl::AdapterAdd& ad) {
+  if (M <= 16) return launch_tc_bm<16, OutT, AD>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
+  if (M <= 32) return launch_tc_bm<32, OutT, AD>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
+  if (M <= 64) return launch_tc_bm<64, OutT, AD>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
+  if (M <= 128) return launch_tc_bm<128, OutT, AD>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
+  return launch_tc_bm<256, OutT, AD>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
 }
 
 template <typename OutT>
 bl_status launch_tc(const int8_t* xq, const float* eta, const int32_t* xsum, int M, int K,
                     const uint8_t* packed, const float* gamma, int N, void* y, int32_t* y_int,
-                    int sms, int ws, cudaStream_t st) {
-  if (M <= 16) return launch_tc_bm<16, OutT>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st);
-  if (M <= 32) return launch_tc_bm<32, OutT>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st);
-  if (M <= 64) return launch_tc_bm<64, OutT>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st);
-  if (M <= 128) return launch_tc_bm<128, OutT>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st);
-  return launch_tc_bm<256, OutT>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st);
+                    int sms, int ws, cudaStream_t st, const bl::AdapterAdd& ad) {
+  return ad.u ? launch_tc_ad<OutT, true>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad)
+              : launch_tc_ad<OutT, false>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
 }
 
 bool fast_layout_ok(int64_t K, const void* xq, const void* packed, const void* y, const void* y_int) {
@@ -714,7 +723,8 @@ bl_path select_path(int64_t M, int64_t K, int64_t N, int sms, const void* xq, co
 
 bl_status forward_impl(const int8_t* xq, const float* eta, const int32_t* xsum, int64_t M,
                        int64_t K, const uint8_t* packed, const float* gamma, int64_t N, void* y,
-                       bl_dtype ydt, int32_t* y_int, bl_path path, unsigned flags, void* stream) {
+                       bl_dtype ydt, int32_t* y_int, bl_path path, unsigned flags, void* stream,
+                       const bl::AdapterAdd& ad = {}) {
   if (M < 0 || K < 1 || N < 1) return BL_ERR_INVALID_ARG;
   if (ydt != BL_F32 && ydt != BL_BF16) return BL_ERR_INVALID_ARG;
   if (path < BL_PATH_AUTO || path > BL_PATH_GENERIC) return BL_ERR_INVALID_ARG;
@@ -735,7 +745,7 @@ bl_status forward_impl(const int8_t* xq, const float* eta, const int32_t* xsum, 
     // 2..8 tokens: the register-resident kernel when the CTA's share fits
     // (and no shape is forced for the shared-memory kernel, which takes up
     // to 4 tokens).
-    const bool reg_on = M >= 2 && g_decode_reg.load(std::memory_order_relaxed) != 0 &&
+    const bool reg_on = (M >= 2 || ad.u) && g_decode_reg.load(std::memory_order_relaxed) != 0 &&
                         g_force_G.load(std::memory_order_relaxed) == 0 &&
                         g_force_RB.load(std::memory_order_relaxed) == 0;
     MmaGeom gm;
@@ -748,10 +758,11 @@ bl_status forward_impl(const int8_t* xq, const float* eta, const int32_t* xsum, 
       r.y_int = y_int;
       r.rows_per_cta = gm.rows_per_cta;
       r.weights_static = (flags & BL_FLAG_WEIGHTS_STATIC) ? 1 : 0;
+      r.ad = ad;
       return launch_decode_mma(r, gm, s);
     }
     RegMGeom mg;
-    if (reg_on && regm_geometry(M, K, N, sms, &mg)) {
+    if (reg_on && regm_geometry(M < 2 ? 2 : M, K, N, sms, &mg)) {
       bl::RegMultiArgs r = {};
       r.xq = xq; r.eta = eta; r.xsum = xsum;
       r.M = static_cast<int>(M); r.K = static_cast<int>(K); r.N = static_cast<int>(N);
@@ -760,9 +771,13 @@ bl_status forward_impl(const int8_t* xq, const float* eta, const int32_t* xsum, 
       r.y_int = y_int;
       r.rows_per_cta = mg.rows_per_cta;
       r.weights_static = (flags & BL_FLAG_WEIGHTS_STATIC) ? 1 : 0;
+      r.ad = ad;
       return launch_decode_regm(r, mg, false, s);
     }
-    if (!decode_ok(M, K)) return BL_ERR_UNSUPPORTED;
+    if (ad.u) path = BL_PATH_TCGEN05;  // the shared-memory kernel has no adapters
+    else if (!decode_ok(M, K)) return BL_ERR_UNSUPPORTED;
+  }
+  if (path == BL_PATH_GEMV) {
     bl::DecodeArgs a = {};
     a.x = xq; a.eta = eta; a.xsum = xsum; a.M = (int)M; a.K = (int)K; a.N = (int)N;
     a.packed = packed; a.gamma = gamma; a.y = y; a.y_int = y_int;
@@ -777,9 +792,9 @@ bl_status forward_impl(const int8_t* xq, const float* eta, const int32_t* xsum, 
       return BL_ERR_UNSUPPORTED;
     return ydt == BL_F32
                ? launch_tc<float>(xq, eta, xsum, (int)M, (int)K, packed, gamma, (int)N, y, y_int,
-                                  sms, ws, s)
+                                  sms, ws, s, ad)
                : launch_tc<__nv_bfloat16>(xq, eta, xsum, (int)M, (int)K, packed, gamma, (int)N, y,
-                                          y_int, sms, ws, s);
+                                          y_int, sms, ws, s, ad);
   }
   return ydt == BL_F32
              ? launch_generic<float>(xq, eta, M, K, packed, gamma, N, y, y_int, sms, s)

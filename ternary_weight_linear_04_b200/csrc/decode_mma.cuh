@@ -44,6 +44,7 @@
 // reads only its share of x~).
 #pragma once
 
+#include "adapter_add.cuh"
 #include "common.cuh"
 #include "decode.cuh"
 
@@ -64,6 +65,7 @@ struct MmaDecodeArgs {
   int32_t* y_int;          // optional
   int rows_per_cta;        // <= 16 * RBK
   int weights_static;
+  AdapterAdd ad;           // u NULL: none
 };
 
 // Slots per token, padded to 4 mod 8 (see above).
@@ -213,7 +215,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_decode_mma(const MmaDecodeAr
     for (int k = 0; k < KP; ++k) tot += part[(static_cast<size_t>(k) * T + t) * PS + row];
     const int32_t yi = tot - s_xsum[t];
     const int64_t o = static_cast<int64_t>(t) * a.N + r_begin + row;
-    const float yv = rescale(yi, s_scale[t]);
+    float yv = rescale(yi, s_scale[t]);
+    if (a.ad.u) yv = adapter_add(a.ad.u, a.ad.B, a.ad.ids, a.ad.L, a.ad.r, t, r_begin + row, a.N, yv);
     if (a.y_bf16) store_out<__nv_bfloat16>(a.y, o, yv);
     else store_out<float>(a.y, o, yv);
     if (a.y_int) a.y_int[o] = yi;

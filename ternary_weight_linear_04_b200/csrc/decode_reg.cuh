@@ -38,6 +38,7 @@
 // 64 registers (every switch between the two kernels then lost the overlap).
 #pragma once
 
+#include "adapter_add.cuh"
 #include "common.cuh"
 #include "decode.cuh"
 #include "quant.cuh"
@@ -59,6 +60,7 @@ struct RegDecodeArgs {
   int8_t* xq_out;          // optional: CTA 0 writes x~, eta, xsum
   float* eta_out;
   int32_t* xsum_out;
+  AdapterAdd ad;           // AD
 };
 
 // The codes of one 16-byte chunk of bf16 activations when eta is the 1e-5
@@ -82,8 +84,9 @@ __device__ __forceinline__ uint32_t ld_nc_na_u32(const void* p) {
 }
 
 // NJ words per lane and row (K <= 512 NJ), RB rows per warp.  Shared
-// memory: 32 NJ slots of 16 bytes.
-template <int RB, int NJ>
+// memory: 32 NJ slots of 16 bytes.  AD: an adapter is added (a variant of its
+// own: the call costs the others a spilled register).
+template <int RB, int NJ, bool AD>
 __global__ void __launch_bounds__(kRegThreads + 64, 2) k_decode_reg(const RegDecodeArgs a) {
   static_assert(RB == 1 || RB == 2 || RB == 4, "RB rows per warp: 1, 2 or 4");
   constexpr int XC = (NJ + 7) / 8;  // 16-byte chunks of x per thread
@@ -233,7 +236,8 @@ __global__ void __launch_bounds__(kRegThreads + 64, 2) k_decode_reg(const RegDec
   if ((lane & (kGroup - 1)) == 0 && row0 + vi < nrows) {
     const int32_t yi = tot - xsum;
     const int64_t o = r_begin + row0 + vi;
-    const float yv = rescale(yi, sc);
+    float yv = rescale(yi, sc);
+    if constexpr (AD) yv = adapter_add(a.ad.u, a.ad.B, a.ad.ids, a.ad.L, a.ad.r, 0, r_begin + row0 + vi, a.N, yv);
     if (a.y_bf16) store_out<__nv_bfloat16>(a.y, o, yv);
     else store_out<float>(a.y, o, yv);
     if (a.y_int) a.y_int[o] = yi;
@@ -276,6 +280,7 @@ struct RegMultiArgs {
   int32_t* y_int;          // optional
   int rows_per_cta;        // <= 16 * RB
   int weights_static;
+  AdapterAdd ad;           // u NULL: none
 };
 
 constexpr int kRegMultiMaxMT = 8;
@@ -469,7 +474,8 @@ __global__ void __launch_bounds__(kRegThreads, 1) k_decode_regm(const RegMultiAr
   if ((lane & (kGroup - 1)) == 0 && row0 + r < nrows && m < M) {
     const int32_t yi = tot - s_xsum[m];
     const int64_t o = static_cast<int64_t>(m) * a.N + r_begin + row0 + r;
-    const float yv = rescale(yi, s_scale[m]);
+    float yv = rescale(yi, s_scale[m]);
+    if (a.ad.u) yv = adapter_add(a.ad.u, a.ad.B, a.ad.ids, a.ad.L, a.ad.r, m, r_begin + row0 + r, a.N, yv);
     if (a.y_bf16) store_out<__nv_bfloat16>(a.y, o, yv);
     else store_out<float>(a.y, o, yv);
     if (a.y_int) a.y_int[o] = yi;

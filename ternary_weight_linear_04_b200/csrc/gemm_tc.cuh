@@ -47,7 +47,9 @@
 
 #include <cuda.h>
 
+#include "adapter_add.cuh"
 #include "common.cuh"
+#include "tc_bf16.cuh"
 
 namespace bl {
 
@@ -73,17 +75,27 @@ struct TcCfg {
   static constexpr int kTmemCols = BM < 32 ? 32 : BM;
   static constexpr int kBarBytes = 8 * (4 * kStages + 2) + 16 + 8 * BM;
   static constexpr size_t kSmem = 1024 + kStageRegion + kBarBytes;
-  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-  static_assert(BM > 32 || kSmem <= 113 * 1024, "two CTAs per SM for the small token tiles");
+  static constexpr size_t kSmemAdapters = kSmem + 8 * BM + 48;  // the tile's adapter ids and their list
+  static_assert(kSmemAdapters <= 227 * 1024, "shared memory per CTA");
+  static_assert(BM > 32 || kSmemAdapters <= 113 * 1024, "two CTAs per SM for the small token tiles");
 };
 
-template <int BM, typename OutT>
+// AD: low-rank adapters beside the projection.  Behind the K loop come steps
+// of 64 entries of a second contraction (kind::f16, bf16 with fp32 sums, its
+// own TMEM columns): an entry is one (adapter of the tile's tokens, part of
+// u, rank index), its weight-side row B_a and its token-side row the part of
+// u, zero for the tokens of other adapters.  u (fp32) is split into two bf16
+// parts for bf16 outputs (2^-17 of it) and three for fp32 ones (all of it).
+// The unpack warps write both operands; entries of several adapters share a
+// step, so small ranks do not pad.  Of a K split only CTA 0 has these steps.
+template <int BM, typename OutT, bool AD>
 __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
     k_gemm_tc(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
               const float* __restrict__ eta, const int32_t* __restrict__ xsum,
               const float* __restrict__ gamma_p, int M, int K, int N, void* __restrict__ y,
-              int32_t* __restrict__ y_int, int ksplit, int wstatic) {
+              int32_t* __restrict__ y_int, int ksplit, int wstatic, const AdapterAdd ad) {
   using Cfg = TcCfg<BM>;
+  constexpr int kParts = sizeof(OutT) == 4 ? 3 : 2;
   constexpr int S = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte aligned base (the swizzle atom), by pointer arithmetic on the
@@ -102,6 +114,10 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* s_scale = reinterpret_cast<float*>(tmem_slot + 4);
   int32_t* s_xsum = reinterpret_cast<int32_t*>(s_scale + BM);
+  int* s_ids = s_xsum + BM;    // AD
+  int* s_list = s_ids + BM;
+  int* s_cnt = s_list + BM;
+  volatile int* s_bad = s_cnt + 8;  // a factor is not finite
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -128,6 +144,7 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
     mbar_init(accum_full, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
+    if constexpr (AD) *s_bad = 0;
     mbar_init_fence();
     tma_prefetch_desc(&tm_x);
     tma_prefetch_desc(&tm_w);
@@ -135,7 +152,7 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
       for (int i = 0; i < p_first; ++i) issue_p(i);  // not written by the preceding kernel
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, Cfg::kTmemCols);
+    tmem_alloc(tmem_slot, AD ? 2 * Cfg::kTmemCols : Cfg::kTmemCols);
     tmem_relinquish();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -148,6 +165,12 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
       s_xsum[i] = in ? xsum[m0 + i] : 0;
     }
   }
+  int entries = 0, asteps = 0;
+  if constexpr (AD)
+    if (zr == 0) {
+      entries = tile_adapters(ad.ids, m0, M, BM, ad.L, s_ids, s_list, s_cnt) * kParts * ad.r;
+      asteps = (entries + 63) >> 6;
+    }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -206,6 +229,25 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
           tc_mma_i8_ss(tmem_d, ad + 2 * kk, bd + 2 * kk, idesc, 1u);
         tc_commit(empty + s);
       }
+      if constexpr (AD) {
+        constexpr uint32_t idesc16 = make_idesc_bf16(kTcBN, BM, false, false);
+        for (int i = nkt; ok && i < nkt + asteps; ++i) {
+          const int s = i % S;
+          ok = mbar_wait(full_a + s, static_cast<uint32_t>(i / S) & 1u, abort_flag);
+          if (!ok) {
+            tc_commit(drain);
+            mbar_drain(drain, 0);
+            break;
+          }
+          tc_fence_after();
+          const uint64_t da = a_desc0 + static_cast<uint64_t>(s * (Cfg::kABytes >> 4));
+          const uint64_t db = b_desc0 + static_cast<uint64_t>(s * (Cfg::kBBytes >> 4));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_bf16_ss(tmem_d + Cfg::kTmemCols, da + 2 * kk, db + 2 * kk, idesc16, i != nkt || kk != 0 ? 1u : 0u);
+          tc_commit(empty + s);
+        }
+      }
       if (ok) tc_commit(accum_full);
     }
   } else {
@@ -246,6 +288,81 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
       if (g_test_fault == 1 && u == 0 && i == 0) continue;  // a wait that nothing completes
 #endif
       if (lane == 0) mbar_arrive(full_a + s);
+    }
+    if constexpr (AD) {
+      const int r = ad.r, group = kParts * r;  // entries of one adapter
+      const bool chunked = (r & 7) == 0;       // eight entries share adapter and part
+      for (int i = nkt; ok && i < nkt + asteps; ++i) {
+        const int s = i % S, e0 = (i - nkt) * 64;
+        if (i >= S) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + s, static_cast<uint32_t>(i / S - 1) & 1u, abort_flag));
+          if (!ok) break;
+        }
+        {  // rows of B: this thread's feature, 32 entries
+          const int64_t n = n0 + urow;
+          uint8_t* dst = a_row + s * Cfg::kABytes;
+#pragma unroll 1
+          for (int c = uhalf * 4; c < uhalf * 4 + 4; ++c) {
+            const int e = e0 + 8 * c;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (n < N && e < entries) {
+              if (chunked) {
+                const int li = e / group, j = (e - li * group) % r;
+                v = __ldg(reinterpret_cast<const uint4*>(ad.B + (static_cast<int64_t>(s_list[li]) * N + n) * r + j));
+              } else {
+                uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                  if (e + b < entries) {
+                    const int li = (e + b) / group, j = (e + b - li * group) % r;
+                    const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(ad.B) +
+                                             (static_cast<int64_t>(s_list[li]) * N + n) * r + j);
+                    w[b >> 1] |= h << (16 * (b & 1));
+                  }
+                v = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+            if (nonfinite8(v)) {
+              v = make_uint4(0, 0, 0, 0);
+              *s_bad = 1;
+            }
+            *reinterpret_cast<uint4*>(dst + ((c ^ r8) << 4)) = v;
+          }
+        }
+        // rows of u: one token and 8 entries at a time
+#pragma unroll 1
+        for (int q = 32 * u + lane; q < BM * 8; q += 32 * kTcUnpackWarps) {
+          const int t = q % BM, c = q / BM, id = s_ids[t];
+          const int e = e0 + 8 * c;
+          const float* ut = ad.u + static_cast<int64_t>(m0 + t) * r;
+          uint32_t w[4] = {0, 0, 0, 0};
+          if (id >= 0 && e < entries) {
+            if (chunked) {
+              const int li = e / group, rem = e - li * group, p = rem / r;
+              if (s_list[li] == id) {
+                const float* x = ut + rem - p * r;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                  w[b] = pack_bf16(bf16_part<kParts>(x[2 * b], p), bf16_part<kParts>(x[2 * b + 1], p));
+              }
+            } else {
+              float f[8];
+#pragma unroll
+              for (int b = 0; b < 8; ++b) {
+                const int li = (e + b) / group, rem = e + b - li * group, p = rem / r;
+                f[b] = e + b < entries && s_list[li] == id ? bf16_part<kParts>(ut[rem - p * r], p) : 0.0f;
+              }
+#pragma unroll
+              for (int b = 0; b < 4; ++b) w[b] = pack_bf16(f[2 * b], f[2 * b + 1]);
+            }
+          }
+          *reinterpret_cast<uint4*>(sB + s * Cfg::kBBytes + (t >> 3) * 1024 + (t & 7) * 128 + ((c ^ (t & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full_a + s);
+      }
     }
     if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(accum_full, 0, abort_flag));
     epi_ok = ok && __all_sync(0xFFFFFFFFu, *abort_flag == 0);
@@ -314,13 +431,22 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
           v[j + 3] += static_cast<uint32_t>(t.w);
         }
       }
+      uint32_t f[16];
+      if constexpr (AD)
+        if (asteps) {
+          tmem_ld_32x32b_x16(t_row + Cfg::kTmemCols + cc, f);
+          tmem_ld_wait();
+        }
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const int m = m0 + cc + j;
         if (m < M && n < N) {
           const int32_t yi = static_cast<int32_t>(v[j]) - s_xsum[cc + j];
           const int64_t o = static_cast<int64_t>(m) * N + n;
-          store_out<OutT>(y, o, rescale(yi, s_scale[cc + j]));
+          float yv = rescale(yi, s_scale[cc + j]);
+          if constexpr (AD)
+            if (asteps) yv = *s_bad ? adapter_add(ad.u, ad.B, ad.ids, ad.L, ad.r, m, n, N, yv) : __fadd_rn(yv, __uint_as_float(f[j]));
+          store_out<OutT>(y, o, yv);
           if (y_int) y_int[o] = yi;
         }
       }
@@ -330,7 +456,7 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_d, Cfg::kTmemCols);
+    tmem_dealloc(tmem_d, AD ? 2 * Cfg::kTmemCols : Cfg::kTmemCols);
   }
 }
 

@@ -15,7 +15,9 @@
 
 #include <cuda.h>
 
+#include "adapter_add.cuh"
 #include "common.cuh"
+#include "decode.cuh"
 #include "tc_bf16.cuh"
 
 namespace bl {
@@ -27,27 +29,32 @@ __device__ __forceinline__ float ld_f32<float>(const float* p) { return *p; }
 template <>
 __device__ __forceinline__ float ld_f32<__nv_bfloat16>(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-// The adapter of token m: ids[m], or -1 (none) when outside [0, L).
-__device__ __forceinline__ int adapter_of(const int32_t* ids, int64_t m, int L) {
-  const int a = ids[m];
-  return static_cast<unsigned>(a) < static_cast<unsigned>(L) ? a : -1;
-}
-
 // ---------------------------------------------------------------- operand copies
 
 // Rows of `bytes` bytes copied into rows of `stride` bytes (a multiple of
 // 16), the rest zero: operands whose rows do not start on 16 bytes cannot be
-// read by TMA.  One pass over the operand, small beside the product.
-__global__ void __launch_bounds__(256)
-    k_pad_rows(const uint8_t* __restrict__ src, int64_t rows, int64_t bytes, int64_t stride,
-               uint8_t* __restrict__ dst) {
-  const int64_t chunks = stride / 16;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < rows * chunks; i += gridDim.x * 256ll) {
+// read by TMA.  One pass over the operand, small beside the product; two
+// operands in one launch.
+struct PadJob {
+  const uint8_t* src;
+  int64_t rows, bytes, stride;  // rows 0: nothing to do
+  uint8_t* dst;
+};
+
+__global__ void __launch_bounds__(256) k_pad_rows(const PadJob first, const PadJob second) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
+  const int64_t n1 = first.rows * (first.stride / 16), n2 = second.rows * (second.stride / 16);
+  for (int64_t it = blockIdx.x * 256ll + threadIdx.x; it < n1 + n2; it += gridDim.x * 256ll) {
+    const PadJob& job = it < n1 ? first : second;
+    const int64_t i = it < n1 ? it : it - n1;
+    const uint8_t* src = job.src;
+    const int64_t chunks = job.stride / 16;
     const int64_t row = i / chunks, c = (i - row * chunks) * 16;
-    const int64_t left = bytes - c;
-    const int64_t off = row * bytes + c;
+    const int64_t left = job.bytes - c;
+    const int64_t off = row * job.bytes + c;
     uint32_t w[4];
-    if (off + 20 <= rows * bytes) {  // rows start anywhere: five aligned words, shifted together
+    if (off + 20 <= job.rows * job.bytes) {  // rows start anywhere: five aligned words, shifted together
       const uint32_t* s4 = reinterpret_cast<const uint32_t*>(src + (off & ~int64_t{3}));
       const unsigned sh = 8 * static_cast<unsigned>(off & 3);
       uint32_t in[5];
@@ -68,7 +75,7 @@ __global__ void __launch_bounds__(256)
           if (4 * j + b < left) w[j] |= static_cast<uint32_t>(src[off + 4 * j + b]) << (8 * b);
       }
     }
-    *reinterpret_cast<uint4*>(dst + row * stride + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(job.dst + row * job.stride + c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -78,6 +85,8 @@ __global__ void __launch_bounds__(256)
     k_split_planes(const float* __restrict__ src, int64_t rows, int64_t cols, int64_t cols_pad,
                    __nv_bfloat16* __restrict__ dst) {
   const int64_t plane = rows * cols_pad;
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < plane; i += gridDim.x * 256ll) {
     const int64_t row = i / cols_pad, c = i - row * cols_pad;
     const float f = c < cols ? src[row * cols + c] : 0.0f;
@@ -141,36 +150,6 @@ struct GiArgs {
   const int32_t* ids;
   int L, r;
 };
-
-// The distinct adapters of a tile's tokens in order of first use: s_ids[t]
-// for t < BM and s_list; returns their number.  Every thread of the block
-// calls it; BM <= 256 <= threads.
-__device__ __forceinline__ int tile_adapters(const int32_t* ids, int64_t m0, int M, int BM, int L, int* s_ids,
-                                             int* s_list, int* s_cnt) {
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int id = t < BM && m0 + t < M ? adapter_of(ids, m0 + t, L) : -1;
-  if (t < BM) s_ids[t] = id;
-  __syncthreads();
-  const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
-  bool first = id >= 0 && lane == __ffs(same) - 1;
-  if (first)
-    for (int j = 0; j < 32 * warp; ++j)
-      if (s_ids[j] == id) {
-        first = false;
-        break;
-      }
-  const unsigned firsts = __ballot_sync(0xFFFFFFFFu, first);
-  if (lane == 0 && warp < 8) s_cnt[warp] = __popc(firsts);
-  __syncthreads();
-  int before = 0, total = 0;
-  for (int w = 0; w < 8; ++w) {
-    if (w < warp) before += s_cnt[w];
-    total += s_cnt[w];
-  }
-  if (first) s_list[before + __popc(firsts & ((1u << lane) - 1))] = id;
-  __syncthreads();
-  return total;
-}
 
 // Sixteen bf16 of a row of the factor in the column order of the expanded
 // weights (pairs (i, i + 8)); zero past `left`.
@@ -244,12 +223,16 @@ __global__ void __launch_bounds__(kGiThreads, 1)
     mbar_init(drain, 1);
     *abort_flag = 0;
     mbar_init_fence();
-    for (int i = 0; i < p_first; ++i) issue_p(i);
-    for (int i = 0; i < a_first; ++i) issue_a(i);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 256 * H);
     tmem_relinquish();
+  }
+  pdl_wait();
+  if (threadIdx.x == 0) {
+    pdl_trigger();
+    for (int i = 0; i < p_first; ++i) issue_p(i);
+    for (int i = 0; i < a_first; ++i) issue_a(i);
   }
   int nadapt = 0, esteps = 0;  // adapters of the tile, steps of 64 entries for each
   if (a.v) {

@@ -72,30 +72,40 @@ struct Rows {
   int planes;
 };
 
-inline bl_status pad_rows(const void* src, int64_t rows, int64_t bytes, Scratch* ws, Rows* out, int sms,
-                          cudaStream_t s) {
+// Up to two copies, made by one launch.
+struct Pads {
+  bl::PadJob job[2] = {};
+  int n = 0;
+};
+
+inline void pad_rows(const void* src, int64_t rows, int64_t bytes, int64_t multiple, Scratch* ws, Rows* out, Pads* pads) {
   *out = {src, bytes, 1};
-  if (bytes % 16 == 0) return BL_OK;
-  out->stride = round_up(bytes, 16);
+  if (bytes % multiple == 0) return;
+  out->stride = round_up(bytes, multiple);
   void* dst = ws->take(static_cast<size_t>(rows * out->stride));
   out->p = dst;
-  if (!ws->base || rows == 0) return BL_OK;
-  bl::k_pad_rows<<<grid_for(rows * (out->stride / 16), 256, sms), 256, 0, s>>>(
-      static_cast<const uint8_t*>(src), rows, bytes, out->stride, static_cast<uint8_t*>(dst));
-  return launch_status();
+  pads->job[pads->n++] = {static_cast<const uint8_t*>(src), rows, bytes, out->stride, static_cast<uint8_t*>(dst)};
+}
+
+inline bl_status run_pads(const Pads& pads, int sms, cudaStream_t s) {
+  if (!pads.n) return BL_OK;
+  const int64_t n = pads.job[0].rows * (pads.job[0].stride / 16) + pads.job[1].rows * (pads.job[1].stride / 16);
+  return launch_pdl(bl::k_pad_rows, dim3(grid_for(n, 256, sms)), dim3(256), 0, s, pads.job[0], pads.job[1]);
 }
 
 // dy as bf16 planes: one, or three of an fp32 dy.
-inline bl_status dy_rows(const void* dy, bl_dtype dydt, int64_t M, int64_t N, Scratch* ws, Rows* out, int sms,
-                         cudaStream_t s) {
-  if (dydt == BL_BF16) return pad_rows(dy, M, 2 * N, ws, out, sms, s);
+inline bl_status dy_rows(const void* dy, bl_dtype dydt, int64_t M, int64_t N, Scratch* ws, Rows* out, Pads* pads,
+                         int sms, cudaStream_t s) {
+  if (dydt == BL_BF16) {
+    pad_rows(dy, M, 2 * N, 16, ws, out, pads);
+    return BL_OK;
+  }
   const int64_t cols = round_up(N, 8);
   void* dst = ws->take(static_cast<size_t>(3 * M * cols * 2));
   *out = {dst, 2 * cols, 3};
   if (!ws->base || M == 0) return BL_OK;
-  bl::k_split_planes<<<grid_for(M * cols, 256, sms), 256, 0, s>>>(static_cast<const float*>(dy), M, N, cols,
-                                                                   static_cast<__nv_bfloat16*>(dst));
-  return launch_status();
+  return launch_pdl(bl::k_split_planes, dim3(grid_for(M * cols, 256, sms)), dim3(256), 0, s,
+                    static_cast<const float*>(dy), M, N, cols, static_cast<__nv_bfloat16*>(dst));
 }
 
 // Whether rows of `cols` values of type dt take 16-byte stores.
@@ -109,16 +119,18 @@ bl_status launch_gi(const CUtensorMap& tdy, const CUtensorMap& tw, const bl::GiA
   if (!ensure_smem(kern, smem, done)) return BL_ERR_CUDA;
   const int64_t tiles = ((a.K + bl::kGiBN - 1) / bl::kGiBN) * ((int64_t{a.M} + 128 * H - 1) / (128 * H));
   if (tiles > INT32_MAX) return BL_ERR_UNSUPPORTED;
-  kern<<<static_cast<unsigned>(tiles), bl::kGiThreads, smem, s>>>(tdy, tw, a);
-  return launch_status();
+  return launch_pdl(kern, dim3(static_cast<unsigned>(tiles)), dim3(bl::kGiThreads), smem, s, tdy, tw, a);
 }
 
 // dx = gamma dy W~ (+ v A where a.v is given); the operands' copies come out of ws.
-bl_status run_grad_input(const Rows& dy, const uint8_t* packed, bl_dtype dxdt, bl::GiArgs a, Scratch* ws, int sms,
-                         cudaStream_t s) {
-  Rows w;
-  bl_status st = pad_rows(packed, a.N, (a.K + 3) / 4, ws, &w, sms, s);
+bl_status run_grad_input(const void* dyp, bl_dtype dydt, const uint8_t* packed, bl_dtype dxdt, bl::GiArgs a,
+                         Scratch* ws, int sms, cudaStream_t s) {
+  Rows dy, w;
+  Pads pads;
+  bl_status st = dy_rows(dyp, dydt, a.M, a.N, ws, &dy, &pads, sms, s);
   if (st != BL_OK) return st;
+  pad_rows(packed, a.N, (a.K + 3) / 4, 16, ws, &w, &pads);
+  if ((st = run_pads(pads, sms, s)) != BL_OK) return st;
   const int H = a.M > 128 ? 2 : 1;
   CUtensorMap tdy, tw;
   if (!make_tmap(&tdy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy.p, a.N, a.M, dy.planes, dy.stride, bl::kGiBK, 128 * H,
@@ -192,23 +204,151 @@ struct AdapterSet {
   int L, r;
 };
 
-template <typename DyT>
-bl_status launch_adapters_grad(const void* dy, const int8_t* xq, const float* eta, int64_t M, int64_t K,
-                               int64_t N, const AdapterSet& ad, void* dA, void* dB, bl_dtype dabdt, float* u,
-                               float* v, int sms, cudaStream_t s) {
-  const auto* d = static_cast<const DyT*>(dy);
-  bl::k_adapter_v<DyT><<<grid_for(M * ad.r, 8, sms), 256, 0, s>>>(d, M, N, ad.B, ad.scale, ad.ids, ad.L, ad.r, v);
-  if (!dA) return launch_status();
-  bl::k_adapter_u<<<grid_for(M * ad.r, 8, sms), 256, 0, s>>>(xq, eta, M, K, ad.A, ad.scale, ad.ids, ad.L, ad.r, u);
-  const unsigned ga = grid_for(int64_t{1} * ad.L * ad.r * K, 256, sms), gb = grid_for(int64_t{1} * ad.L * ad.r * N, 256, sms);
-  if (dabdt == BL_F32) {
-    bl::k_adapter_da<float><<<ga, 256, 0, s>>>(v, xq, eta, M, K, ad.ids, ad.L, ad.r, dA);
-    bl::k_adapter_db<DyT, float><<<gb, 256, 0, s>>>(d, u, M, N, ad.ids, ad.L, ad.r, dB);
-  } else {
-    bl::k_adapter_da<__nv_bfloat16><<<ga, 256, 0, s>>>(v, xq, eta, M, K, ad.ids, ad.L, ad.r, dA);
-    bl::k_adapter_db<DyT, __nv_bfloat16><<<gb, 256, 0, s>>>(d, u, M, N, ad.ids, ad.L, ad.r, dB);
+// u of up to 16 tokens (k_adapter_u): rows of x~ (or of x, quantised there)
+// and of A in 16-byte pieces, K within a CTA's registers.
+inline bool few_tokens_u(int64_t M, int64_t K) {
+  return M <= 16 && K % 8 == 0 && K <= 8 * bl::kAuChunks * bl::kAuThreads;
+}
+
+bl_status launch_u_few(const void* x, int8_t* xq, float* eta, int32_t* xsum, int64_t M, int64_t K, const AdapterSet& ad,
+                       float* u, int sms, cudaStream_t s) {
+  // rank indices per CTA: one while the CTAs fit on the GPU about at once
+  // (eight of 256 threads an SM), more where every CTA would read its token
+  // again for little work
+  const int64_t group = (M * ad.r + sms * 8 - 1) / (sms * 8);
+  const dim3 grid(static_cast<unsigned>((ad.r + group - 1) / group), static_cast<unsigned>(M));
+  auto kern = x ? bl::k_adapter_u<true> : bl::k_adapter_u<false>;
+  return launch_pdl(kern, grid, dim3(bl::kAuThreads), 0, s, static_cast<const __nv_bfloat16*>(x), xq, eta, xsum,
+                    static_cast<int>(K), ad.A, ad.scale, ad.ids, ad.L, ad.r, static_cast<int>(group), u);
+}
+
+template <typename DyT, int RT>
+bl_status launch_uv_rt(const bl::UvArgs& g, int sides, int64_t steps, int sms, cudaStream_t s) {
+  const int64_t tiles = (g.M + 16 * RT - 1) / (16 * RT);
+  // CTAs of a cluster along the contraction: as many as the GPU has room for
+  // (four of these CTAs an SM), no less than a step for each of their warps
+  int cs = 8;
+  while (cs > 1 && (tiles * sides * cs > 8 * sms || 4 * cs > steps + 3)) cs /= 2;
+  if (tiles > INT32_MAX) return BL_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(sides), static_cast<unsigned>(cs));
+  return launch_pdl_cluster(bl::k_adapter_uv<DyT, RT>, grid, dim3(bl::kUvThreads), 0, s, static_cast<unsigned>(cs), g);
+}
+
+// u (where out_u is given) and v (out_v) of any number of tokens.
+bl_status launch_uv(const void* dy, bl_dtype dydt, const int8_t* xq, const float* eta, int64_t M, int64_t K, int64_t N,
+                    const AdapterSet& ad, float* out_u, float* out_v, int sms, cudaStream_t s) {
+  bl::UvArgs g = {};
+  g.scale = ad.scale; g.ids = ad.ids; g.M = M; g.L = ad.L; g.r = ad.r;
+  int n = 0;
+  if (out_v) g.side[n++] = {1, dy, N, ad.B, nullptr, out_v, N % 4 == 0 ? 1 : 0};
+  if (out_u) g.side[n++] = {0, xq, K, ad.A, eta, out_u, K % 16 == 0 ? 1 : 0};
+  int64_t steps = out_v ? (N + 63) / 64 : 0;
+  if (out_u && (K + 63) / 64 > steps) steps = (K + 63) / 64;
+  if (out_v && dydt == BL_F32) return launch_uv_rt<float, 1>(g, n, steps, sms, s);
+  // 64 tokens a CTA read a factor a quarter as often as 16, which fill the
+  // GPU sooner: from 512 tokens on
+  return M > 512 ? launch_uv_rt<__nv_bfloat16, 4>(g, n, steps, sms, s) : launch_uv_rt<__nv_bfloat16, 1>(g, n, steps, sms, s);
+}
+
+template <typename DyT, typename OutT, int JT>
+bl_status launch_dab_jt(const bl::DabArgs& g, dim3 grid, cudaStream_t s) {
+  static int done[kMaxDevices] = {0};
+  auto kern = bl::k_adapter_dab<DyT, OutT, JT>;
+  constexpr int parts = sizeof(OutT) == 4 ? 3 : 2, xparts = sizeof(DyT) == 4 ? 3 : 1;
+  if (!ensure_smem(kern, bl::dab_smem(16 * JT, parts, xparts), done)) return BL_ERR_CUDA;
+  return launch_pdl_cluster(kern, grid, dim3(bl::kDabThreads), bl::dab_smem(g.r, parts, xparts), s, grid.z, g);
+}
+
+template <typename DyT, typename OutT>
+bl_status launch_dab(const void* dy, const int8_t* xq, const float* eta, int64_t M, int64_t K, int64_t N,
+                     const AdapterSet& ad, const float* u, const float* v, void* dA, void* dB, int sms, cudaStream_t s) {
+  const int64_t sa = (K + bl::kDabCols - 1) / bl::kDabCols, sb = (N + bl::kDabCols - 1) / bl::kDabCols;
+  bl::DabArgs g = {};
+  g.a = {xq, K, v, dA, K % 16 == 0 ? 1 : 0};
+  g.b = {dy, N, u, dB, N % 8 == 0 ? 1 : 0};
+  g.eta = eta; g.ids = ad.ids; g.M = M; g.r = ad.r; g.slabs_a = static_cast<unsigned>(sa);
+  // CTAs of a cluster along the tokens: while there are fewer than four CTAs
+  // an SM, and two chunks of tokens for each
+  int cs = 1;
+  while (cs < 8 && (sa + sb) * ad.L * cs < 4 * sms && M >= 4 * bl::kDabTokens * cs) cs *= 2;
+  const dim3 grid(static_cast<unsigned>(sa + sb), static_cast<unsigned>(ad.L), static_cast<unsigned>(cs));
+  if (ad.r <= 16) return launch_dab_jt<DyT, OutT, 1>(g, grid, s);
+  if (ad.r <= 32) return launch_dab_jt<DyT, OutT, 2>(g, grid, s);
+  if (ad.r <= 64) return launch_dab_jt<DyT, OutT, 4>(g, grid, s);
+  return launch_dab_jt<DyT, OutT, 8>(g, grid, s);
+}
+
+// Scratch of the forward pass: u, then the operands' copies where K is not a
+// multiple of 64 (rows of x~ padded with zeros, which meet any code).
+struct FaScratch {
+  float* u;
+  Rows x, w;
+  Pads pads;
+};
+
+inline void fa_scratch(const int8_t* xq, const uint8_t* packed, int64_t M, int64_t K, int64_t N, int64_t r, Scratch* ws,
+                       FaScratch* f) {
+  f->u = static_cast<float*>(ws->take(static_cast<size_t>(M * r * 4)));
+  if (K % 64 == 0) {
+    f->x = {xq, K, 1};
+    f->w = {packed, K / 4, 1};
+    return;
   }
-  return launch_status();
+  const int64_t kp = round_up(K, 64);
+  auto* x = static_cast<uint8_t*>(ws->take(static_cast<size_t>(M * kp)));
+  auto* w = static_cast<uint8_t*>(ws->take(static_cast<size_t>(N * (kp / 4))));
+  f->x = {x, kp, 1};
+  f->w = {w, kp / 4, 1};
+  f->pads.job[0] = {reinterpret_cast<const uint8_t*>(xq), M, K, kp, x};
+  f->pads.job[1] = {packed, N, (K + 3) / 4, kp / 4, w};
+  f->pads.n = 2;
+}
+
+// The projection with adapters, u given in f.
+bl_status run_forward_adapters(const FaScratch& f, const float* eta, const int32_t* xsum, int64_t M, const float* gamma,
+                               int64_t N, const AdapterSet& ad, void* y, bl_dtype ydt, unsigned flags, int sms,
+                               cudaStream_t s) {
+  const bl_status st = run_pads(f.pads, sms, s);
+  if (st != BL_OK) return st;
+  if (f.pads.n) flags &= ~static_cast<unsigned>(BL_FLAG_WEIGHTS_STATIC);  // the copy is new
+  const bl::AdapterAdd add = {f.u, ad.B, ad.ids, ad.L, ad.r};
+  return forward_impl(static_cast<const int8_t*>(f.x.p), eta, xsum, M, f.x.stride, static_cast<const uint8_t*>(f.w.p),
+                      gamma, N, y, ydt, nullptr, BL_PATH_AUTO, flags, s, add);
+}
+
+// Scratch of linear_adapters: the quantised tokens, then the forward pass's.
+struct LaScratch {
+  int8_t* xq;
+  float* eta;
+  int32_t* xsum;
+};
+
+inline void la_scratch(int64_t M, int64_t K, Scratch* ws, LaScratch* q) {
+  q->xq = static_cast<int8_t*>(ws->take(static_cast<size_t>(M * K)));
+  q->eta = static_cast<float*>(ws->take(static_cast<size_t>(M * 4)));
+  q->xsum = static_cast<int32_t*>(ws->take(static_cast<size_t>(M * 4)));
+}
+
+// Checks that forward_adapters and linear_adapters share, in the order of
+// the other calls: arguments, sizes, then (after M = 0) the rest.
+bl_status fa_check(int64_t M, int64_t N, int64_t K, int64_t L, int64_t r, const uint8_t* packed, const float* gamma,
+                   const void* A, const void* B, const float* scale, bl_dtype ydt) {
+  const bl_status st = train_sizes(M, N, K), sa = adapter_sizes(L, r, N, K);
+  if (st == BL_ERR_INVALID_ARG || sa == BL_ERR_INVALID_ARG) return BL_ERR_INVALID_ARG;
+  if (!dtype_ok(ydt) || !packed || !gamma || !A || !B || !scale) return BL_ERR_INVALID_ARG;
+  if (st != BL_OK || sa != BL_OK || 127 * round_up(K, 64) >= (int64_t{1} << 31)) return BL_ERR_UNSUPPORTED;
+  return BL_OK;
+}
+
+inline bool adapters_aligned(const uint8_t* packed, const float* gamma, const void* A, const void* B, const float* scale,
+                             const int32_t* ids) {
+  return aligned(packed, 16) && aligned(A, 16) && aligned(B, 16) && aligned(gamma, 4) && aligned(scale, 4) &&
+         aligned(ids, 4);
+}
+
+inline AdapterSet adapter_set(const void* A, const void* B, const float* scale, const int32_t* ids, int64_t L, int64_t r) {
+  return {static_cast<const __nv_bfloat16*>(A), static_cast<const __nv_bfloat16*>(B), scale, ids, static_cast<int>(L),
+          static_cast<int>(r)};
 }
 
 }  // namespace
@@ -219,8 +359,9 @@ size_t bitlinear_grad_input_workspace_bytes(int64_t M, int64_t N, int64_t K, bl_
   if (train_sizes(M, N, K) != BL_OK || !dtype_ok(dydt)) return 0;
   Scratch ws(nullptr);
   Rows r;
-  dy_rows(nullptr, dydt, M, N, &ws, &r, 1, nullptr);
-  pad_rows(nullptr, N, (K + 3) / 4, &ws, &r, 1, nullptr);
+  Pads pads;
+  dy_rows(nullptr, dydt, M, N, &ws, &r, &pads, 1, nullptr);
+  pad_rows(nullptr, N, (K + 3) / 4, 16, &ws, &r, &pads);
   return ws.used;
 }
 
@@ -240,11 +381,9 @@ bl_status bitlinear_grad_input(const void* dy, bl_dtype dydt, int64_t M, int64_t
   if ((st = device_info(&sms)) != BL_OK) return st;
   const cudaStream_t s = as_stream(stream);
   Scratch ws(workspace);
-  Rows rdy;
-  if ((st = dy_rows(dy, dydt, M, N, &ws, &rdy, sms, s)) != BL_OK) return st;
   bl::GiArgs a = {};
   a.gamma = gamma; a.M = static_cast<int>(M); a.N = static_cast<int>(N); a.K = static_cast<int>(K); a.dx = dx;
-  return run_grad_input(rdy, packed, dxdt, a, &ws, sms, s);
+  return run_grad_input(dy, dydt, packed, dxdt, a, &ws, sms, s);
 }
 
 size_t bitlinear_grad_weight_workspace_bytes(int64_t M, int64_t N, int64_t K, bl_dtype dydt, bl_dtype dwdt) {
@@ -324,8 +463,8 @@ bl_status bitlinear_rmsnorm_grad(const void* dn, bl_dtype dndt, const int8_t* xq
 size_t bitlinear_forward_adapters_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r) {
   if (train_sizes(M, N, K) != BL_OK || adapter_sizes(L, r, N, K) != BL_OK) return 0;
   Scratch ws(nullptr);
-  ws.take(static_cast<size_t>(M) * r * 4);  // u
-  ws.take(static_cast<size_t>(M) * N * 4);  // the projection in fp32
+  FaScratch f;
+  fa_scratch(nullptr, nullptr, M, K, N, r, &ws, &f);
   return ws.used;
 }
 
@@ -334,37 +473,82 @@ bl_status bitlinear_forward_adapters(const int8_t* xq, const float* eta, const i
                                      const void* A, const void* B, const float* scale, const int32_t* ids,
                                      int64_t L, int64_t r, void* y, bl_dtype ydt, void* workspace,
                                      size_t workspace_bytes, unsigned flags, void* stream) {
-  bl_status st = train_sizes(M, N, K), sa = adapter_sizes(L, r, N, K);
-  if (st == BL_ERR_INVALID_ARG || sa == BL_ERR_INVALID_ARG) return BL_ERR_INVALID_ARG;
-  if (!dtype_ok(ydt) || !packed || !gamma || !A || !B || !scale) return BL_ERR_INVALID_ARG;
-  if (st != BL_OK || sa != BL_OK) return BL_ERR_UNSUPPORTED;
-  if (M == 0) return BL_OK;
+  bl_status st = fa_check(M, N, K, L, r, packed, gamma, A, B, scale, ydt);
+  if (st != BL_OK || M == 0) return st;
   const size_t need = bitlinear_forward_adapters_workspace_bytes(M, K, N, L, r);
   if (!xq || !eta || !xsum || !ids || !y || !workspace || workspace_bytes < need) return BL_ERR_INVALID_ARG;
-  if (!aligned(xq, 16) || !aligned(packed, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(y, 16) ||
-      !aligned(eta, 4) || !aligned(xsum, 4) || !aligned(gamma, 4) || !aligned(scale, 4) || !aligned(ids, 4) ||
+  if (!adapters_aligned(packed, gamma, A, B, scale, ids) || !aligned(xq, 16) || !aligned(y, 16) || !aligned(eta, 4) ||
+      !aligned(xsum, 4) || !aligned(workspace, 256))
+    return BL_ERR_ALIGNMENT;
+  int sms = 148;
+  if ((st = device_info(&sms)) != BL_OK) return st;
+  const cudaStream_t s = as_stream(stream);
+  Scratch ws(workspace);
+  FaScratch f;
+  fa_scratch(xq, packed, M, K, N, r, &ws, &f);
+  const AdapterSet ad = adapter_set(A, B, scale, ids, L, r);
+  st = few_tokens_u(M, K) ? launch_u_few(nullptr, const_cast<int8_t*>(xq), const_cast<float*>(eta), nullptr, M, K, ad, f.u, sms, s)
+                          : launch_uv(nullptr, BL_BF16, xq, eta, M, K, N, ad, f.u, nullptr, sms, s);
+  return st == BL_OK ? run_forward_adapters(f, eta, xsum, M, gamma, N, ad, y, ydt, flags, sms, s) : st;
+}
+
+size_t bitlinear_linear_adapters_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r) {
+  const size_t fwd = bitlinear_forward_adapters_workspace_bytes(M, K, N, L, r);
+  if (!fwd) return 0;
+  Scratch ws(nullptr);
+  LaScratch q;
+  la_scratch(M, K, &ws, &q);
+  return ws.used + fwd;
+}
+
+bl_status bitlinear_linear_adapters(const void* x, bl_dtype xdt, int64_t M, int64_t K, const uint8_t* packed,
+                                    const float* gamma, int64_t N, const void* A, const void* B,
+                                    const float* scale, const int32_t* ids, int64_t L, int64_t r, void* y,
+                                    bl_dtype ydt, void* workspace, size_t workspace_bytes, unsigned flags,
+                                    void* stream) {
+  bl_status st = fa_check(M, N, K, L, r, packed, gamma, A, B, scale, ydt);
+  if (st == BL_ERR_INVALID_ARG || !dtype_ok(xdt)) return BL_ERR_INVALID_ARG;
+  const bool norm = (flags & BL_FLAG_RMSNORM) != 0;
+  if (st != BL_OK || (norm && xdt != BL_BF16)) return BL_ERR_UNSUPPORTED;
+  if (M == 0) return BL_OK;
+  const size_t need = bitlinear_linear_adapters_workspace_bytes(M, K, N, L, r);
+  if (!x || !ids || !y || !workspace || workspace_bytes < need) return BL_ERR_INVALID_ARG;
+  if (!adapters_aligned(packed, gamma, A, B, scale, ids) || !aligned(x, dtype_bytes(xdt)) || !aligned(y, 16) ||
       !aligned(workspace, 256))
     return BL_ERR_ALIGNMENT;
   int sms = 148;
   if ((st = device_info(&sms)) != BL_OK) return st;
   const cudaStream_t s = as_stream(stream);
   Scratch ws(workspace);
-  float* u = static_cast<float*>(ws.take(static_cast<size_t>(M) * r * 4));
-  float* base = static_cast<float*>(ws.take(static_cast<size_t>(M) * N * 4));
-  const auto* a = static_cast<const __nv_bfloat16*>(A);
-  const auto* b = static_cast<const __nv_bfloat16*>(B);
-  if ((st = forward_impl(xq, eta, xsum, M, K, packed, gamma, N, base, BL_F32, nullptr, BL_PATH_AUTO, flags,
-                         stream)) != BL_OK)
-    return st;
-  bl::k_adapter_u<<<grid_for(M * r, 8, sms), 256, 0, s>>>(xq, eta, M, K, a, scale, ids, static_cast<int>(L),
-                                                          static_cast<int>(r), u);
-  const unsigned g = grid_for(M * N, 256, sms);
-  if (ydt == BL_F32)
-    bl::k_adapter_add<float><<<g, 256, 0, s>>>(base, M, N, u, b, r, 1, ids, static_cast<int>(L), static_cast<int>(r), y);
-  else
-    bl::k_adapter_add<__nv_bfloat16><<<g, 256, 0, s>>>(base, M, N, u, b, r, 1, ids, static_cast<int>(L),
-                                                       static_cast<int>(r), y);
-  return launch_status();
+  LaScratch q;
+  la_scratch(M, K, &ws, &q);
+  FaScratch f;
+  fa_scratch(q.xq, packed, M, K, N, r, &ws, &f);
+  const AdapterSet ad = adapter_set(A, B, scale, ids, L, r);
+  if (!norm && xdt == BL_BF16 && aligned(x, 16) && few_tokens_u(M, K)) {
+    RegGeom rg;
+    const bool one = M == 1 && g_decode_reg.load(std::memory_order_relaxed) != 0 && reg_decode_geometry(K, N, sms, &rg);
+    // one token: the accumulate kernel quantises again, x~ need not be written
+    if ((st = launch_u_few(x, one ? nullptr : q.xq, q.eta, q.xsum, M, K, ad, f.u, sms, s)) != BL_OK) return st;
+    if (one) {
+      bl::RegDecodeArgs a = {};
+      a.x = static_cast<const __nv_bfloat16*>(x);
+      a.K = static_cast<int>(K); a.N = static_cast<int>(N);
+      a.packed = packed; a.gamma = gamma; a.y = y; a.y_bf16 = ydt == BL_BF16 ? 1 : 0;
+      a.rows_per_cta = rg.rows_per_cta;
+      a.weights_static = (flags & BL_FLAG_WEIGHTS_STATIC) ? 1 : 0;
+      a.ad = {f.u, ad.B, ids, ad.L, ad.r};
+      return launch_decode_reg(a, rg, s);
+    }
+  } else {
+    st = norm ? rmsnorm_quant_impl(x, xdt, M, K, q.xq, q.eta, q.xsum, nullptr, stream)
+              : bitlinear_quant_act(x, xdt, M, K, q.xq, q.eta, q.xsum, stream);
+    if (st != BL_OK) return st;
+    st = few_tokens_u(M, K) ? launch_u_few(nullptr, q.xq, q.eta, q.xsum, M, K, ad, f.u, sms, s)
+                            : launch_uv(nullptr, BL_BF16, q.xq, q.eta, M, K, N, ad, f.u, nullptr, sms, s);
+    if (st != BL_OK) return st;
+  }
+  return run_forward_adapters(f, q.eta, q.xsum, M, gamma, N, ad, y, ydt, flags, sms, s);
 }
 
 size_t bitlinear_adapters_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t r,
@@ -373,10 +557,7 @@ size_t bitlinear_adapters_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, 
   Scratch ws(nullptr);
   ws.take(static_cast<size_t>(M) * r * 4);  // u
   ws.take(static_cast<size_t>(M) * r * 4);  // v
-  Rows rows;
-  dy_rows(nullptr, dydt, M, N, &ws, &rows, 1, nullptr);
-  pad_rows(nullptr, N, (K + 3) / 4, &ws, &rows, 1, nullptr);
-  return ws.used;
+  return ws.used + bitlinear_grad_input_workspace_bytes(M, N, K, dydt);
 }
 
 bl_status bitlinear_adapters_grad(const void* dy, bl_dtype dydt, const int8_t* xq, const float* eta, int64_t M,
@@ -393,9 +574,8 @@ bl_status bitlinear_adapters_grad(const void* dy, bl_dtype dydt, const int8_t* x
   const size_t need = bitlinear_adapters_grad_workspace_bytes(M, N, K, L, r, dydt);
   if (M > 0 && (!dy || !xq || !eta || !ids || !workspace)) return BL_ERR_INVALID_ARG;
   if (workspace_bytes < need) return BL_ERR_INVALID_ARG;
-  if (!aligned(dy, 16) || !aligned(xq, 16) || !aligned(packed, 16) || !aligned(A, 16) || !aligned(B, 16) ||
-      !aligned(dx, 16) || !aligned(dA, 16) || !aligned(dB, 16) || !aligned(eta, 4) || !aligned(gamma, 4) ||
-      !aligned(scale, 4) || !aligned(ids, 4) || !aligned(workspace, 256))
+  if (!adapters_aligned(packed, gamma, A, B, scale, ids) || !aligned(dy, 16) || !aligned(xq, 16) ||
+      !aligned(dx, 16) || !aligned(dA, 16) || !aligned(dB, 16) || !aligned(eta, 4) || !aligned(workspace, 256))
     return BL_ERR_ALIGNMENT;
   int sms = 148;
   if ((st = device_info(&sms)) != BL_OK) return st;
@@ -403,18 +583,22 @@ bl_status bitlinear_adapters_grad(const void* dy, bl_dtype dydt, const int8_t* x
   Scratch ws(workspace);
   float* u = static_cast<float*>(ws.take(static_cast<size_t>(M) * r * 4));
   float* v = static_cast<float*>(ws.take(static_cast<size_t>(M) * r * 4));
-  const AdapterSet ad = {static_cast<const __nv_bfloat16*>(A), static_cast<const __nv_bfloat16*>(B), scale, ids,
-                         static_cast<int>(L), static_cast<int>(r)};
-  st = dydt == BL_F32
-           ? launch_adapters_grad<float>(dy, xq, eta, M, K, N, ad, dA, dB, dabdt, u, v, sms, s)
-           : launch_adapters_grad<__nv_bfloat16>(dy, xq, eta, M, K, N, ad, dA, dB, dabdt, u, v, sms, s);
-  if (st != BL_OK || !dx || M == 0) return st;
-  Rows rdy;
-  if ((st = dy_rows(dy, dydt, M, N, &ws, &rdy, sms, s)) != BL_OK) return st;
+  const AdapterSet ad = adapter_set(A, B, scale, ids, L, r);
+  if (M > 0 && (st = launch_uv(dy, dydt, xq, eta, M, K, N, ad, dA ? u : nullptr, v, sms, s)) != BL_OK) return st;
+  if (dA) {  // no tokens: zeros
+    if (dydt == BL_F32)
+      st = dabdt == BL_F32 ? launch_dab<float, float>(dy, xq, eta, M, K, N, ad, u, v, dA, dB, sms, s)
+                           : launch_dab<float, __nv_bfloat16>(dy, xq, eta, M, K, N, ad, u, v, dA, dB, sms, s);
+    else
+      st = dabdt == BL_F32 ? launch_dab<__nv_bfloat16, float>(dy, xq, eta, M, K, N, ad, u, v, dA, dB, sms, s)
+                           : launch_dab<__nv_bfloat16, __nv_bfloat16>(dy, xq, eta, M, K, N, ad, u, v, dA, dB, sms, s);
+    if (st != BL_OK) return st;
+  }
+  if (!dx || M == 0) return BL_OK;
   bl::GiArgs g = {};
   g.gamma = gamma; g.M = static_cast<int>(M); g.N = static_cast<int>(N); g.K = static_cast<int>(K); g.dx = dx;
   g.v = v; g.A = ad.A; g.ids = ids; g.L = ad.L; g.r = ad.r;
-  return run_grad_input(rdy, packed, dxdt, g, &ws, sms, s);
+  return run_grad_input(dy, dydt, packed, dxdt, g, &ws, sms, s);
 }
 
 }  // extern "C"

@@ -52,33 +52,46 @@ __device__ __noinline__ float adapter_add(const float* u, const __nv_bfloat16* B
 }
 
 // The distinct adapters of a tile's tokens in order of first use: s_ids[t]
-// for t < BM and s_list; returns their number.  Every thread of the block
-// calls it; BM <= 256 and BM <= threads.
+// for t < BM and s_list; returns their number.  Called by whole warps, the
+// threads t = 0 .. (BM at least) that `sync` brings together; BM <= 256;
+// s_cnt has 8 entries.
+template <typename Sync>
 __device__ __forceinline__ int tile_adapters(const int32_t* ids, int64_t m0, int64_t M, int BM, int L, int* s_ids,
-                                             int* s_list, int* s_cnt) {
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, groups = (BM + 31) >> 5;
+                                             int* s_list, int* s_cnt, int t, Sync sync) {
+  const int lane = t & 31, warp = t >> 5, groups = (BM + 31) >> 5;
   const int id = t < BM && m0 + t < M ? adapter_of(ids, m0 + t, L) : -1;
   if (t < BM) s_ids[t] = id;
-  __syncthreads();
+  // each warp's distinct ones, then those that no warp before has
   const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
   bool first = id >= 0 && lane == __ffs(same) - 1;
-  if (first)
-    for (int j = 0; j < 32 * warp; ++j)
-      if (s_ids[j] == id) {
+  const unsigned below = (1u << lane) - 1;
+  unsigned firsts = __ballot_sync(0xFFFFFFFFu, first);
+  if (first) s_list[32 * warp + __popc(firsts & below)] = id;
+  if (lane == 0 && warp < groups) s_cnt[warp] = __popc(firsts);
+  sync();
+  for (int w = 0; first && w < warp; ++w)
+    for (int j = 0; j < s_cnt[w]; ++j)
+      if (s_list[32 * w + j] == id) {
         first = false;
         break;
       }
-  const unsigned firsts = __ballot_sync(0xFFFFFFFFu, first);
+  firsts = __ballot_sync(0xFFFFFFFFu, first);
+  sync();
   if (lane == 0 && warp < groups) s_cnt[warp] = __popc(firsts);
-  __syncthreads();
+  sync();
   int before = 0, total = 0;
   for (int w = 0; w < groups; ++w) {
     if (w < warp) before += s_cnt[w];
     total += s_cnt[w];
   }
-  if (first) s_list[before + __popc(firsts & ((1u << lane) - 1))] = id;
-  __syncthreads();
+  if (first) s_list[before + __popc(firsts & below)] = id;
+  sync();
   return total;
+}
+
+__device__ __forceinline__ int tile_adapters(const int32_t* ids, int64_t m0, int64_t M, int BM, int L, int* s_ids,
+                                             int* s_list, int* s_cnt) {
+  return tile_adapters(ids, m0, M, BM, L, s_ids, s_list, s_cnt, static_cast<int>(threadIdx.x), [] { __syncthreads(); });
 }
 
 // Part p of the bf16 values x0 + x1 + x2 that hold an fp32 (8 bits each, the

@@ -41,18 +41,6 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&d)[4], const void* 
                : "memory");
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-
-__device__ __forceinline__ uint32_t cluster_nctarank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-
 // The codes in bytes 0 and 2 of w as a bf16 pair: the low seven bits on 128
 // (one step of bf16 there is one), minus 128 or, for a negative code, 256.
 __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
@@ -243,6 +231,7 @@ struct UvArgs {
 };
 
 constexpr int kUvThreads = 128;
+constexpr int kUvRedPitch = 40;
 constexpr int kUvPitch = 40;  // bf16 of a staged row of B: 32 and 8 that spread the banks
 
 // The plain sum for one output, where a factor is not finite.
@@ -262,7 +251,7 @@ __device__ __noinline__ float uv_plain(const UvArgs& g, const UvSide& s, int64_t
 // their staged rows of B (64 x kUvPitch).
 template <typename XT, int RT>
 __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_t* smem, const int* s_ids,
-                                        const int* s_list, int nad, volatile int* s_bad) {
+                                        const int* s_list, int nad, volatile float* s_bad) {
   constexpr bool V = sizeof(XT) > 1;
   constexpr int T = 16 * RT, PX = sizeof(XT) == 4 ? 3 : 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, q = lane & 3;
@@ -370,28 +359,44 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
           } else {
             const __nv_bfloat16* f = s.F + (a * C + k0) * r + jb;
             __syncwarp();
-            if (bvec) {
-              for (int i = lane; i < 64 * nt; i += 32) {
-                const int n = i / nt, c = i - n * nt;
-                uint4 w = k0 + n < C ? __ldg(reinterpret_cast<const uint4*>(f + static_cast<int64_t>(n) * r) + c)
-                                     : make_uint4(0, 0, 0, 0);
-                if (nonfinite8(w)) {
-                  bad = true;
-                  w = make_uint4(0, 0, 0, 0);
-                }
-                *reinterpret_cast<uint4*>(stage + n * kUvPitch + 8 * c) = w;
+            if (bvec) {  // every load in flight at once
+              uint4 w[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const int i = lane + 32 * x, n = i / nt, c = i - n * nt;
+                w[x] = x < 2 * nt && k0 + n < C ? __ldg(reinterpret_cast<const uint4*>(f + static_cast<int64_t>(n) * r) + c)
+                                                : make_uint4(0, 0, 0, 0);
               }
-            } else {
-              const int cols = 8 * nt;
-              for (int i = lane; i < 64 * cols; i += 32) {
-                const int n = i / cols, j = i - n * cols;
-                uint16_t w = k0 + n < C && jb + j < r
-                                 ? __ldg(reinterpret_cast<const uint16_t*>(f) + static_cast<int64_t>(n) * r + j) : 0;
-                if (nonfinite2(w)) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                if (x >= 2 * nt) continue;
+                const int i = lane + 32 * x, n = i / nt, c = i - n * nt;
+                if (nonfinite8(w[x])) {
                   bad = true;
-                  w = 0;
+                  w[x] = make_uint4(0, 0, 0, 0);
                 }
-                reinterpret_cast<uint16_t*>(stage)[n * kUvPitch + j] = w;
+                *reinterpret_cast<uint4*>(stage + n * kUvPitch + 8 * c) = w[x];
+              }
+            } else {  // value by value, 16 in flight
+              const int cols = 8 * nt;
+#pragma unroll 1
+              for (int i0 = lane; i0 < 64 * cols; i0 += 512) {
+                uint16_t w[16];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                  const int i = i0 + 32 * x, n = i / cols, j = i - n * cols;
+                  w[x] = k0 + n < C && jb + j < r
+                             ? __ldg(reinterpret_cast<const uint16_t*>(f) + static_cast<int64_t>(n) * r + j) : 0;
+                }
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                  const int i = i0 + 32 * x, n = i / cols, j = i - n * cols;
+                  if (nonfinite2(w[x])) {
+                    bad = true;
+                    w[x] = 0;
+                  }
+                  reinterpret_cast<uint16_t*>(stage)[n * kUvPitch + j] = w[x];
+                }
               }
             }
             __syncwarp();
@@ -429,7 +434,7 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
         }
       }
     }
-    if (bad) *s_bad = 1;
+    if (bad) *s_bad = 1.0f;
     __syncthreads();  // the staged rows are read
 #pragma unroll
     for (int t = 0; t < RT; ++t)
@@ -437,24 +442,24 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
       for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2*>(red + (warp * T + 16 * t + 8 * h + gr) * 32 + 8 * n + 2 * q) =
+          *reinterpret_cast<float2*>(red + (warp * T + 16 * t + 8 * h + gr) * kUvRedPitch + 8 * n + 2 * q) =
               make_float2(acc[t][n][2 * h], acc[t][n][2 * h + 1]);
     __syncthreads();
-    for (int e = tid; e < T * 32; e += kUvThreads)
-      red[e] = __fadd_rn(__fadd_rn(red[e], red[T * 32 + e]), __fadd_rn(red[2 * T * 32 + e], red[3 * T * 32 + e]));
+    for (int e = tid; e < T * 32; e += kUvThreads) {
+      float* p = red + (e >> 5) * kUvRedPitch + (e & 31);
+      constexpr int kWarp = T * kUvRedPitch;
+      *p = __fadd_rn(__fadd_rn(p[0], p[kWarp]), __fadd_rn(p[2 * kWarp], p[3 * kWarp]));
+    }
     if (CS > 1) cluster_sync_all();
     else __syncthreads();
-    int any = *s_bad;
-    for (int c = 0; CS > 1 && c < CS; ++c) any |= __float_as_int(ld_cluster_f32(cluster_map(const_cast<int*>(s_bad), c)));
+    const bool any = (CS > 1 ? cluster_total(const_cast<float*>(s_bad), CS) : *s_bad) != 0.0f;
     for (int e = z * kUvThreads + tid; e < T * 32; e += CS * kUvThreads) {
       const int m = e >> 5, j = jb + (e & 31), a = s_ids[m];
       if (j >= r || m0 + m >= g.M) continue;
       float v = 0.0f;
       if (a >= 0) {
-        if (CS > 1)
-          for (int c = 0; c < CS; ++c) v = __fadd_rn(v, ld_cluster_f32(cluster_map(red + e, c)));
-        else
-          v = red[e];
+        const float* p = red + m * kUvRedPitch + (e & 31);
+        v = CS > 1 ? cluster_total(p, CS) : *p;
         if (any) v = uv_plain<typename std::conditional<V, XT, float>::type>(g, s, m0 + m, a, j);
         if constexpr (!V) v = __fmul_rn(v, div127_rn(s.eta[m0 + m]));
         v = __fmul_rn(v, g.scale[a]);
@@ -468,16 +473,16 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
 
 // Grid (tiles of 16 RT tokens, sides, CTAs of a cluster).
 template <typename DyT, int RT>
-__global__ void __launch_bounds__(kUvThreads, 2) k_adapter_uv(const __grid_constant__ UvArgs g) {
+__global__ void __launch_bounds__(kUvThreads, 3) k_adapter_uv(const __grid_constant__ UvArgs g) {
   constexpr int T = 16 * RT;
-  constexpr int kStage = 4 * 64 * kUvPitch * 2, kRed = 4 * T * 32 * 4;
+  constexpr int kStage = 4 * 64 * kUvPitch * 2, kRed = 4 * T * kUvRedPitch * 4;
   __shared__ __align__(16) uint8_t smem[kStage > kRed ? kStage : kRed];
   __shared__ int s_ids[T < 32 ? 32 : T], s_list[T], s_cnt[8];
-  __shared__ int s_bad;
+  __shared__ float s_bad;  // not zero: a factor is not finite
   pdl_wait();
   if (threadIdx.x == 0) {
     pdl_trigger();
-    s_bad = 0;
+    s_bad = 0.0f;
   }
   const UvSide& s = g.side[blockIdx.y];
   const int nad = tile_adapters(g.ids, static_cast<int64_t>(blockIdx.x) * T, g.M, T, g.L, s_ids, s_list, s_cnt);
@@ -545,7 +550,105 @@ __device__ __forceinline__ void dab_tile(const DabArgs& g, const DabSide& s, int
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[t][n][i] = 0.0f;
 
-  const int xt = tid >> 1, xh = tid & 1;  // this thread's token of a chunk and half of its 64 columns
+  // A thread takes one token of a chunk and half of its columns and rank
+  // indices: into registers, then (next chunk) into shared memory.
+  const int xt = tid >> 1, xh = tid & 1;
+  constexpr int kXRegs = 8 * static_cast<int>(sizeof(XT));  // 32 columns
+  constexpr int kCoefs = 8 * JT;
+  uint32_t xr[kXRegs];
+  float cf[kCoefs];
+  const bool cvec = (r & 3) == 0;
+  auto load = [&](const uint16_t* tok, int left, int64_t w0) {
+    const bool in = xt < left;
+    const int64_t m = w0 + (in ? tok[xt] : 0);
+    const XT* src = static_cast<const XT*>(s.x) + m * s.C + c0 + 32 * xh;
+    const int64_t cols = in ? s.C - c0 - 32 * xh : 0;
+    constexpr int kPer = 16 / static_cast<int>(sizeof(XT));  // values of a 16-byte piece
+    if (s.vec) {
+#pragma unroll
+      for (int i = 0; i < kXRegs / 4; ++i) {
+        const uint4 v = kPer * i < cols ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+        xr[4 * i] = v.x; xr[4 * i + 1] = v.y; xr[4 * i + 2] = v.z; xr[4 * i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kXRegs; ++i) {
+        if constexpr (sizeof(XT) == 4) {
+          xr[i] = i < cols ? __ldg(reinterpret_cast<const uint32_t*>(src) + i) : 0u;
+        } else if constexpr (sizeof(XT) == 2) {
+          const uint16_t* h = reinterpret_cast<const uint16_t*>(src) + 2 * i;
+          xr[i] = (2 * i < cols ? __ldg(h) : 0u) | (2 * i + 1 < cols ? static_cast<uint32_t>(__ldg(h + 1)) << 16 : 0u);
+        } else {
+          const uint8_t* h = reinterpret_cast<const uint8_t*>(src) + 4 * i;
+          xr[i] = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (4 * i + b < cols) xr[i] |= static_cast<uint32_t>(__ldg(h + b)) << (8 * b);
+        }
+      }
+    }
+    const float f = in && is_a ? div127_rn(__ldg(g.eta + m)) : 1.0f;
+    const float* cp = s.coef + m * r;
+#pragma unroll
+    for (int i = 0; i < kCoefs; i += 4) {
+      const int j = xh * (rows / 2) + i;  // rows / 2 <= kCoefs; what passes it is not stored
+      float4 v = make_float4(0, 0, 0, 0);
+      if (in && i < rows / 2) {
+        if (cvec) {
+          if (j < r) v = *reinterpret_cast<const float4*>(cp + j);
+        } else {
+          if (j < r) v.x = cp[j];
+          if (j + 1 < r) v.y = cp[j + 1];
+          if (j + 2 < r) v.z = cp[j + 2];
+          if (j + 3 < r) v.w = cp[j + 3];
+        }
+      }
+      cf[i] = __fmul_rn(v.x, f);
+      cf[i + 1] = __fmul_rn(v.y, f);
+      cf[i + 2] = __fmul_rn(v.z, f);
+      cf[i + 3] = __fmul_rn(v.w, f);
+    }
+  };
+  auto put = [&]() {
+    uint4* dst = reinterpret_cast<uint4*>(s_x + xt * kDabXPitch + 32 * xh);
+    if constexpr (sizeof(XT) == 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t e = codes_bf16(xr[2 * i + k]), d = codes_bf16(xr[2 * i + k] >> 8);  // codes 0, 2 and 1, 3
+          o[2 * k] = __byte_perm(e, d, 0x5410);
+          o[2 * k + 1] = __byte_perm(e, d, 0x7632);
+        }
+        dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    } else if constexpr (sizeof(XT) == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dst[i] = make_uint4(xr[4 * i], xr[4 * i + 1], xr[4 * i + 2], xr[4 * i + 3]);
+    } else {
+#pragma unroll
+      for (int p = 0; p < PX; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            o[k] = pack_bf16(bf16_part<PX>(__uint_as_float(xr[8 * i + 2 * k]), p),
+                             bf16_part<PX>(__uint_as_float(xr[8 * i + 2 * k + 1]), p));
+          dst[p * (kDabTokens * kDabXPitch / 8) + i] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kCoefs; i += 4) {
+      if (i >= rows / 2) continue;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        *reinterpret_cast<uint2*>(s_coef + (p * kDabTokens + xt) * cpitch + xh * (rows / 2) + i) =
+            make_uint2(pack_bf16(bf16_part<P>(cf[i], p), bf16_part<P>(cf[i + 1], p)),
+                       pack_bf16(bf16_part<P>(cf[i + 2], p), bf16_part<P>(cf[i + 3], p)));
+    }
+  };
   int chunk0 = 0;                         // chunks of the windows before, for the turns of a cluster's CTAs
   for (int64_t w0 = 0; w0 < g.M; w0 += kDabWindow) {
     // the window's tokens of this adapter, in order
@@ -580,67 +683,13 @@ __device__ __forceinline__ void dab_tile(const DabArgs& g, const DabSide& s, int
     }
     __syncthreads();
     const int chunks = (total + kDabTokens - 1) / kDabTokens;
-    for (int c = 0; c < chunks; ++c) {
-      if ((chunk0 + c) % CS != z) continue;
-      const int left = total - c * kDabTokens;
-      const uint16_t* tok = s_tok + c * kDabTokens;
-      // 32 columns of a token a thread
-      {
-        const bool in = xt < left;
-        const XT* src = static_cast<const XT*>(s.x) + (w0 + (in ? tok[xt] : 0)) * s.C + c0 + 32 * xh;
-        const int64_t cols = in ? s.C - c0 - 32 * xh : 0;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(s_x + xt * kDabXPitch + 32 * xh);
-        if constexpr (sizeof(XT) == 1) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t w[4] = {0, 0, 0, 0};
-            if (s.vec) {
-              if (16 * i < cols) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
-                w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-              }
-            } else {
-#pragma unroll
-              for (int b = 0; b < 16; ++b)
-                if (16 * i + b < cols) w[b >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(src[16 * i + b])) << (8 * (b & 3));
-            }
-            uint32_t o[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t e = codes_bf16(w[k]), d = codes_bf16(w[k] >> 8);  // codes 0, 2 and 1, 3
-              o[2 * k] = __byte_perm(e, d, 0x5410);
-              o[2 * k + 1] = __byte_perm(e, d, 0x7632);
-            }
-            reinterpret_cast<uint4*>(dst)[2 * i] = make_uint4(o[0], o[1], o[2], o[3]);
-            reinterpret_cast<uint4*>(dst)[2 * i + 1] = make_uint4(o[4], o[5], o[6], o[7]);
-          }
-        } else {
-#pragma unroll
-          for (int p = 0; p < PX; ++p)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint2 lo = load4_bf16(src + 8 * i, cols - 8 * i, s.vec != 0, p);
-              const uint2 hi = load4_bf16(src + 8 * i + 4, cols - 8 * i - 4, s.vec != 0, p);
-              reinterpret_cast<uint4*>(dst + p * kDabTokens * kDabXPitch / 2)[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-            }
-        }
-      }
-      for (int i = tid; i < kDabTokens * rows; i += kDabThreads) {
-        const int t = i / rows, j = i - t * rows;
-        float f = 0.0f;
-        if (t < left && j < r) {
-          const int64_t m = w0 + tok[t];
-          f = s.coef[m * r + j];
-          if (is_a) f = __fmul_rn(f, div127_rn(__ldg(g.eta + m)));
-        }
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const __nv_bfloat16 h = __float2bfloat16_rn(f);
-          s_coef[(p * kDabTokens + t) * cpitch + j] = h;
-          f = bf16_part<2>(f, 1);
-        }
-      }
+    int c = (z - chunk0 % CS + CS) % CS;  // this CTA's chunks: every CS-th
+    if (c < chunks) load(s_tok + c * kDabTokens, total - c * kDabTokens, w0);
+    for (; c < chunks; c += CS) {
+      put();
       __syncthreads();
+      // the next chunk's rows are on their way while this one is multiplied
+      if (c + CS < chunks) load(s_tok + (c + CS) * kDabTokens, total - (c + CS) * kDabTokens, w0);
       const int kk = lane & 7, mat = lane >> 3;
 #pragma unroll
       for (int ks = 0; ks < kDabTokens / 16; ++ks) {
@@ -691,10 +740,7 @@ __device__ __forceinline__ void dab_tile(const DabArgs& g, const DabSide& s, int
     const int j = is_a ? e / kDabCols : e % r, c = is_a ? e % kDabCols : e / r;
     if (c >= cols) continue;
     float v = s_out[j * kOPitch + c];
-    if (CS > 1) {
-      v = 0.0f;
-      for (int k = 0; k < CS; ++k) v = __fadd_rn(v, ld_cluster_f32(cluster_map(s_out + j * kOPitch + c, k)));
-    }
+    if (CS > 1) v = cluster_total(s_out + j * kOPitch + c, CS);
     store_out<OutT>(s.out, base + (is_a ? j * s.C + c : static_cast<int64_t>(c) * r + j), v);
   }
   if (CS > 1) cluster_sync_all();  // the sums stay until they are read

@@ -671,10 +671,10 @@ bl_status launch_tc_bm(const int8_t* xq, const float* eta, const int32_t* xsum, 
   if (grid.y > 65535) return BL_ERR_UNSUPPORTED;
   const int ks = tc_split<BM>(grid.x * grid.y, K, sms);
   if (ks <= 1)
-    return launch_pdl(kern, grid, dim3(bl::kTcThreads), smem, st, tm_x, tm_w, eta, xsum,
+    return launch_pdl(kern, grid, dim3(bl::tc_threads(AD)), smem, st, tm_x, tm_w, eta, xsum,
                       gamma, M, K, N, y, y_int, 1, wstatic, ad);
   grid.z = static_cast<unsigned>(ks);
-  return launch_pdl_cluster(kern, grid, dim3(bl::kTcThreads), smem, st,
+  return launch_pdl_cluster(kern, grid, dim3(bl::tc_threads(AD)), smem, st,
                             static_cast<unsigned>(ks), tm_x, tm_w, eta, xsum, gamma, M, K, N, y,
                             y_int, ks, wstatic, ad);
 }

@@ -166,6 +166,53 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_
                : "memory");
 }
 
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// The sum over the CTAs of a cluster of the value at one place of their
+// shared memory, in their order, the reads all in flight at once.
+__device__ __forceinline__ float cluster_total(const float* p, int ctas) {
+  float v[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) v[c] = c < ctas ? ld_cluster_f32(cluster_map(p, c)) : 0.0f;
+  float t = v[0];
+#pragma unroll
+  for (int c = 1; c < 8; ++c) t = __fadd_rn(t, v[c]);
+  return t;
+}
+
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+// The same for four neighbouring values.
+__device__ __forceinline__ float4 cluster_total4(const float* p, int ctas) {
+  float4 v[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    v[c] = make_float4(0, 0, 0, 0);
+    if (c < ctas)
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[c].x), "=f"(v[c].y), "=f"(v[c].z), "=f"(v[c].w)
+                   : "r"(cluster_map(p, c))
+                   : "memory");
+  }
+  float4 t = v[0];
+#pragma unroll
+  for (int c = 1; c < 8; ++c) {
+    t.x = __fadd_rn(t.x, v[c].x);
+    t.y = __fadd_rn(t.y, v[c].y);
+    t.z = __fadd_rn(t.z, v[c].z);
+    t.w = __fadd_rn(t.w, v[c].w);
+  }
+  return t;
+}
+
 // ---------------------------------------------------------------- tcgen05
 
 __device__ __forceinline__ void tmem_alloc(uint32_t* smem_dst, uint32_t ncols) {

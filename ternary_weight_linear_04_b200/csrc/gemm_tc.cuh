@@ -73,7 +73,7 @@ struct TcCfg {
           ? 8
           : 1 + static_cast<int>(kStageRegion / (static_cast<size_t>(kTcBN) * BM * 4));
   static constexpr int kTmemCols = BM < 32 ? 32 : BM;
-  static constexpr int kBarBytes = 8 * (4 * kStages + 2) + 16 + 8 * BM;
+  static constexpr int kBarBytes = 8 * (4 * kStages + 4) + 16 + 8 * BM;
   static constexpr size_t kSmem = 1024 + kStageRegion + kBarBytes;
   static constexpr size_t kSmemAdapters = kSmem + 8 * BM + 48;  // the tile's adapter ids and their list
   static_assert(kSmemAdapters <= 227 * 1024, "shared memory per CTA");
@@ -86,10 +86,16 @@ struct TcCfg {
 // u, rank index), its weight-side row B_a and its token-side row the part of
 // u, zero for the tokens of other adapters.  u (fp32) is split into two bf16
 // parts for bf16 outputs (2^-17 of it) and three for fp32 ones (all of it).
-// The unpack warps write both operands; entries of several adapters share a
+// Eight more warps write both operands: they find the tile's adapters and
+// hold the first step's values in registers while the K loop runs (built by
+// the unpack warps behind the loop, 16 us a tile of 256 tokens were left
+// open), and take half of the epilogue.  Entries of several adapters share a
 // step, so small ranks do not pad.  Of a K split only CTA 0 has these steps.
+constexpr int kTcAdWarps = 8;
+constexpr int tc_threads(bool ad) { return kTcThreads + (ad ? 32 * kTcAdWarps : 0); }
+
 template <int BM, typename OutT, bool AD>
-__global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
+__global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
     k_gemm_tc(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
               const float* __restrict__ eta, const int32_t* __restrict__ xsum,
               const float* __restrict__ gamma_p, int M, int K, int N, void* __restrict__ y,
@@ -110,7 +116,9 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
   uint64_t* empty = full_b + S;   // the MMA is done with the stage
   uint64_t* accum_full = empty + S;
   uint64_t* drain = accum_full + 1;  // the MMAs issued before an abort are done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* counted = drain + 1;     // AD: the tile's adapters are known
+  uint64_t* unpacked = counted + 1;  // AD: the K loop's last stage has been written
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(unpacked + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* s_scale = reinterpret_cast<float*>(tmem_slot + 4);
   int32_t* s_xsum = reinterpret_cast<int32_t*>(s_scale + BM);
@@ -118,6 +126,7 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
   int* s_list = s_ids + BM;
   int* s_cnt = s_list + BM;
   volatile int* s_bad = s_cnt + 8;  // a factor is not finite
+  volatile int* s_entries = s_bad + 1;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -144,7 +153,11 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
     mbar_init(accum_full, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
-    if constexpr (AD) *s_bad = 0;
+    if constexpr (AD) {
+      mbar_init(counted, 1);
+      mbar_init(unpacked, 1);
+      *s_bad = 0;
+    }
     mbar_init_fence();
     tma_prefetch_desc(&tm_x);
     tma_prefetch_desc(&tm_w);
@@ -165,12 +178,6 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
       s_xsum[i] = in ? xsum[m0 + i] : 0;
     }
   }
-  int entries = 0, asteps = 0;
-  if constexpr (AD)
-    if (zr == 0) {
-      entries = tile_adapters(ad.ids, m0, M, BM, ad.L, s_ids, s_list, s_cnt) * kParts * ad.r;
-      asteps = (entries + 63) >> 6;
-    }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -231,7 +238,9 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
       }
       if constexpr (AD) {
         constexpr uint32_t idesc16 = make_idesc_bf16(kTcBN, BM, false, false);
-        for (int i = nkt; ok && i < nkt + asteps; ++i) {
+        ok = ok && mbar_wait(counted, 0, abort_flag);
+        const int asteps = ok ? (*s_entries + 63) >> 6 : 0;
+        for (int i = nkt; i < nkt + asteps; ++i) {
           const int s = i % S;
           ok = mbar_wait(full_a + s, static_cast<uint32_t>(i / S) & 1u, abort_flag);
           if (!ok) {
@@ -250,7 +259,7 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
       }
       if (ok) tc_commit(accum_full);
     }
-  } else {
+  } else if (warp < 2 + kTcUnpackWarps) {
     // ---------------- unpack, then epilogue (warps 2..9)
     const int u = warp - 2;            // 0..7
     // thread t = 32u + lane: row t / 2, half t % 2 of the row's 32 packed
@@ -289,80 +298,112 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
 #endif
       if (lane == 0) mbar_arrive(full_a + s);
     }
-    if constexpr (AD) {
-      const int r = ad.r, group = kParts * r;  // entries of one adapter
-      const bool chunked = (r & 7) == 0;       // eight entries share adapter and part
-      for (int i = nkt; ok && i < nkt + asteps; ++i) {
-        const int s = i % S, e0 = (i - nkt) * 64;
-        if (i >= S) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + s, static_cast<uint32_t>(i / S - 1) & 1u, abort_flag));
-          if (!ok) break;
-        }
-        {  // rows of B: this thread's feature, 32 entries
-          const int64_t n = n0 + urow;
-          uint8_t* dst = a_row + s * Cfg::kABytes;
-#pragma unroll 1
-          for (int c = uhalf * 4; c < uhalf * 4 + 4; ++c) {
-            const int e = e0 + 8 * c;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (n < N && e < entries) {
-              if (chunked) {
-                const int li = e / group, j = (e - li * group) % r;
-                v = __ldg(reinterpret_cast<const uint4*>(ad.B + (static_cast<int64_t>(s_list[li]) * N + n) * r + j));
-              } else {
-                uint32_t w[4] = {0, 0, 0, 0};
+    if constexpr (AD)
+      if (u == 0 && lane == 0) mbar_arrive(unpacked);
+    if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(accum_full, 0, abort_flag));
+    epi_ok = ok && __all_sync(0xFFFFFFFFu, *abort_flag == 0);
+  } else if constexpr (AD) {
+    // ---------------- adapter operands (warps 10..17), then epilogue
+    const int t = threadIdx.x - kTcThreads;
+    const int r = ad.r, group = kParts * r;  // entries of one adapter
+    const bool chunked = (r & 7) == 0;       // eight entries share adapter and part
+    int entries = 0;
+    if (zr == 0)
+      entries = tile_adapters(ad.ids, m0, M, BM, ad.L, s_ids, s_list, s_cnt, t,
+                              [] { asm volatile("bar.sync 1, 256;" ::: "memory"); }) * group;
+    if (t == 0) {
+      *s_entries = entries;
+      mbar_arrive(counted);
+    }
+    const int asteps = (entries + 63) >> 6;
+    // thread: feature t / 2 and half of a step's entries; tokens in pieces of
+    // one token and 8 entries
+    constexpr int kEach = BM * 8 / (32 * kTcAdWarps) > 0 ? BM * 8 / (32 * kTcAdWarps) : 1;
+    const int frow = t >> 1, fhalf = t & 1;
+    uint4 va[4], vu[kEach];
+    auto load = [&](int e0) {
+      const int64_t n = n0 + frow;
 #pragma unroll
-                for (int b = 0; b < 8; ++b)
-                  if (e + b < entries) {
-                    const int li = (e + b) / group, j = (e + b - li * group) % r;
-                    const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(ad.B) +
-                                             (static_cast<int64_t>(s_list[li]) * N + n) * r + j);
-                    w[b >> 1] |= h << (16 * (b & 1));
-                  }
-                v = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int wi = 0; wi < 4; ++wi) {
+        const int e = e0 + 32 * fhalf + 8 * wi;
+        va[wi] = make_uint4(0, 0, 0, 0);
+        if (n < N && e < entries) {
+          if (chunked) {
+            const int li = e / group, j = (e - li * group) % r;
+            va[wi] = __ldg(reinterpret_cast<const uint4*>(ad.B + (static_cast<int64_t>(s_list[li]) * N + n) * r + j));
+          } else {
+            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+              if (e + b < entries) {
+                const int li = (e + b) / group, j = (e + b - li * group) % r;
+                const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(ad.B) +
+                                         (static_cast<int64_t>(s_list[li]) * N + n) * r + j);
+                w[b >> 1] |= h << (16 * (b & 1));
               }
-            }
-            if (nonfinite8(v)) {
-              v = make_uint4(0, 0, 0, 0);
-              *s_bad = 1;
-            }
-            *reinterpret_cast<uint4*>(dst + ((c ^ r8) << 4)) = v;
+            va[wi] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
-        // rows of u: one token and 8 entries at a time
-#pragma unroll 1
-        for (int q = 32 * u + lane; q < BM * 8; q += 32 * kTcUnpackWarps) {
-          const int t = q % BM, c = q / BM, id = s_ids[t];
-          const int e = e0 + 8 * c;
-          const float* ut = ad.u + static_cast<int64_t>(m0 + t) * r;
-          uint32_t w[4] = {0, 0, 0, 0};
-          if (id >= 0 && e < entries) {
-            if (chunked) {
-              const int li = e / group, rem = e - li * group, p = rem / r;
-              if (s_list[li] == id) {
-                const float* x = ut + rem - p * r;
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                  w[b] = pack_bf16(bf16_part<kParts>(x[2 * b], p), bf16_part<kParts>(x[2 * b + 1], p));
-              }
-            } else {
-              float f[8];
-#pragma unroll
-              for (int b = 0; b < 8; ++b) {
-                const int li = (e + b) / group, rem = e + b - li * group, p = rem / r;
-                f[b] = e + b < entries && s_list[li] == id ? bf16_part<kParts>(ut[rem - p * r], p) : 0.0f;
-              }
-#pragma unroll
-              for (int b = 0; b < 4; ++b) w[b] = pack_bf16(f[2 * b], f[2 * b + 1]);
-            }
-          }
-          *reinterpret_cast<uint4*>(sB + s * Cfg::kBBytes + (t >> 3) * 1024 + (t & 7) * 128 + ((c ^ (t & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full_a + s);
       }
+#pragma unroll
+      for (int y4 = 0; y4 < kEach; ++y4) {
+        const int q = t + 32 * kTcAdWarps * y4;
+        const int tok = q % BM, e = e0 + 8 * (q / BM);
+        vu[y4] = make_uint4(0, 0, 0, 0);
+        const int id = s_ids[tok];
+        if (id < 0 || q >= BM * 8 || e >= entries) continue;
+        const float* ut = ad.u + static_cast<int64_t>(m0 + tok) * r;
+        float f[8];
+        if (chunked) {
+          const int li = e / group, rem = e - li * group, p = rem / r;
+          if (s_list[li] != id) continue;
+          const float4* x = reinterpret_cast<const float4*>(ut + rem - p * r);
+          const float4 lo = x[0], hi = x[1];
+          const float g[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+          for (int b = 0; b < 8; ++b) f[b] = bf16_part<kParts>(g[b], p);
+        } else {
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            const int li = (e + b) / group, rem = e + b - li * group, p = rem / r;
+            f[b] = e + b < entries && s_list[li] == id ? bf16_part<kParts>(ut[rem - p * r], p) : 0.0f;
+          }
+        }
+        vu[y4] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+      }
+    };
+    if (asteps > 0) load(0);
+    // from here on `empty` of every stage is in the phase of its last step of
+    // the K loop or past it, so that a parity says which (these warps have
+    // not followed the phases)
+    bool ok = asteps == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(unpacked, 0, abort_flag));
+    for (int i = nkt; ok && i < nkt + asteps; ++i) {
+      const int s = i % S;
+      if (i >= S) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + s, static_cast<uint32_t>(i / S - 1) & 1u, abort_flag));
+        if (!ok) break;
+      }
+      uint8_t* dst = sA + s * Cfg::kABytes + (frow >> 3) * 1024 + (frow & 7) * 128;
+#pragma unroll
+      for (int wi = 0; wi < 4; ++wi) {
+        if (nonfinite8(va[wi])) {
+          va[wi] = make_uint4(0, 0, 0, 0);
+          *s_bad = 1;
+        }
+        *reinterpret_cast<uint4*>(dst + (((fhalf * 4 + wi) ^ (frow & 7)) << 4)) = va[wi];
+      }
+#pragma unroll
+      for (int y4 = 0; y4 < kEach; ++y4) {
+        const int q = t + 32 * kTcAdWarps * y4;
+        const int tok = q % BM, c = q / BM;
+        if (q < BM * 8)
+          *reinterpret_cast<uint4*>(sB + s * Cfg::kBBytes + (tok >> 3) * 1024 + (tok & 7) * 128 + ((c ^ (tok & 7)) << 4)) =
+              vu[y4];
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full_a + s);
+      if (i + 1 < nkt + asteps) load((i + 1 - nkt) * 64);
     }
     if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(accum_full, 0, abort_flag));
     epi_ok = ok && __all_sync(0xFFFFFFFFu, *abort_flag == 0);
@@ -385,9 +426,10 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
   const int q = warp & 3;
   const int row = q * 32 + lane;
   const int half = (warp - 2) >> 2;
-  constexpr int kColsPerWarp = BM < 32 ? 16 : BM / 2;  // two warps per lane quarter
-  const int col0 = (BM < 32) ? 0 : half * kColsPerWarp;
-  const bool epi_cols = epi_warp && !(BM < 32 && half == 1);
+  constexpr int kColParts = BM < 32 ? 1 : (AD && BM >= 64 ? 4 : 2);  // warps per lane quarter
+  constexpr int kColsPerWarp = BM / kColParts;
+  const int col0 = half * kColsPerWarp;
+  const bool epi_cols = epi_warp && half < kColParts;
   const uint32_t t_row = tmem_d + (static_cast<uint32_t>(q * 32) << 16);
   // CTA 0's stage memory receives the partial tiles of CTAs 1..ksplit-1:
   // slot r-1, [128 rows][BM columns] int32
@@ -415,6 +457,7 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
   if (zr == 0 && epi_cols && epi_ok) {
     tc_fence_after();
     const int n = n0 + row;
+    const bool added = AD && *s_entries > 0, plain = AD && *s_bad != 0;
 #pragma unroll 1
     for (int cc = col0; cc < col0 + kColsPerWarp; cc += 16) {
       uint32_t v[16];
@@ -431,12 +474,26 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
           v[j + 3] += static_cast<uint32_t>(t.w);
         }
       }
-      uint32_t f[16];
-      if constexpr (AD)
-        if (asteps) {
-          tmem_ld_32x32b_x16(t_row + Cfg::kTmemCols + cc, f);
+      float f[16];
+      if constexpr (AD) {
+        uint32_t w[16];
+        if (added) {
+          tmem_ld_32x32b_x16(t_row + Cfg::kTmemCols + cc, w);
           tmem_ld_wait();
         }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) f[j] = added ? __uint_as_float(w[j]) : 0.0f;
+        if (plain) {
+#pragma unroll 1
+          for (int j = 0; j < 16; ++j) {
+            const int m = m0 + cc + j;
+            const float sum = m < M && n < N ? adapter_add(ad.u, ad.B, ad.ids, ad.L, ad.r, m, n, N, 0.0f) : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (k == j) f[k] = sum;
+          }
+        }
+      }
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const int m = m0 + cc + j;
@@ -444,8 +501,7 @@ __global__ void __launch_bounds__(kTcThreads, BM <= 32 ? 2 : 1)
           const int32_t yi = static_cast<int32_t>(v[j]) - s_xsum[cc + j];
           const int64_t o = static_cast<int64_t>(m) * N + n;
           float yv = rescale(yi, s_scale[cc + j]);
-          if constexpr (AD)
-            if (asteps) yv = *s_bad ? adapter_add(ad.u, ad.B, ad.ids, ad.L, ad.r, m, n, N, yv) : __fadd_rn(yv, __uint_as_float(f[j]));
+          if constexpr (AD) yv = __fadd_rn(yv, f[j]);
           store_out<OutT>(y, o, yv);
           if (y_int) y_int[o] = yi;
         }

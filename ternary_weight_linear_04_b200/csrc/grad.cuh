@@ -112,18 +112,25 @@ __global__ void __launch_bounds__(256)
 //     its 16, which leaves the columns of a 16-group in the order 0 8 1 9 ..
 //     7 15; the epilogue puts them back by naming registers;
 //   * eight (H = 2) MMAs 128 x 256 x 16.
-// H = 2 shares one expanded tile between two MMAs of 128 tokens; H = 1 is
-// for token counts that would leave the second half empty.
+// Two groups of eight expanding warps take the steps in turn, which hides
+// the chain wait - load - store - fence of one step behind the other's.
+// H = 2 shares one expanded tile between two MMAs of 128 tokens and fills
+// TMEM, for token counts that fill the GPU; H = 1 is for the rest, where a
+// cluster splits the steps and adds the tiles through distributed shared
+// memory.
 //
-// Adapters: behind the steps over n come steps over the adapters of the
-// tile's tokens, whose operands the eight warps write: v (each token's row
-// masked to its own adapter, divided by gamma because the sum is multiplied
-// by it at the end) in two bf16 parts against A_a twice, 64 entries a step.
+// Adapters: behind the steps over n come steps of 64 entries, an entry being
+// one (adapter of the tile's tokens, part of v, rank index): v (each token's
+// row masked to its own adapter, divided by gamma because the sum is
+// multiplied by it at the end; three bf16 parts for fp32 results, two for
+// bf16 ones) against A_a's row, written by the expanding warps.
 
 constexpr int kGiBK = 64;    // n per step
 constexpr int kGiBN = 256;   // inputs k per tile
-constexpr int kGiWarps = 8;  // expanding warps
-constexpr int kGiThreads = 32 * (2 + kGiWarps);
+constexpr int kGiGroup = 8;  // warps that expand a step
+constexpr int kGiGroups = 2;
+constexpr int kGiThreads = 32 * (2 + kGiGroup * kGiGroups);
+constexpr int kGiTilePitch = kGiBN + 4;  // floats of a token's row in the finished tile (H = 1)
 
 template <int H>
 struct GiCfg {
@@ -133,9 +140,10 @@ struct GiCfg {
   static constexpr int kBBytes = kGiBK * kGiBN * 2;  // expanded weights
   static constexpr int kPBytes = kGiBK * kGiBN / 4;  // packed weights
   static constexpr int kBars = 3 * kStages + 2 * kPStages + 2;
-  static constexpr int kTail = 8 * kBars + 16 + 4 * (2 * 128 * H + 16);
+  static constexpr int kTail = 8 * kBars + 32 + 4 * (2 * 128 * H + 8);
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * (kABytes + kBBytes) + kPStages * kPBytes + kTail;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  static_assert(H == 2 || 128 * kGiTilePitch * 4 <= kStages * (kABytes + kBBytes), "the finished tile in the stages");
 };
 
 struct GiArgs {
@@ -152,8 +160,9 @@ struct GiArgs {
 };
 
 // Sixteen bf16 of a row of the factor in the column order of the expanded
-// weights (pairs (i, i + 8)); zero past `left`.
-__device__ __forceinline__ void load16_paired(const __nv_bfloat16* p, int64_t left, bool vec, uint32_t (&o)[8]) {
+// weights (pairs (i, i + 8)); zero past `left`, and in the place of values
+// that are not finite, in which case it returns true.
+__device__ __forceinline__ bool load16_paired(const __nv_bfloat16* p, int64_t left, bool vec, uint32_t (&o)[8]) {
   uint32_t w[8];
   if (left >= 16 && vec) {
     const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 8);
@@ -165,29 +174,52 @@ __device__ __forceinline__ void load16_paired(const __nv_bfloat16* p, int64_t le
     for (int i = 0; i < 8; ++i)
       w[i] = (2 * i < left ? h[2 * i] : 0u) | (2 * i + 1 < left ? static_cast<uint32_t>(h[2 * i + 1]) << 16 : 0u);
   }
+  uint32_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bad |= nonfinite2(w[i]);
+  if (bad)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t b = nonfinite2(w[i]);
+      w[i] &= ((b & 0x8000u) ? 0u : 0xFFFFu) | ((b & 0x80000000u) ? 0u : 0xFFFF0000u);
+    }
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = __byte_perm(w[i >> 1], w[4 + (i >> 1)], (i & 1) ? 0x7632 : 0x5410);
+  return bad != 0;
 }
 
+// What load16_paired left out of one output: the terms of its adapter's
+// values that are not finite.
+__device__ __noinline__ float gi_nonfinite(const float* v, const __nv_bfloat16* A, int a, int r, int m, int k, int K) {
+  float s = 0.0f;
+  for (int j = 0; j < r; ++j) {
+    const float w = __bfloat162float(A[(static_cast<int64_t>(a) * r + j) * K + k]);
+    if (__fsub_rn(w, w) != 0.0f) s = __fmaf_rn(v[static_cast<int64_t>(m) * r + j], w, s);
+  }
+  return s;
+}
+
+// Grid (tiles, 1, CTAs of a cluster along the contraction; H = 2: 1).
 template <int H, typename OutT>
 __global__ void __launch_bounds__(kGiThreads, 1)
     k_grad_input(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_w, const GiArgs a) {
   using Cfg = GiCfg<H>;
-  constexpr int S = Cfg::kStages, SP = Cfg::kPStages;
+  constexpr int S = Cfg::kStages, SP = Cfg::kPStages, kParts = sizeof(OutT) == 4 ? 3 : 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sA = base;
   uint8_t* sB = sA + S * Cfg::kABytes;
   uint8_t* sP = sB + S * Cfg::kBBytes;
   uint64_t* full_a = reinterpret_cast<uint64_t*>(sP + SP * Cfg::kPBytes);  // dy tile in
-  uint64_t* full_b = full_a + S;      // weights expanded (8 warps)
+  uint64_t* full_b = full_a + S;      // weights expanded (a group's warps)
   uint64_t* empty = full_b + S;       // the MMAs are done with the stage
   uint64_t* full_p = empty + S;       // packed tile in
-  uint64_t* empty_p = full_p + SP;    // packed tile read (8 warps)
+  uint64_t* empty_p = full_p + SP;    // packed tile read (a group's warps)
   uint64_t* accum_full = empty_p + SP;
   uint64_t* drain = accum_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile float* s_bad = reinterpret_cast<volatile float*>(tmem_slot + 2);  // not zero: a value of A is not finite
   int* s_ids = reinterpret_cast<int*>(tmem_slot + 4);
   int* s_list = s_ids + 128 * H;
   int* s_cnt = s_list + 128 * H;
@@ -196,32 +228,37 @@ __global__ void __launch_bounds__(kGiThreads, 1)
   const int ktiles = (a.K + kGiBN - 1) / kGiBN;
   const int k0 = static_cast<int>(blockIdx.x % ktiles) * kGiBN, m0 = static_cast<int>(blockIdx.x / ktiles) * (128 * H);
   const int steps_n = (a.N + kGiBK - 1) / kGiBK;
-  const int nst = steps_n * a.planes;
+  const int CS = H == 1 ? static_cast<int>(cluster_nctarank()) : 1;
+  const int z = CS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  // this CTA's steps over n: [lo, lo + nst) of all planes'
+  const int64_t all = static_cast<int64_t>(steps_n) * a.planes;
+  const int lo = static_cast<int>(all * z / CS), nst = static_cast<int>(all * (z + 1) / CS) - lo;
 
   auto issue_p = [&](int i) {
     const int s = i % SP;
     mbar_arrive_expect_tx(full_p + s, Cfg::kPBytes);
-    tma_load_2d(sP + s * Cfg::kPBytes, &tm_w, full_p + s, k0 / 4, (i % steps_n) * kGiBK);
+    tma_load_2d(sP + s * Cfg::kPBytes, &tm_w, full_p + s, k0 / 4, ((lo + i) % steps_n) * kGiBK);
   };
   auto issue_a = [&](int i) {
     const int s = i % S;
     mbar_arrive_expect_tx(full_a + s, Cfg::kABytes);
-    tma_load_3d(sA + s * Cfg::kABytes, &tm_dy, full_a + s, (i % steps_n) * kGiBK, m0, i / steps_n);
+    tma_load_3d(sA + s * Cfg::kABytes, &tm_dy, full_a + s, ((lo + i) % steps_n) * kGiBK, m0, (lo + i) / steps_n);
   };
   const int a_first = nst < S ? nst : S, p_first = nst < SP ? nst : SP;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_a + s, 1);
-      mbar_init(full_b + s, kGiWarps);
+      mbar_init(full_b + s, kGiGroup);
       mbar_init(empty + s, 1);
     }
     for (int s = 0; s < SP; ++s) {
       mbar_init(full_p + s, 1);
-      mbar_init(empty_p + s, kGiWarps);
+      mbar_init(empty_p + s, kGiGroup);
     }
     mbar_init(accum_full, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
+    *s_bad = 0.0f;
     mbar_init_fence();
   }
   if (warp == 1) {
@@ -234,12 +271,14 @@ __global__ void __launch_bounds__(kGiThreads, 1)
     for (int i = 0; i < p_first; ++i) issue_p(i);
     for (int i = 0; i < a_first; ++i) issue_a(i);
   }
-  int nadapt = 0, esteps = 0;  // adapters of the tile, steps of 64 entries for each
+  int entries = 0, ast = 0, alo = 0;  // entries of the tile's adapters, this CTA's steps of 64 of them
   if (a.v) {
-    nadapt = tile_adapters(a.ids, m0, a.M, 128 * H, a.L, s_ids, s_list, s_cnt);
-    esteps = (2 * a.r + kGiBK - 1) / kGiBK;
+    entries = tile_adapters(a.ids, m0, a.M, 128 * H, a.L, s_ids, s_list, s_cnt) * kParts * a.r;
+    const int asteps = (entries + kGiBK - 1) / kGiBK;
+    alo = asteps * z / CS;
+    ast = asteps * (z + 1) / CS - alo;
   }
-  const int nall = nst + nadapt * esteps;
+  const int nall = nst + ast;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -295,12 +334,14 @@ __global__ void __launch_bounds__(kGiThreads, 1)
     }
   } else {
     // ---------------- expand: thread = row n of the tile and 64 of its inputs
-    const int t = threadIdx.x - 64;
+    const int grp = (warp - 2) / kGiGroup;
+    const int t = (threadIdx.x - 64) & (32 * kGiGroup - 1);
     const int n = t & 63, q = t >> 6;
     const uint32_t src_off = n * 64 + ((q ^ ((n >> 1) & 3)) << 4);  // 64-byte swizzle
     uint8_t* const dst0 = sB + q * (kGiBK * 128) + (n >> 3) * 1024 + (n & 7) * 128;
     bool ok = true;
-    for (int i = 0; i < nst; ++i) {
+    int i = grp;
+    for (; i < nst; i += kGiGroups) {
       const int s = i % S, sp = i % SP;
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(full_p + sp, static_cast<uint32_t>(i / SP) & 1u, abort_flag));
       if (!ok) break;
@@ -330,51 +371,71 @@ __global__ void __launch_bounds__(kGiThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(full_b + s);
     }
-    // ---------------- adapters: entry e of 2 r is v's first part (e < r) or its rest
-    const float inv_gamma = nall > nst ? __frcp_rn(*a.gamma) : 0.0f;
-    const bool avec = (a.K & 7) == 0;
-    for (int i = nst; ok && i < nall; ++i) {
-      const int s = i % S;
+    // ---------------- adapters
+    const int r = a.r, group = kParts * r;
+    const float inv_gamma = ok && i < nall ? __frcp_rn(*a.gamma) : 0.0f;
+    const bool avec = (a.K & 7) == 0, chunked = (r & 7) == 0;
+    for (; ok && i < nall; i += kGiGroups) {
+      const int s = i % S, e0 = (alo + i - nst) * kGiBK;
       if (i >= S) {
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + s, static_cast<uint32_t>(i / S - 1) & 1u, abort_flag));
         if (!ok) break;
       }
-      const int ad = s_list[(i - nst) / esteps], e0 = (i - nst) % esteps * kGiBK;
-      if (t < 128 * H) {  // this token's row of v
-        const bool mine = s_ids[t] == ad;
-        const float* vr = a.v + static_cast<int64_t>(m0 + t) * a.r;
-        uint8_t* row = sA + s * Cfg::kABytes + (t >> 3) * 1024 + (t & 7) * 128;
-#pragma unroll 2
-        for (int c = 0; c < 8; ++c) {
-          uint32_t o[4];
+      {  // a row of A: one entry, 64 inputs
+        const int e = e0 + n, li = e / group, j = (e - li * group) % r;
+        uint32_t o[4][8];
+        bool bad = false;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float f[2];
+        for (int wi = 0; wi < 4; ++wi) {
+          const int k = k0 + 64 * q + 16 * wi;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const int e = e0 + 8 * c + 2 * j + b;
-              float x = 0.0f;
-              if (mine && e < 2 * a.r) {
-                x = __fmul_rn(vr[e < a.r ? e : e - a.r], inv_gamma);
-                if (e >= a.r) x = __fsub_rn(x, __bfloat162float(__float2bfloat16_rn(x)));
-              }
-              f[b] = x;
-            }
-            o[j] = pack_bf16(f[0], f[1]);
-          }
-          *reinterpret_cast<uint4*>(row + ((c ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int b = 0; b < 8; ++b) o[wi][b] = 0;
+          if (e < entries && k < a.K)
+            bad |= load16_paired(a.A + (static_cast<int64_t>(s_list[li]) * r + j) * a.K + k, a.K - k, avec, o[wi]);
+        }
+        if (bad) *s_bad = 1.0f;
+        uint8_t* dst = dst0 + s * Cfg::kBBytes;
+#pragma unroll
+        for (int wi = 0; wi < 4; ++wi) {
+          *reinterpret_cast<uint4*>(dst + (((2 * wi) ^ (n & 7)) << 4)) = make_uint4(o[wi][0], o[wi][1], o[wi][2], o[wi][3]);
+          *reinterpret_cast<uint4*>(dst + (((2 * wi + 1) ^ (n & 7)) << 4)) = make_uint4(o[wi][4], o[wi][5], o[wi][6], o[wi][7]);
         }
       }
-      const int e = e0 + n;
-      const __nv_bfloat16* ar = a.A + (static_cast<int64_t>(ad) * a.r + (e < a.r ? e : e - a.r)) * a.K;
-      uint8_t* dst = dst0 + s * Cfg::kBBytes;
-#pragma unroll 1
-      for (int wi = 0; wi < 4; ++wi) {
-        uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        const int k = k0 + 64 * q + 16 * wi;
-        if (e < 2 * a.r && k < a.K) load16_paired(ar + k, a.K - k, avec, o);
-        *reinterpret_cast<uint4*>(dst + (((2 * wi) ^ (n & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(dst + (((2 * wi + 1) ^ (n & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      // rows of v: a token's 64 entries (H = 1: two threads a token)
+      constexpr int kPer = H == 2 ? 8 : 4;
+      const int tok = H == 2 ? t : t >> 1, c0 = H == 2 ? 0 : 4 * (t & 1), id = s_ids[tok];
+      const float* vr = a.v + static_cast<int64_t>(m0 + tok) * r;
+      uint8_t* row = sA + s * Cfg::kABytes + (tok >> 3) * 1024 + (tok & 7) * 128;
+#pragma unroll
+      for (int h4 = 0; h4 < kPer; h4 += 4) {
+        float f[4][8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int e = e0 + 8 * (c0 + h4 + c);
+#pragma unroll
+          for (int b = 0; b < 8; ++b) f[c][b] = 0.0f;
+          if (id < 0 || e >= entries) continue;
+          if (chunked) {
+            const int li = e / group, rem = e - li * group, p = rem / r;
+            if (s_list[li] != id) continue;
+            const float4* x = reinterpret_cast<const float4*>(vr + rem - p * r);
+            const float4 u = x[0], w = x[1];
+            const float g[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int b = 0; b < 8; ++b) f[c][b] = bf16_part<kParts>(__fmul_rn(g[b], inv_gamma), p);
+          } else {
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+              const int li = (e + b) / group, rem = e + b - li * group, p = rem / r;
+              if (e + b < entries && s_list[li] == id) f[c][b] = bf16_part<kParts>(__fmul_rn(vr[rem - p * r], inv_gamma), p);
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(row + (((c0 + h4 + c) ^ (tok & 7)) << 4)) =
+              make_uint4(pack_bf16(f[c][0], f[c][1]), pack_bf16(f[c][2], f[c][3]), pack_bf16(f[c][4], f[c][5]),
+                         pack_bf16(f[c][6], f[c][7]));
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -395,33 +456,98 @@ __global__ void __launch_bounds__(kGiThreads, 1)
       mbar_drain(bars + i % ring, static_cast<uint32_t>(i / ring) & 1u);
   }
 
-  // ---------------- epilogue: one TMEM lane = one token
+  // ---------------- epilogue: one TMEM lane = one token; four warps share a
+  // lane quarter: H = 2: two for each half of the tokens, half of the columns
+  // each; H = 1: a quarter of the columns each.
+  float* tile = reinterpret_cast<float*>(sA);  // H = 1: 128 x kGiTilePitch; H = 2: a 32 x 33 patch for each warp
+  const int qd = warp & 3, part = (warp - 2) >> 2;
   if (warp >= 2 && epi_ok) {
     tc_fence_after();
     const float gamma = *a.gamma;
-    const int qd = warp & 3, part = (warp - 2) >> 2;
-    // H = 2: the two warps of a lane quarter take one half of the tokens
-    // each; H = 1: half of the columns each
-    const int h = H == 2 ? part : 0;
-    const int c_begin = H == 2 ? 0 : part * 128, c_end = H == 2 ? 256 : c_begin + 128;
-    const int64_t m = static_cast<int64_t>(m0) + 128 * h + 32 * qd + lane;
-    const uint32_t trow = tmem_d + 256 * h + (static_cast<uint32_t>(qd * 32) << 16);
+    const int h = H == 2 ? part >> 1 : 0;
+    const int c_begin = H == 2 ? (part & 1) * 128 : part * 64, c_end = c_begin + (H == 2 ? 128 : 64);
+    const int trow = 128 * h + 32 * qd;
+    const int64_t m = static_cast<int64_t>(m0) + trow + lane;
+    const uint32_t taddr = tmem_d + 256 * h + (static_cast<uint32_t>(qd * 32) << 16);
+    const bool fix = a.v && *s_bad != 0.0f;
 #pragma unroll 1
     for (int c = c_begin; c < c_end; c += 32) {
       uint32_t v[32];
-      tmem_ld_32x32b_x32(trow + c, v);
-      tmem_ld_wait();
+      if (nall > 0) {
+        tmem_ld_32x32b_x32(taddr + c, v);
+        tmem_ld_wait();
+      } else {
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        float f[16];
+        for (int j = 0; j < 32; ++j) v[j] = 0;
+      }
+      float f[32];
+#pragma unroll
+      for (int g = 0; g < 32; g += 16)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          f[j] = __fmul_rn(__uint_as_float(v[16 * g + 2 * j]), gamma);
-          f[8 + j] = __fmul_rn(__uint_as_float(v[16 * g + 2 * j + 1]), gamma);
+          f[g + j] = __fmul_rn(__uint_as_float(v[g + 2 * j]), gamma);
+          f[g + 8 + j] = __fmul_rn(__uint_as_float(v[g + 2 * j + 1]), gamma);
         }
-        if (m < a.M) store16<OutT>(a.dx, m * a.K, k0 + c + 16 * g, a.K, f, a.vec);
+      if (fix && m < a.M  // (every CTA that saw one adds the same infinities and NaN)
+           && s_ids[trow + lane] >= 0)
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (k0 + c + j < a.K)
+            f[j] = __fadd_rn(f[j], gi_nonfinite(a.v, a.A, s_ids[trow + lane], a.r, static_cast<int>(m), k0 + c + j, a.K));
+      if constexpr (H == 1) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+          *reinterpret_cast<float4*>(tile + (trow + lane) * kGiTilePitch + c + j) =
+              make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+      } else if (a.vec) {
+#pragma unroll
+        for (int g = 0; g < 32; g += 16) {
+          float o[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = f[g + j];
+          if (m < a.M) store16<OutT>(a.dx, m * a.K, k0 + c + g, a.K, o, true);
+        }
+      } else {  // turned, so that a warp stores consecutive columns
+        float* patch = tile + (warp - 2) * (32 * 33);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) patch[lane * 33 + j] = f[j];
+        __syncwarp();
+        const int k = k0 + c + lane, rows = min(32, a.M - m0 - trow);
+        if (k < a.K)
+          for (int x = 0; x < rows; ++x)
+            store_out<OutT>(a.dx, static_cast<int64_t>(m0 + trow + x) * a.K + k, patch[x * 33 + lane]);
       }
     }
+  }
+  if constexpr (H == 1) {
+    __syncwarp();
+    if (CS > 1) cluster_sync_all();
+    else __syncthreads();
+    // this CTA's rows of the finished tile, four columns a thread
+    const int rows = 128 / CS, row0 = z * rows;
+    if (*abort_flag == 0)
+      for (int e = threadIdx.x; e < rows * (kGiBN / 4); e += kGiThreads) {
+        const int row = row0 + e / (kGiBN / 4), c = e % (kGiBN / 4) * 4, k = k0 + c;
+        if (m0 + row >= a.M || k >= a.K) continue;
+        const float* p = tile + row * kGiTilePitch + c;
+        float4 v = *reinterpret_cast<const float4*>(p);
+        if (CS > 1) v = cluster_total4(p, CS);
+        const int64_t at = static_cast<int64_t>(m0 + row) * a.K + k;
+        if (a.vec) {
+          if constexpr (sizeof(OutT) == 4)
+            *reinterpret_cast<float4*>(static_cast<float*>(a.dx) + at) = v;
+          else
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.dx) + at) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+        } else {
+          store_out<OutT>(a.dx, at, v.x);
+          if (k + 1 < a.K) store_out<OutT>(a.dx, at + 1, v.y);
+          if (k + 2 < a.K) store_out<OutT>(a.dx, at + 2, v.z);
+          if (k + 3 < a.K) store_out<OutT>(a.dx, at + 3, v.w);
+        }
+      }
+    __syncwarp();
+    if (CS > 1) cluster_sync_all();  // the tile stays until it is read
   }
   tc_fence_before();
   __syncthreads();

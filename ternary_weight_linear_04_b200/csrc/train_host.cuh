@@ -108,18 +108,56 @@ inline bl_status dy_rows(const void* dy, bl_dtype dydt, int64_t M, int64_t N, Sc
                     static_cast<const float*>(dy), M, N, cols, static_cast<__nv_bfloat16*>(dst));
 }
 
+// How many clusters of cs CTAs of a kernel the device holds at once (clusters
+// stay within a part of the GPU: 16 CTAs' worth of eight do not fit 148 SMs
+// where each takes one).  Asked once per device and size.
+template <typename Kern>
+int cluster_room(Kern kern, int threads, size_t smem, int cs, int (*known)[9]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 1;
+  int& room = known[dev][cs];
+  if (room) return room;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1, 1, static_cast<unsigned>(cs));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = static_cast<unsigned>(cs);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    n = 1;
+  }
+  return room = n;
+}
+
 // Whether rows of `cols` values of type dt take 16-byte stores.
 inline int vec_rows(int64_t cols, bl_dtype dt) { return cols % (16 / dtype_bytes(dt)) == 0 ? 1 : 0; }
 
 template <int H, typename OutT>
 bl_status launch_gi(const CUtensorMap& tdy, const CUtensorMap& tw, const bl::GiArgs& a, cudaStream_t s) {
-  static int done[kMaxDevices] = {0};
+  static int done[kMaxDevices] = {0}, room[kMaxDevices][9] = {{0}};
   auto kern = bl::k_grad_input<H, OutT>;
   constexpr size_t smem = bl::GiCfg<H>::kSmem;
   if (!ensure_smem(kern, smem, done)) return BL_ERR_CUDA;
   const int64_t tiles = ((a.K + bl::kGiBN - 1) / bl::kGiBN) * ((int64_t{a.M} + 128 * H - 1) / (128 * H));
   if (tiles > INT32_MAX) return BL_ERR_UNSUPPORTED;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(tiles)), dim3(bl::kGiThreads), smem, s, tdy, tw, a);
+  int split = 1;
+  if (H == 1) {
+    // as many CTAs along the contraction as the GPU has room for beside the
+    // tiles (a power of two, so that they share the tile's rows evenly), four
+    // steps each at least.  77 x 3200 x 8640, 34 tiles: 32 us with one CTA a
+    // tile, 21 with two, 27 with four, which do not all fit
+    const int64_t steps = (int64_t{a.N} + bl::kGiBK - 1) / bl::kGiBK * a.planes;
+    while (split < 8 && steps >= 8 * split && tiles <= cluster_room(kern, bl::kGiThreads, smem, 2 * split, room)) split *= 2;
+  }
+  const dim3 grid(static_cast<unsigned>(tiles), 1, static_cast<unsigned>(split));
+  return launch_pdl_cluster(kern, grid, dim3(bl::kGiThreads), smem, s, grid.z, tdy, tw, a);
 }
 
 // dx = gamma dy W~ (+ v A where a.v is given); the operands' copies come out of ws.
@@ -131,7 +169,9 @@ bl_status run_grad_input(const void* dyp, bl_dtype dydt, const uint8_t* packed, 
   if (st != BL_OK) return st;
   pad_rows(packed, a.N, (a.K + 3) / 4, 16, ws, &w, &pads);
   if ((st = run_pads(pads, sms, s)) != BL_OK) return st;
-  const int H = a.M > 128 ? 2 : 1;
+  // 256 tokens a tile where such tiles fill most of the GPU, else 128
+  const int64_t ktiles = (a.K + bl::kGiBN - 1) / bl::kGiBN;
+  const int H = a.M > 128 && ktiles * ((a.M + 255) / 256) * 4 > int64_t{3} * sms ? 2 : 1;
   CUtensorMap tdy, tw;
   if (!make_tmap(&tdy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy.p, a.N, a.M, dy.planes, dy.stride, bl::kGiBK, 128 * H,
                  CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -140,7 +180,8 @@ bl_status run_grad_input(const void* dyp, bl_dtype dydt, const uint8_t* packed, 
     return BL_ERR_CUDA;
   a.planes = dy.planes;
   a.vec = vec_rows(a.K, dxdt);
-  if (H == 2) return dxdt == BL_F32 ? launch_gi<2, float>(tdy, tw, a, s) : launch_gi<2, __nv_bfloat16>(tdy, tw, a, s);
+  if (H == 2)
+    return dxdt == BL_F32 ? launch_gi<2, float>(tdy, tw, a, s) : launch_gi<2, __nv_bfloat16>(tdy, tw, a, s);
   return dxdt == BL_F32 ? launch_gi<1, float>(tdy, tw, a, s) : launch_gi<1, __nv_bfloat16>(tdy, tw, a, s);
 }
 
@@ -245,9 +286,9 @@ bl_status launch_uv(const void* dy, bl_dtype dydt, const int8_t* xq, const float
   int64_t steps = out_v ? (N + 63) / 64 : 0;
   if (out_u && (K + 63) / 64 > steps) steps = (K + 63) / 64;
   if (out_v && dydt == BL_F32) return launch_uv_rt<float, 1>(g, n, steps, sms, s);
-  // 64 tokens a CTA read a factor a quarter as often as 16, which fill the
-  // GPU sooner: from 512 tokens on
-  return M > 512 ? launch_uv_rt<__nv_bfloat16, 4>(g, n, steps, sms, s) : launch_uv_rt<__nv_bfloat16, 1>(g, n, steps, sms, s);
+  // 32 tokens a CTA read a factor half as often as 16, which fill the GPU
+  // sooner: from 512 tokens on
+  return M > 512 ? launch_uv_rt<__nv_bfloat16, 2>(g, n, steps, sms, s) : launch_uv_rt<__nv_bfloat16, 1>(g, n, steps, sms, s);
 }
 
 template <typename DyT, typename OutT, int JT>
@@ -265,7 +306,7 @@ bl_status launch_dab(const void* dy, const int8_t* xq, const float* eta, int64_t
   const int64_t sa = (K + bl::kDabCols - 1) / bl::kDabCols, sb = (N + bl::kDabCols - 1) / bl::kDabCols;
   bl::DabArgs g = {};
   g.a = {xq, K, v, dA, K % 16 == 0 ? 1 : 0};
-  g.b = {dy, N, u, dB, N % 8 == 0 ? 1 : 0};
+  g.b = {dy, N, u, dB, N % (sizeof(DyT) == 4 ? 4 : 8) == 0 ? 1 : 0};
   g.eta = eta; g.ids = ad.ids; g.M = M; g.r = ad.r; g.slabs_a = static_cast<unsigned>(sa);
   // CTAs of a cluster along the tokens: while there are fewer than four CTAs
   // an SM, and two chunks of tokens for each

@@ -49,31 +49,6 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
   return reinterpret_cast<const uint32_t&>(d);
 }
 
-// Four values of a row as two bf16 pairs (0, 1) and (2, 3): part p of fp32.
-template <typename T>
-__device__ __forceinline__ uint2 load4_bf16(const T* p, int64_t left, bool vec, int part) {
-  if constexpr (sizeof(T) == 2) {
-    if (vec) return left > 0 ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
-    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-    uint32_t v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < left ? __ldg(h + i) : 0u;
-    return make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
-  } else {
-    float f[4];
-    if (vec) {
-      const float4 v = left > 0 ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(0, 0, 0, 0);
-      f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = i < left ? __ldg(p + i) : 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = bf16_part<3>(f[i], part);
-    return make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
-  }
-}
-
 // ---------------------------------------------------------------- u of up to 16 tokens
 //
 // Few tokens: every (token, rank index) is a dot product over K that reads
@@ -200,17 +175,18 @@ __global__ void __launch_bounds__(kAuThreads)
 
 // ---------------------------------------------------------------- u and v of many tokens
 //
-// One CTA per 16 RT tokens and part of the contraction (a cluster splits it
-// and adds the parts through distributed shared memory); the four warps take
-// its steps of 64 in turn, each for all the tokens, so every factor is read
-// once per CTA.  Products on mma.sync m16n8k16: bf16 by bf16, fp32 sums; x~ is
-// exact in bf16, an fp32 dy goes in as three parts.  (tcgen05 would need its
-// operands in shared memory: the work is small beside reading dy, and these
-// fragments come straight from global memory.)  The order of the contraction
-// is free, so lane q of a row reads 16 consecutive codes, and A's row the
-// same 16; for v, B's rows lie across the contraction and pass through shared
-// memory (ldmatrix.trans).  A row's fragment is zeroed for the adapters that
-// are not its own.
+// One CTA per 16 tokens; its 16 warps take the contraction's steps of 64 in
+// turn and add their sums at the end (with few tokens a cluster splits the
+// contraction too).  Products on mma.sync m16n8k16: bf16 by bf16, fp32 sums;
+// x~ is exact in bf16, an fp32 dy goes in as three parts.  (tcgen05 would need
+// its operands in shared memory: the work is small beside reading dy, and
+// these fragments come straight from global memory.)  The order of the
+// contraction is free, so lane q of a row reads 16 consecutive codes, and A's
+// row the same 16; for v, B's rows lie across the contraction and pass
+// through shared memory (ldmatrix.trans).  A row's fragment is zeroed for the
+// adapters that are not its own.  The tokens' values of the next step are
+// loaded while this one's are multiplied: a warp's steps are a chain of
+// loads, and the time of the kernel.
 
 struct UvSide {
   int is_v;                // u: x = codes, F = A; v: x = dy, F = B
@@ -230,9 +206,12 @@ struct UvArgs {
   int L, r;
 };
 
-constexpr int kUvThreads = 128;
-constexpr int kUvRedPitch = 40;
-constexpr int kUvPitch = 40;  // bf16 of a staged row of B: 32 and 8 that spread the banks
+constexpr int kUvWarps = 16;
+constexpr int kUvThreads = 32 * kUvWarps;
+constexpr int kUvRedPitch = 40;  // floats of a row of sums: 32 and 8 that spread the banks
+constexpr int kUvPitch = 40;     // bf16 of a staged row of B, the same
+constexpr size_t kUvSmem = kUvWarps * 64 * kUvPitch * 2;  // staged rows; the sums (16 rows a warp) take half
+static_assert(kUvWarps * 16 * kUvRedPitch * 4 <= kUvSmem, "the sums in the staged rows' place");
 
 // The plain sum for one output, where a factor is not finite.
 template <typename DyT>
@@ -247,237 +226,268 @@ __device__ __noinline__ float uv_plain(const UvArgs& g, const UvSide& s, int64_t
   return t;
 }
 
-// DyT void: u.  smem: the four warps' partial sums (16 RT x 32 each) or
-// their staged rows of B (64 x kUvPitch).
-template <typename XT, int RT>
+// A lane's share of two token rows (g and g + 8) at a step: 16 codes from
+// 16 q on, or values 16 i + 4 q .. + 3 for each of the step's four MMAs.
+template <typename XT>
+struct UvRaw {
+  static constexpr int kWords = 4 * static_cast<int>(sizeof(XT));
+  uint32_t w[2][kWords];
+
+  __device__ __forceinline__ void load(const XT* const (&row)[2], int64_t k0, int64_t C, int q, bool vec) {
+    constexpr int kEach = sizeof(XT) == 1 ? 16 : 4;  // values in a row
+    constexpr int kW = kEach * static_cast<int>(sizeof(XT)) / 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 16 / kEach; ++i) {
+        const int64_t k = k0 + (sizeof(XT) == 1 ? 16 * q : 16 * i + 4 * q);
+        const XT* p = row[h] + k;
+        uint32_t* o = w[h] + kW * i;
+#pragma unroll
+        for (int j = 0; j < kW; ++j) o[j] = 0;
+        if (vec) {
+          if (k < C) {
+            if constexpr (kW == 2) {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+              o[0] = v.x; o[1] = v.y;
+            } else {
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+              o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kEach; ++j) {
+            if (k + j >= C) continue;
+            if constexpr (sizeof(XT) == 1) o[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(__ldg(p + j))) << (8 * (j & 3));
+            else if constexpr (sizeof(XT) == 2) o[j >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + j)) << (16 * (j & 1));
+            else o[j] = __ldg(reinterpret_cast<const uint32_t*>(p) + j);
+          }
+        }
+      }
+  }
+
+  // A fragment of MMA i: registers 0, 1 the rows' first pairs, 2, 3 the
+  // second (of codes 0, 2 and 1, 3 of the four); `own`: the rows' masks.
+  __device__ __forceinline__ void fragment(uint32_t (&xf)[4], int i, int part, const uint32_t (&own)[2]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (sizeof(XT) == 1) {
+        xf[h] = codes_bf16(w[h][i]);
+        xf[2 + h] = codes_bf16(w[h][i] >> 8);
+      } else if constexpr (sizeof(XT) == 2) {
+        xf[h] = w[h][2 * i];
+        xf[2 + h] = w[h][2 * i + 1];
+      } else {
+        float f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = bf16_part<3>(__uint_as_float(w[h][4 * i + j]), part);
+        xf[h] = pack_bf16(f[0], f[1]);
+        xf[2 + h] = pack_bf16(f[2], f[3]);
+      }
+      xf[h] &= own[h];
+      xf[2 + h] &= own[h];
+    }
+  }
+};
+
+template <typename XT>
 __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_t* smem, const int* s_ids,
                                         const int* s_list, int nad, volatile float* s_bad) {
   constexpr bool V = sizeof(XT) > 1;
-  constexpr int T = 16 * RT, PX = sizeof(XT) == 4 ? 3 : 1;
+  constexpr int PX = sizeof(XT) == 4 ? 3 : 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, q = lane & 3;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * T;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16;
   const int CS = static_cast<int>(cluster_nctarank()), z = CS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int64_t C = s.C, nst = (C + 63) >> 6;
-  const int64_t lo = nst * z / CS, hi = nst * (z + 1) / CS;
+  const int64_t C = s.C;
+  const int64_t nst = (C + 63) >> 6;
+  const int step = kUvWarps * CS;
   const int r = g.r;
   const bool vec = s.vec != 0, bvec = (r & 7) == 0;
   float* red = reinterpret_cast<float*>(smem);
   __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(smem) + warp * 64 * kUvPitch;
-  int id[RT][2];
-  const XT* row[RT][2];
-#pragma unroll
-  for (int t = 0; t < RT; ++t)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int m = 16 * t + 8 * h + gr;
-      id[t][h] = s_ids[m];
-      row[t][h] = static_cast<const XT*>(s.x) + min(m0 + m, g.M - 1) * C;  // rows past M repeat the last, unused
-    }
+  const int id0 = s_ids[gr], id1 = s_ids[8 + gr];
+  const XT* const row[2] = {static_cast<const XT*>(s.x) + min(m0 + gr, g.M - 1) * C,  // rows past M repeat the last
+                            static_cast<const XT*>(s.x) + min(m0 + 8 + gr, g.M - 1) * C};
   for (int jb = 0; jb < r; jb += 32) {
     const int nt = min(4, (r - jb + 7) >> 3);
-    float acc[RT][4][4];
+    float acc[4][4];
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][n][i] = 0.0f;
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
     bool bad = false;
-    for (int64_t st = lo + warp; nad && st < hi; st += 4) {
+    constexpr bool kAhead = sizeof(XT) < 4;  // fp32 rows: not enough registers for two steps
+    UvRaw<XT> next;
+    const int64_t first = warp * CS + z;
+    if (kAhead && nad && first < nst) next.load(row, first << 6, C, q, vec);
+    for (int64_t st = first; nad && st < nst; st += step) {
       const int64_t k0 = st << 6;
-#pragma unroll 1
-      for (int part = 0; part < PX; ++part) {
-        uint32_t xf[RT][4][4];
+      UvRaw<XT> raw;
+      if constexpr (kAhead) {
+        raw = next;
+        if (st + step < nst) next.load(row, (st + step) << 6, C, q, vec);
+      } else {
+        raw.load(row, k0, C, q, vec);
+      }
+      for (int li = 0; li < nad; ++li) {
+        const int a = s_list[li];
+        const uint32_t own[2] = {id0 == a ? 0xFFFFFFFFu : 0u, id1 == a ? 0xFFFFFFFFu : 0u};
+        if constexpr (!V) {
+          const int64_t k = k0 + 16 * q;
+          uint4 wf[4][2];  // A's rows: 8 rank indices each, 16 values
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if constexpr (!V) {
-              const int64_t k = k0 + 16 * q;
-              uint32_t w[4] = {0, 0, 0, 0};
+          for (int n = 0; n < 4; ++n) {
+            uint4(&w)[2] = wf[n];
+            w[0] = w[1] = make_uint4(0, 0, 0, 0);
+            if (n >= nt) continue;
+            const int j = jb + 8 * n + gr;
+            const __nv_bfloat16* f = s.F + (static_cast<int64_t>(a) * r + j) * C + k;
+            if (j < r && k < C) {
               if (vec) {
-                if (k < C) {
-                  const uint4 v = __ldg(reinterpret_cast<const uint4*>(row[t][h] + k));
-                  w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-                }
+                w[0] = __ldg(reinterpret_cast<const uint4*>(f));
+                w[1] = __ldg(reinterpret_cast<const uint4*>(f) + 1);
               } else {
+                uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                  if (k + i < C) w[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(row[t][h][k + i])) << (8 * (i & 3));
-              }
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                xf[t][i][h] = codes_bf16(w[i]);           // codes 0, 2 of the four
-                xf[t][i][2 + h] = codes_bf16(w[i] >> 8);  // 1, 3
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int64_t k = k0 + 16 * i + 4 * q;
-                const uint2 w = load4_bf16(row[t][h] + k, C - k, vec, part);
-                xf[t][i][h] = w.x;
-                xf[t][i][2 + h] = w.y;
+                  if (k + i < C)
+                    e[i >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(f) + i)) << (16 * (i & 1));
+                w[0] = make_uint4(e[0], e[1], e[2], e[3]);
+                w[1] = make_uint4(e[4], e[5], e[6], e[7]);
               }
             }
           }
-        for (int li = 0; li < nad; ++li) {
-          const int a = s_list[li];
-          uint32_t b[4][4][2];  // [MMA][8 rank indices][register]
-          if constexpr (!V) {
-            const int64_t k = k0 + 16 * q;
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+            if (nonfinite8(wf[n][0]) || nonfinite8(wf[n][1])) {
+              bad = true;
+              wf[n][0] = wf[n][1] = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t xf[4];
+            raw.fragment(xf, i, 0, own);
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
               if (n >= nt) continue;
-              uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-              const int j = jb + 8 * n + gr;
-              const __nv_bfloat16* f = s.F + (static_cast<int64_t>(a) * r + j) * C + k;
-              if (j < r && k < C) {
-                if (vec) {
-                  w[0] = __ldg(reinterpret_cast<const uint4*>(f));
-                  w[1] = __ldg(reinterpret_cast<const uint4*>(f) + 1);
-                } else {
-                  uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+              const uint4 w = wf[n][i >> 1];
+              const uint32_t lo = (i & 1) ? w.z : w.x, hi = (i & 1) ? w.w : w.y;
+              mma_bf16_16816(acc[n], xf[0], xf[1], xf[2], xf[3], __byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+            }
+          }
+        } else {
+          const __nv_bfloat16* f = s.F + (a * C + k0) * r + jb;
+          __syncwarp();
+          if (bvec) {  // every load in flight at once
+            uint4 w[8];
 #pragma unroll
-                  for (int i = 0; i < 16; ++i)
-                    if (k + i < C)
-                      e[i >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(f) + i)) << (16 * (i & 1));
-                  w[0] = make_uint4(e[0], e[1], e[2], e[3]);
-                  w[1] = make_uint4(e[4], e[5], e[6], e[7]);
-                }
-              }
-              if (nonfinite8(w[0]) || nonfinite8(w[1])) {
+            for (int x = 0; x < 8; ++x) {
+              const int i = lane + 32 * x, n = i / nt, c = i - n * nt;
+              w[x] = x < 2 * nt && k0 + n < C ? __ldg(reinterpret_cast<const uint4*>(f + static_cast<int64_t>(n) * r) + c)
+                                              : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              if (x >= 2 * nt) continue;
+              const int i = lane + 32 * x, n = i / nt, c = i - n * nt;
+              if (nonfinite8(w[x])) {
                 bad = true;
-                w[0] = w[1] = make_uint4(0, 0, 0, 0);
+                w[x] = make_uint4(0, 0, 0, 0);
               }
-              const uint32_t e[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                b[i][n][0] = __byte_perm(e[2 * i], e[2 * i + 1], 0x5410);
-                b[i][n][1] = __byte_perm(e[2 * i], e[2 * i + 1], 0x7632);
-              }
+              *reinterpret_cast<uint4*>(stage + n * kUvPitch + 8 * c) = w[x];
             }
-          } else {
-            const __nv_bfloat16* f = s.F + (a * C + k0) * r + jb;
-            __syncwarp();
-            if (bvec) {  // every load in flight at once
-              uint4 w[8];
-#pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                const int i = lane + 32 * x, n = i / nt, c = i - n * nt;
-                w[x] = x < 2 * nt && k0 + n < C ? __ldg(reinterpret_cast<const uint4*>(f + static_cast<int64_t>(n) * r) + c)
-                                                : make_uint4(0, 0, 0, 0);
-              }
-#pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                if (x >= 2 * nt) continue;
-                const int i = lane + 32 * x, n = i / nt, c = i - n * nt;
-                if (nonfinite8(w[x])) {
-                  bad = true;
-                  w[x] = make_uint4(0, 0, 0, 0);
-                }
-                *reinterpret_cast<uint4*>(stage + n * kUvPitch + 8 * c) = w[x];
-              }
-            } else {  // value by value, 16 in flight
-              const int cols = 8 * nt;
+          } else {  // value by value, 16 in flight
+            const int cols = 8 * nt;
 #pragma unroll 1
-              for (int i0 = lane; i0 < 64 * cols; i0 += 512) {
-                uint16_t w[16];
+            for (int i0 = lane; i0 < 64 * cols; i0 += 512) {
+              uint16_t w[16];
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                  const int i = i0 + 32 * x, n = i / cols, j = i - n * cols;
-                  w[x] = k0 + n < C && jb + j < r
-                             ? __ldg(reinterpret_cast<const uint16_t*>(f) + static_cast<int64_t>(n) * r + j) : 0;
-                }
+              for (int x = 0; x < 16; ++x) {
+                const int i = i0 + 32 * x, n = i / cols, j = i - n * cols;
+                w[x] = k0 + n < C && jb + j < r
+                           ? __ldg(reinterpret_cast<const uint16_t*>(f) + static_cast<int64_t>(n) * r + j) : 0;
+              }
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                  const int i = i0 + 32 * x, n = i / cols, j = i - n * cols;
-                  if (nonfinite2(w[x])) {
-                    bad = true;
-                    w[x] = 0;
-                  }
-                  reinterpret_cast<uint16_t*>(stage)[n * kUvPitch + j] = w[x];
+              for (int x = 0; x < 16; ++x) {
+                const int i = i0 + 32 * x, n = i / cols, j = i - n * cols;
+                if (nonfinite2(w[x])) {
+                  bad = true;
+                  w[x] = 0;
                 }
+                reinterpret_cast<uint16_t*>(stage)[n * kUvPitch + j] = w[x];
               }
             }
-            __syncwarp();
-            // matrix lane / 8: rows of the contraction 0 1 4 5 .. (registers
-            // 0) or 2 3 6 7 .. (1), rank indices 0-7 or 8-15 of the pair
-            const int mat = lane >> 3, kk = lane & 7;
-            const __nv_bfloat16* at = stage + (4 * (kk >> 1) + (kk & 1) + 2 * (mat & 1)) * kUvPitch + 8 * (mat >> 1);
+          }
+          __syncwarp();
+          // matrix lane / 8: rows of the contraction 0 1 4 5 .. (registers
+          // 0) or 2 3 6 7 .. (1), rank indices 0-7 or 8-15 of the pair
+          const int mat = lane >> 3, kk = lane & 7;
+          const __nv_bfloat16* at = stage + (4 * (kk >> 1) + (kk & 1) + 2 * (mat & 1)) * kUvPitch + 8 * (mat >> 1);
+#pragma unroll 1
+          for (int part = 0; part < PX; ++part)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+              uint32_t xf[4];
+              raw.fragment(xf, i, part, own);
 #pragma unroll
               for (int n = 0; n < 4; n += 2) {
                 if (n >= nt) continue;
                 uint32_t d[4];
-                ldmatrix_x4_trans(d, at + 16 * i * kUvPitch + 8 * n);  // an odd nt: the second half is not used
-                b[i][n][0] = d[0];
-                b[i][n][1] = d[1];
-                b[i][n + 1][0] = d[2];
-                b[i][n + 1][1] = d[3];
+                ldmatrix_x4_trans(d, at + 16 * i * kUvPitch + 8 * n);
+                mma_bf16_16816(acc[n], xf[0], xf[1], xf[2], xf[3], d[0], d[1]);
+                // an odd nt: the staged columns behind it hold anything, and
+                // neither do their sums go anywhere
+                mma_bf16_16816(acc[n + 1], xf[0], xf[1], xf[2], xf[3], d[2], d[3]);
               }
-          }
-#pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            const bool m0own = id[t][0] == a, m1own = id[t][1] == a;
-            if (!__any_sync(0xFFFFFFFFu, m0own || m1own)) continue;
-            const uint32_t k0m = m0own ? 0xFFFFFFFFu : 0u, k1m = m1own ? 0xFFFFFFFFu : 0u;
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              if (n >= nt) continue;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mma_bf16_16816(acc[t][n], xf[t][i][0] & k0m, xf[t][i][1] & k1m, xf[t][i][2] & k0m, xf[t][i][3] & k1m,
-                               b[i][n][0], b[i][n][1]);
             }
-          }
         }
       }
-    }
+  }
     if (bad) *s_bad = 1.0f;
     __syncthreads();  // the staged rows are read
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2*>(red + (warp * T + 16 * t + 8 * h + gr) * kUvRedPitch + 8 * n + 2 * q) =
-              make_float2(acc[t][n][2 * h], acc[t][n][2 * h + 1]);
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2*>(red + (warp * 16 + 8 * h + gr) * kUvRedPitch + 8 * n + 2 * q) =
+            make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
     __syncthreads();
-    for (int e = tid; e < T * 32; e += kUvThreads) {
-      float* p = red + (e >> 5) * kUvRedPitch + (e & 31);
-      constexpr int kWarp = T * kUvRedPitch;
-      *p = __fadd_rn(__fadd_rn(p[0], p[kWarp]), __fadd_rn(p[2 * kWarp], p[3 * kWarp]));
-    }
-    if (CS > 1) cluster_sync_all();
-    else __syncthreads();
-    const bool any = (CS > 1 ? cluster_total(const_cast<float*>(s_bad), CS) : *s_bad) != 0.0f;
-    for (int e = z * kUvThreads + tid; e < T * 32; e += CS * kUvThreads) {
-      const int m = e >> 5, j = jb + (e & 31), a = s_ids[m];
-      if (j >= r || m0 + m >= g.M) continue;
-      float v = 0.0f;
-      if (a >= 0) {
-        const float* p = red + m * kUvRedPitch + (e & 31);
-        v = CS > 1 ? cluster_total(p, CS) : *p;
-        if (any) v = uv_plain<typename std::conditional<V, XT, float>::type>(g, s, m0 + m, a, j);
-        if constexpr (!V) v = __fmul_rn(v, div127_rn(s.eta[m0 + m]));
-        v = __fmul_rn(v, g.scale[a]);
+    static_assert(kUvThreads == 16 * 32, "one sum a thread");
+    float* mine = red + (tid >> 5) * kUvRedPitch + (tid & 31);
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kUvWarps; ++w) t = __fadd_rn(t, mine[w * 16 * kUvRedPitch]);
+    bool any = *s_bad != 0.0f;
+    if (CS > 1) {  // CTA 0 adds the cluster's
+      *mine = t;
+      cluster_sync_all();
+      if (z == 0) {
+        t = cluster_total(mine, CS);
+        any = cluster_total(const_cast<float*>(s_bad), CS) != 0.0f;
       }
-      s.out[(m0 + m) * r + j] = v;
+    }
+    const int m = tid >> 5, j = jb + (tid & 31), a = s_ids[m];
+    if (z == 0 && j < r && m0 + m < g.M) {
+      if (a >= 0) {
+        if (any) t = uv_plain<typename std::conditional<V, XT, float>::type>(g, s, m0 + m, a, j);
+        if constexpr (!V) t = __fmul_rn(t, div127_rn(s.eta[m0 + m]));
+        t = __fmul_rn(t, g.scale[a]);
+      } else {
+        t = 0.0f;
+      }
+      s.out[(m0 + m) * r + j] = t;
     }
     if (CS > 1) cluster_sync_all();
     else __syncthreads();
   }
 }
 
-// Grid (tiles of 16 RT tokens, sides, CTAs of a cluster).
-template <typename DyT, int RT>
-__global__ void __launch_bounds__(kUvThreads, 3) k_adapter_uv(const __grid_constant__ UvArgs g) {
-  constexpr int T = 16 * RT;
-  constexpr int kStage = 4 * 64 * kUvPitch * 2, kRed = 4 * T * kUvRedPitch * 4;
-  __shared__ __align__(16) uint8_t smem[kStage > kRed ? kStage : kRed];
-  __shared__ int s_ids[T < 32 ? 32 : T], s_list[T], s_cnt[8];
+// Grid (tiles of 16 tokens, sides, CTAs of a cluster).
+template <typename DyT>
+__global__ void __launch_bounds__(kUvThreads, 1) k_adapter_uv(const __grid_constant__ UvArgs g) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int s_ids[32], s_list[32], s_cnt[8];
   __shared__ float s_bad;  // not zero: a factor is not finite
   pdl_wait();
   if (threadIdx.x == 0) {
@@ -485,9 +495,9 @@ __global__ void __launch_bounds__(kUvThreads, 3) k_adapter_uv(const __grid_const
     s_bad = 0.0f;
   }
   const UvSide& s = g.side[blockIdx.y];
-  const int nad = tile_adapters(g.ids, static_cast<int64_t>(blockIdx.x) * T, g.M, T, g.L, s_ids, s_list, s_cnt);
-  if (s.is_v) uv_tile<DyT, RT>(g, s, smem, s_ids, s_list, nad, &s_bad);
-  else uv_tile<int8_t, RT>(g, s, smem, s_ids, s_list, nad, &s_bad);
+  const int nad = tile_adapters(g.ids, static_cast<int64_t>(blockIdx.x) * 16, g.M, 16, g.L, s_ids, s_list, s_cnt);
+  if (s.is_v) uv_tile<DyT>(g, s, smem, s_ids, s_list, nad, &s_bad);
+  else uv_tile<int8_t>(g, s, smem, s_ids, s_list, nad, &s_bad);
 }
 
 // ---------------------------------------------------------------- dA and dB

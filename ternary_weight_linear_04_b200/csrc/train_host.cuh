@@ -263,16 +263,19 @@ bl_status launch_u_few(const void* x, int8_t* xq, float* eta, int32_t* xsum, int
                     static_cast<int>(K), ad.A, ad.scale, ad.ids, ad.L, ad.r, static_cast<int>(group), u);
 }
 
-template <typename DyT, int RT>
-bl_status launch_uv_rt(const bl::UvArgs& g, int sides, int64_t steps, int sms, cudaStream_t s) {
-  const int64_t tiles = (g.M + 16 * RT - 1) / (16 * RT);
-  // CTAs of a cluster along the contraction: as many as the GPU has room for
-  // (four of these CTAs an SM), no less than a step for each of their warps
-  int cs = 8;
-  while (cs > 1 && (tiles * sides * cs > 8 * sms || 4 * cs > steps + 3)) cs /= 2;
+template <typename DyT>
+bl_status launch_uv_t(const bl::UvArgs& g, int sides, int64_t steps, int sms, cudaStream_t s) {
+  static int done[kMaxDevices] = {0};
+  auto kern = bl::k_adapter_uv<DyT>;
+  if (!ensure_smem(kern, bl::kUvSmem, done)) return BL_ERR_CUDA;
+  const int64_t tiles = (g.M + 15) / 16;
   if (tiles > INT32_MAX) return BL_ERR_UNSUPPORTED;
+  // CTAs of a cluster along the contraction: while they fit beside one
+  // another and a warp keeps two steps
+  int cs = 1;
+  while (cs < 4 && tiles * sides * cs * 2 <= sms && steps >= 4 * bl::kUvWarps * cs) cs *= 2;
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(sides), static_cast<unsigned>(cs));
-  return launch_pdl_cluster(bl::k_adapter_uv<DyT, RT>, grid, dim3(bl::kUvThreads), 0, s, static_cast<unsigned>(cs), g);
+  return launch_pdl_cluster(kern, grid, dim3(bl::kUvThreads), bl::kUvSmem, s, grid.z, g);
 }
 
 // u (where out_u is given) and v (out_v) of any number of tokens.
@@ -285,10 +288,7 @@ bl_status launch_uv(const void* dy, bl_dtype dydt, const int8_t* xq, const float
   if (out_u) g.side[n++] = {0, xq, K, ad.A, eta, out_u, K % 16 == 0 ? 1 : 0};
   int64_t steps = out_v ? (N + 63) / 64 : 0;
   if (out_u && (K + 63) / 64 > steps) steps = (K + 63) / 64;
-  if (out_v && dydt == BL_F32) return launch_uv_rt<float, 1>(g, n, steps, sms, s);
-  // 32 tokens a CTA read a factor half as often as 16, which fill the GPU
-  // sooner: from 512 tokens on
-  return M > 512 ? launch_uv_rt<__nv_bfloat16, 2>(g, n, steps, sms, s) : launch_uv_rt<__nv_bfloat16, 1>(g, n, steps, sms, s);
+  return out_v && dydt == BL_F32 ? launch_uv_t<float>(g, n, steps, sms, s) : launch_uv_t<__nv_bfloat16>(g, n, steps, sms, s);
 }
 
 template <typename DyT, typename OutT, int JT>

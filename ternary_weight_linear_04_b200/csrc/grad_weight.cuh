@@ -7,7 +7,7 @@
 // The tokens are int8 already.  The other factor, g[m,n] = dy[m,n] f_m, is
 // held in fixed point: over each chunk of 512 tokens a column n gets the
 // power of two that brings its largest |g| just below the top of ND signed
-// base-256 digits (k_gw_digits), q = round(g 2^e) = sum_j d_j 256^j with
+// base-256 digits (k_gw_operands), q = round(g 2^e) = sum_j d_j 256^j with
 // d_j in [-128, 127].  The MMA sums d_j x~ over a chunk without any rounding
 // (at most 512 * 128 * 127 < 2^23), and the epilogue adds D_j 256^j 2^-e to
 // fp32 accumulators in registers.  ND = 3 (23 bits beside the column's
@@ -21,7 +21,7 @@
 // the time of 1 or 1.5 bf16 products and sum exactly.
 //
 // Both operands are rewritten once with the tokens contiguous (K-major):
-// the digits by k_gw_digits, the codes by k_gw_codes.
+// by k_gw_operands.
 #pragma once
 
 #include <cuda.h>
@@ -66,16 +66,55 @@ __device__ __forceinline__ uint32_t biased_round(float p) {
   }
 }
 
+// The codes with the tokens contiguous: a tile of 64 inputs by 128 tokens of
+// xt (K x Mp) from xq (M x K), zero past M, transposed 4 x 4 bytes at a time
+// on the way into shared memory.
+__device__ __forceinline__ void gw_codes_tile(const int8_t* __restrict__ xq, int64_t M, int64_t K, int64_t Mp,
+                                              int64_t at, uint32_t (&tile)[64][33], uint8_t* __restrict__ xt) {
+  const int64_t ktiles = (K + 63) / 64;
+  const int64_t k0 = (at % ktiles) * 64, m0 = (at / ktiles) * 128;
+  const int kq = threadIdx.x & 15, mq = threadIdx.x >> 4;
+  const int64_t k = k0 + 4 * kq, m = m0 + 4 * mq;
+  uint32_t w[4], o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = 0;
+    if (m + i < M && k < K) {
+      const int8_t* p = xq + (m + i) * K + k;
+      if ((K & 3) == 0) {
+        w[i] = __ldg(reinterpret_cast<const uint32_t*>(p));
+      } else {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (k + b < K) w[i] |= static_cast<uint32_t>(static_cast<uint8_t>(__ldg(p + b))) << (8 * b);
+      }
+    }
+  }
+  transpose4x4_bytes(w[0], w[1], w[2], w[3], o[0], o[1], o[2], o[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tile[4 * kq + i][mq] = o[i];
+  __syncthreads();
+  const int row = threadIdx.x >> 3, c = threadIdx.x & 7;
+  const int64_t mc = m0 + 16 * c;
+  if (k0 + row < K && mc < Mp)
+    *reinterpret_cast<uint4*>(xt + (k0 + row) * Mp + mc) =
+        make_uint4(tile[row][4 * c], tile[row][4 * c + 1], tile[row][4 * c + 2], tile[row][4 * c + 3]);
+}
+
+// Both operands in one launch: blocks below digit_blocks make digits, the
+// others codes.
 template <typename DyT, int ND>
 __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
-    k_gw_digits(const DyT* __restrict__ dy, const float* __restrict__ eta, int64_t M, int64_t N, int64_t Mp,
-                int pairs, uint8_t* __restrict__ digits, float* __restrict__ scale) {
+    k_gw_operands(unsigned digit_blocks, const int8_t* __restrict__ xq, int64_t K, uint8_t* __restrict__ xt,
+                  const DyT* __restrict__ dy, const float* __restrict__ eta, int64_t M, int64_t N, int64_t Mp,
+                  int pairs, uint8_t* __restrict__ digits, float* __restrict__ scale) {
   constexpr float kTop = ND == 3 ? 8355711.0f : 32639.0f;  // 127 (1 + 256 (+ 65536)): the largest q
   constexpr int kBits = ND == 3 ? 22 : 14;
   constexpr int kRegs = sizeof(DyT) == 2 ? 1 : 2;
   extern __shared__ __align__(16) uint8_t smem[];  // ND x 64 columns x 512 bytes, words XORed with the lane
   __shared__ uint32_t s_max[16][kGdCols];
   __shared__ float s_f[kGwChunk];
+  __shared__ uint32_t s_codes[64][33];
   uint32_t* words = reinterpret_cast<uint32_t*>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t ntiles = (N + kGdCols - 1) / kGdCols;
@@ -84,6 +123,10 @@ __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
   const int64_t mc = chunk * kGwChunk;
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
+  if (blockIdx.x >= digit_blocks) {
+    gw_codes_tile(xq, M, K, Mp, blockIdx.x - digit_blocks, s_codes, xt);
+    return;
+  }
   uint32_t raw[32][kRegs];
   const int rows = static_cast<int>(min(static_cast<int64_t>(32), M - mc - 32 * warp));  // of this warp, may be < 1
   const DyT* src = dy + (mc + 32 * warp) * N + n;
@@ -174,52 +217,6 @@ __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
   }
 }
 
-// The codes with the tokens contiguous: xt (K x Mp) from xq (M x K), zero
-// past M.  Tiles of 64 inputs by 128 tokens, transposed 4 x 4 bytes at a time
-// on the way into shared memory.
-__global__ void __launch_bounds__(256)
-    k_gw_codes(const int8_t* __restrict__ xq, int64_t M, int64_t K, int64_t Mp, uint8_t* __restrict__ xt) {
-  __shared__ uint32_t tile[64][33];
-  const int64_t ktiles = (K + 63) / 64;
-  const int64_t k0 = (blockIdx.x % ktiles) * 64, m0 = (blockIdx.x / ktiles) * 128;
-  const int kq = threadIdx.x & 15, mq = threadIdx.x >> 4;
-  const bool words = (K & 3) == 0;
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_trigger();
-#pragma unroll
-  for (int it = 0; it < 2; ++it) {
-    const int64_t k = k0 + 4 * kq, m = m0 + 4 * (mq + 16 * it);
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[i] = 0;
-      if (m + i < M && k < K) {
-        const int8_t* p = xq + (m + i) * K + k;
-        if (words) {
-          w[i] = *reinterpret_cast<const uint32_t*>(p);
-        } else {
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            if (k + b < K) w[i] |= static_cast<uint32_t>(static_cast<uint8_t>(p[b])) << (8 * b);
-        }
-      }
-    }
-    uint32_t o[4];
-    transpose4x4_bytes(w[0], w[1], w[2], w[3], o[0], o[1], o[2], o[3]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) tile[4 * kq + i][mq + 16 * it] = o[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int it = 0; it < 2; ++it) {
-    const int row = (threadIdx.x >> 3) + 32 * it, c = threadIdx.x & 7;
-    const int64_t m = m0 + 16 * c;
-    if (k0 + row < K && m < Mp)
-      *reinterpret_cast<uint4*>(xt + (k0 + row) * Mp + m) =
-          make_uint4(tile[row][4 * c], tile[row][4 * c + 1], tile[row][4 * c + 2], tile[row][4 * c + 3]);
-  }
-}
-
 // ---------------------------------------------------------------- product
 //
 // Persistent CTAs, tiles of 128 outputs n (TMEM lanes) by 256 inputs k
@@ -233,11 +230,12 @@ __global__ void __launch_bounds__(256)
 constexpr int kGwBM = 128;   // tokens per step
 constexpr int kGwBN = 256;   // inputs per tile
 constexpr int kGwSlots = 4;  // code blocks held
-constexpr int kGwStages = 6;
+constexpr int kGwStages = 5;
 constexpr int kGwThreads = 32 * 10;
 constexpr int kGwABytes = 128 * kGwBM, kGwBBytes = kGwBN * kGwBM;
 constexpr int kGwBars = 2 * kGwStages + 2 * kGwSlots + 4 + 1;
-constexpr size_t kGwSmem = 1024 + kGwStages * kGwABytes + kGwSlots * kGwBBytes + 8 * kGwBars + 16;
+constexpr int kGwPatch = 32 * 17;  // floats of a warp's 32 x 16 outputs, turned for rows that take no vectors
+constexpr size_t kGwSmem = 1024 + kGwStages * kGwABytes + kGwSlots * kGwBBytes + 8 * 4 * kGwPatch + 8 * kGwBars + 16;
 static_assert(kGwSmem <= 227 * 1024, "shared memory per CTA");
 static_assert(kGwChunk == kGwSlots * kGwBM, "a chunk's codes are held whole");
 
@@ -284,7 +282,8 @@ __global__ void __launch_bounds__(kGwThreads, 1)
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sA = base;
   uint8_t* sB = sA + S * kGwABytes;
-  uint64_t* full_a = reinterpret_cast<uint64_t*>(sB + SB * kGwBBytes);
+  float* patches = reinterpret_cast<float*>(sB + SB * kGwBBytes);
+  uint64_t* full_a = reinterpret_cast<uint64_t*>(patches + 8 * kGwPatch);
   uint64_t* empty_a = full_a + S;
   uint64_t* full_b = empty_a + S;
   uint64_t* empty_b = full_b + SB;
@@ -425,13 +424,31 @@ __global__ void __launch_bounds__(kGwThreads, 1)
           sc = __fmul_rn(sc, 0.00390625f);
         }
       }
-      if (ok && n < N) {
+      if (ok && vec) {
+        if (n < N)
+#pragma unroll
+          for (int i = 0; i < 128; i += 16) {
+            float f[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) f[x] = acc[i + x];
+            store16<OutT>(dw, n * K, k0 + i, K, f, true);
+          }
+      } else if (ok) {
+        // rows that start anywhere: 16 columns of two rows a store (one value
+        // a lane and 32 rows would take 32 sectors each: 43 us for 129 x 901 x 1501)
+        float* patch = patches + (warp - 2) * kGwPatch;
+        const int64_t nw = t / ktiles * 128 + 32 * qd;
+        const int rows = static_cast<int>(min(static_cast<int64_t>(32), N - nw)), col = lane & 15;
 #pragma unroll
         for (int i = 0; i < 128; i += 16) {
-          float f[16];
+          __syncwarp();
 #pragma unroll
-          for (int x = 0; x < 16; ++x) f[x] = acc[i + x];
-          store16<OutT>(dw, n * K, k0 + i, K, f, vec);
+          for (int x = 0; x < 16; ++x) patch[lane * 17 + x] = acc[i + x];
+          __syncwarp();
+          if (k0 + i + col < K)
+#pragma unroll 4
+            for (int r = lane >> 4; r < rows; r += 2)
+              store_out<OutT>(dw, (nw + r) * K + k0 + i + col, patch[r * 17 + col]);
         }
       }
     }

@@ -185,19 +185,6 @@ bl_status run_grad_input(const void* dyp, bl_dtype dydt, const uint8_t* packed, 
   return dxdt == BL_F32 ? launch_gi<1, float>(tdy, tw, a, s) : launch_gi<1, __nv_bfloat16>(tdy, tw, a, s);
 }
 
-template <typename DyT, int ND>
-bl_status launch_gw_digits(const void* dy, const float* eta, int64_t M, int64_t N, int64_t Mp, uint8_t* digits,
-                           float* scale, cudaStream_t s) {
-  static int done[kMaxDevices] = {0};
-  auto kern = bl::k_gw_digits<DyT, ND>;
-  constexpr size_t smem = ND * bl::kGdCols * bl::kGwChunk;
-  if (!ensure_smem(kern, smem, done)) return BL_ERR_CUDA;
-  const int64_t blocks = ((N + bl::kGdCols - 1) / bl::kGdCols) * ((M + bl::kGwChunk - 1) / bl::kGwChunk);
-  if (blocks > INT32_MAX) return BL_ERR_UNSUPPORTED;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(bl::kGdThreads), smem, s,
-                    static_cast<const DyT*>(dy), eta, M, N, Mp, N % 2 == 0 ? 1 : 0, digits, scale);
-}
-
 template <int ND, typename OutT>
 bl_status launch_gw(const CUtensorMap& td, const CUtensorMap& tx, const float* scale, int M, int N, int K, void* dw,
                     int vec, int sms, cudaStream_t s) {
@@ -224,6 +211,21 @@ inline GwScratch gw_scratch(int64_t M, int64_t N, int64_t K, int nd, Scratch* ws
   g.codes = static_cast<uint8_t*>(ws->take(static_cast<size_t>(K * g.Mp)));
   g.scale = static_cast<float*>(ws->take(static_cast<size_t>((M + bl::kGwChunk - 1) / bl::kGwChunk * N * 4)));
   return g;
+}
+
+template <typename DyT, int ND>
+bl_status launch_gw_operands(const void* dy, const int8_t* xq, const float* eta, int64_t M, int64_t N, int64_t K,
+                             const GwScratch& g, cudaStream_t s) {
+  static int done[kMaxDevices] = {0};
+  auto kern = bl::k_gw_operands<DyT, ND>;
+  constexpr size_t smem = ND * bl::kGdCols * bl::kGwChunk;
+  if (!ensure_smem(kern, smem, done)) return BL_ERR_CUDA;
+  const int64_t digits = ((N + bl::kGdCols - 1) / bl::kGdCols) * ((M + bl::kGwChunk - 1) / bl::kGwChunk);
+  const int64_t blocks = digits + ((K + 63) / 64) * ((M + 127) / 128);
+  if (blocks > INT32_MAX) return BL_ERR_UNSUPPORTED;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(bl::kGdThreads), smem, s,
+                    static_cast<unsigned>(digits), xq, K, g.codes, static_cast<const DyT*>(dy), eta, M, N, g.Mp,
+                    N % 2 == 0 ? 1 : 0, g.digits, g.scale);
 }
 
 // One CTA per row, of as many warps as hold the row at kRgHeld chunks a thread.
@@ -458,17 +460,12 @@ bl_status bitlinear_grad_weight(const void* dy, bl_dtype dydt, const int8_t* xq,
   const int nd = dwdt == BL_F32 ? 3 : 2;
   const GwScratch g = gw_scratch(M, N, K, nd, &ws);
   if (dydt == BL_F32)
-    st = nd == 3 ? launch_gw_digits<float, 3>(dy, eta, M, N, g.Mp, g.digits, g.scale, s)
-                 : launch_gw_digits<float, 2>(dy, eta, M, N, g.Mp, g.digits, g.scale, s);
+    st = nd == 3 ? launch_gw_operands<float, 3>(dy, xq, eta, M, N, K, g, s)
+                 : launch_gw_operands<float, 2>(dy, xq, eta, M, N, K, g, s);
   else
-    st = nd == 3 ? launch_gw_digits<__nv_bfloat16, 3>(dy, eta, M, N, g.Mp, g.digits, g.scale, s)
-                 : launch_gw_digits<__nv_bfloat16, 2>(dy, eta, M, N, g.Mp, g.digits, g.scale, s);
+    st = nd == 3 ? launch_gw_operands<__nv_bfloat16, 3>(dy, xq, eta, M, N, K, g, s)
+                 : launch_gw_operands<__nv_bfloat16, 2>(dy, xq, eta, M, N, K, g, s);
   if (st != BL_OK) return st;
-  const int64_t blocks = ((K + 63) / 64) * ((M + 127) / 128);
-  if (blocks > INT32_MAX) return BL_ERR_UNSUPPORTED;
-  if ((st = launch_pdl(bl::k_gw_codes, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, xq, M, K, g.Mp, g.codes)) !=
-      BL_OK)
-    return st;
   CUtensorMap td, tx;
   if (!make_tmap(&td, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.digits, g.Mp, N, nd, g.Mp, bl::kGwBM, 128,
                  CU_TENSOR_MAP_SWIZZLE_128B) ||

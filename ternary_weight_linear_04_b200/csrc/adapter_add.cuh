@@ -51,16 +51,16 @@ __device__ __noinline__ float adapter_add(const float* u, const __nv_bfloat16* B
   return __fadd_rn(base, s);
 }
 
-// The distinct adapters of a tile's tokens in order of first use: s_ids[t]
-// for t < BM and s_list; returns their number.  Called by whole warps, the
+// The distinct adapters of a tile's tokens in order of first use: s_list, and
+// s_ids[t], t < BM, the place of token t's in it (-1: none); returns their
+// number.  Token t is rows[m0 + t], or m0 + t where rows is NULL.  Called by whole warps, the
 // threads t = 0 .. (BM at least) that `sync` brings together; BM <= 256;
 // s_cnt has 8 entries.
 template <typename Sync>
-__device__ __forceinline__ int tile_adapters(const int32_t* ids, int64_t m0, int64_t M, int BM, int L, int* s_ids,
-                                             int* s_list, int* s_cnt, int t, Sync sync) {
+__device__ __forceinline__ int tile_adapters(const int32_t* ids, const int32_t* rows, int64_t m0, int64_t M, int BM, int L,
+                                             int* s_ids, int* s_list, int* s_cnt, int t, Sync sync) {
   const int lane = t & 31, warp = t >> 5, groups = (BM + 31) >> 5;
-  const int id = t < BM && m0 + t < M ? adapter_of(ids, m0 + t, L) : -1;
-  if (t < BM) s_ids[t] = id;
+  const int id = t < BM && m0 + t < M ? adapter_of(ids, rows ? rows[m0 + t] : m0 + t, L) : -1;
   // each warp's distinct ones, then those that no warp before has
   const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
   bool first = id >= 0 && lane == __ffs(same) - 1;
@@ -86,12 +86,22 @@ __device__ __forceinline__ int tile_adapters(const int32_t* ids, int64_t m0, int
   }
   if (first) s_list[before + __popc(firsts & below)] = id;
   sync();
+  if (t < BM) {
+    int at = -1;
+    for (int j = 0; id >= 0 && j < total; ++j)
+      if (s_list[j] == id) {
+        at = j;
+        break;
+      }
+    s_ids[t] = at;
+  }
+  sync();
   return total;
 }
 
-__device__ __forceinline__ int tile_adapters(const int32_t* ids, int64_t m0, int64_t M, int BM, int L, int* s_ids,
-                                             int* s_list, int* s_cnt) {
-  return tile_adapters(ids, m0, M, BM, L, s_ids, s_list, s_cnt, static_cast<int>(threadIdx.x), [] { __syncthreads(); });
+__device__ __forceinline__ int tile_adapters(const int32_t* ids, const int32_t* rows, int64_t m0, int64_t M, int BM, int L,
+                                             int* s_ids, int* s_list, int* s_cnt) {
+  return tile_adapters(ids, rows, m0, M, BM, L, s_ids, s_list, s_cnt, static_cast<int>(threadIdx.x), [] { __syncthreads(); });
 }
 
 // Part p of the bf16 values x0 + x1 + x2 that hold an fp32 (8 bits each, the
@@ -105,6 +115,22 @@ __device__ __forceinline__ float bf16_part(float x, int p) {
       x = __fsub_rn(h, h) == 0.0f ? __fsub_rn(x, h) : 0.0f;  // an infinity has no rest
     }
   return x;  // to be rounded to bf16
+}
+
+// Eight entries of a token's row of u (or v) in the tensor-core kernels: its
+// own `group` = P r entries (P parts of r values) begin at entry `own`, the
+// rest are zeros; value(j) gives its j-th value.
+template <int P, typename F>
+__device__ __forceinline__ uint4 own_entries(int e, int own, int r, F value) {
+  float f[8];
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    const int i = e + b - own, p = i >= 2 * r ? 2 : i >= r ? 1 : 0;
+    f[b] = i >= 0 && i < P * r ? bf16_part<P>(value(i - p * r), p) : 0.0f;
+  }
+  const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(f[0], f[1]), __floats2bfloat162_rn(f[2], f[3]),
+                               __floats2bfloat162_rn(f[4], f[5]), __floats2bfloat162_rn(f[6], f[7])};
+  return reinterpret_cast<const uint4&>(h);
 }
 
 // Whether a pair of bf16 holds an infinity or a NaN.  The tensor-core kernels

@@ -173,6 +173,90 @@ __global__ void __launch_bounds__(kAuThreads)
   }
 }
 
+// ---------------------------------------------------------------- tokens by adapter
+//
+// rows: the tokens in the order of their adapters (those without one last),
+// within an adapter in their own; start[a]: where adapter a's begin, start[L]
+// where those without one do.  One CTA: a stable counting sort by the adapter's
+// low and (L > 255) high eight bits.  Each of 32 warps counts and places its
+// own stretch of the tokens, ranks within a step of 32 by matching keys, so
+// the order needs no atomics.  With it the kernels behind read one or two
+// adapters a tile whatever the order of the requests.
+
+constexpr int kSortThreads = 1024;
+
+__global__ void __launch_bounds__(kSortThreads)
+    k_adapter_sort(const int32_t* __restrict__ ids, int64_t M, int L, int32_t* first, int32_t* rows,
+                   int32_t* __restrict__ start) {
+  __shared__ int s_count[32][257];  // a warp's tokens with a digit, then where the next of them goes
+  __shared__ int s_sum[8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t seg = (M + 1023) / 1024 * 32, lo = warp * seg, hi = min(M, lo + seg);
+  const int passes = L > 255 ? 2 : 1;
+  pdl_wait();
+  if (tid == 0) pdl_trigger();
+  auto key_of = [&](int64_t m) {
+    const int a = adapter_of(ids, m, L);
+    return a < 0 ? L : a;
+  };
+  for (int pass = 0; pass < passes; ++pass) {
+    const int32_t* src = pass ? first : nullptr;
+    int32_t* dst = pass == passes - 1 ? rows : first;
+    auto digit = [&](int64_t i, int& item) {
+      item = src ? src[i] : static_cast<int>(i);
+      return (key_of(item) >> (8 * pass)) & 255;
+    };
+    for (int i = tid; i < 32 * 257; i += kSortThreads) (&s_count[0][0])[i] = 0;
+    __syncthreads();
+    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+      int item, d = 256;
+      if (i0 + lane < hi) d = digit(i0 + lane, item);
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
+      if (lane == __ffs(same) - 1) s_count[warp][d] += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    int total = 0, inc = 0;
+    if (tid < 256) {
+      for (int w = 0; w < 32; ++w) {  // where a warp's go among its digit's
+        const int n = s_count[w][tid];
+        s_count[w][tid] = total;
+        total += n;
+      }
+      inc = total;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += up;
+      }
+      if (lane == 31) s_sum[warp] = inc;
+    }
+    __syncthreads();
+    if (tid < 256) {
+      int before = inc - total;  // the digits below
+      for (int w = 0; w < warp; ++w) before += s_sum[w];
+      for (int w = 0; w < 32; ++w) s_count[w][tid] += before;
+    }
+    __syncthreads();
+    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+      int item = 0, d = 256;
+      const bool in = i0 + lane < hi;
+      if (in) d = digit(i0 + lane, item);
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
+      const int base = s_count[warp][d];
+      __syncwarp();
+      if (in) dst[base + __popc(same & ((1u << lane) - 1))] = item;
+      if (lane == __ffs(same) - 1) s_count[warp][d] = base + __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();  // this pass's order is there for the whole CTA
+  }
+  for (int64_t p = tid; p <= M; p += kSortThreads) {
+    const int k = p < M ? key_of(rows[p]) : L, before = p > 0 ? key_of(rows[p - 1]) : -1;
+    for (int b = before + 1; b <= k; ++b) start[b] = static_cast<int>(p);
+  }
+}
+
 // ---------------------------------------------------------------- u and v of many tokens
 //
 // One CTA per 16 tokens; its 16 warps take the contraction's steps of 64 in
@@ -202,6 +286,7 @@ struct UvArgs {
   UvSide side[2];
   const float* scale;
   const int32_t* ids;
+  const int32_t* rows;     // the order of the tokens (k_adapter_sort), or NULL: as they are
   int64_t M;
   int L, r;
 };
@@ -268,8 +353,8 @@ struct UvRaw {
   }
 
   // A fragment of MMA i: registers 0, 1 the rows' first pairs, 2, 3 the
-  // second (of codes 0, 2 and 1, 3 of the four); `own`: the rows' masks.
-  __device__ __forceinline__ void fragment(uint32_t (&xf)[4], int i, int part, const uint32_t (&own)[2]) const {
+  // second (of codes 0, 2 and 1, 3 of the four).
+  __device__ __forceinline__ void fragment(uint32_t (&xf)[4], int i, int part) const {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if constexpr (sizeof(XT) == 1) {
@@ -285,13 +370,13 @@ struct UvRaw {
         xf[h] = pack_bf16(f[0], f[1]);
         xf[2 + h] = pack_bf16(f[2], f[3]);
       }
-      xf[h] &= own[h];
-      xf[2 + h] &= own[h];
     }
   }
 };
 
-template <typename XT>
+// NT: tiles of 8 rank indices at a time (r <= 8 NT, or 32 of them after one
+// another); four such tiles are in flight, so 4 / NT adapters.
+template <typename XT, int NT>
 __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_t* smem, const int* s_ids,
                                         const int* s_list, int nad, volatile float* s_bad) {
   constexpr bool V = sizeof(XT) > 1;
@@ -306,14 +391,16 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
   const bool vec = s.vec != 0, bvec = (r & 7) == 0;
   float* red = reinterpret_cast<float*>(smem);
   __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(smem) + warp * 64 * kUvPitch;
-  const int id0 = s_ids[gr], id1 = s_ids[8 + gr];
-  const XT* const row[2] = {static_cast<const XT*>(s.x) + min(m0 + gr, g.M - 1) * C,  // rows past M repeat the last
-                            static_cast<const XT*>(s.x) + min(m0 + 8 + gr, g.M - 1) * C};
-  for (int jb = 0; jb < r; jb += 32) {
-    const int nt = min(4, (r - jb + 7) >> 3);
-    float acc[4][4];
+  const int own0 = s_ids[gr], own1 = s_ids[8 + gr];
+  auto token = [&](int i) {  // of the tile's row i; rows past M repeat the last
+    const int64_t at = min(m0 + i, g.M - 1);
+    return g.rows ? static_cast<int64_t>(g.rows[at]) : at;
+  };
+  const XT* const row[2] = {static_cast<const XT*>(s.x) + token(gr) * C, static_cast<const XT*>(s.x) + token(8 + gr) * C};
+  for (int jb = 0; jb < r; jb += 8 * NT) {
+    float acc[NT][4];
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
     bool bad = false;
@@ -330,98 +417,91 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
       } else {
         raw.load(row, k0, C, q, vec);
       }
-      for (int li = 0; li < nad; ++li) {
-        const int a = s_list[li];
-        const uint32_t own[2] = {id0 == a ? 0xFFFFFFFFu : 0u, id1 == a ? 0xFFFFFFFFu : 0u};
-        if constexpr (!V) {
-          const int64_t k = k0 + 16 * q;
-          uint4 wf[4][2];  // A's rows: 8 rank indices each, 16 values
+      for (int lb = 0; lb < nad; lb += 4 / NT) {
+        // slot x of the four: rank indices jb + 8 (x % NT) .. of adapter lb + x / NT
+        uint4 w[4][2];
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            uint4(&w)[2] = wf[n];
-            w[0] = w[1] = make_uint4(0, 0, 0, 0);
-            if (n >= nt) continue;
-            const int j = jb + 8 * n + gr;
-            const __nv_bfloat16* f = s.F + (static_cast<int64_t>(a) * r + j) * C + k;
+        for (int x = 0; x < 4; ++x) {
+          w[x][0] = w[x][1] = make_uint4(0, 0, 0, 0);
+          const int li = lb + x / NT, j0 = jb + 8 * (x % NT);
+          if (li >= nad || j0 >= r) continue;
+          const int64_t a = s_list[li];
+          if constexpr (!V) {  // A's row j0 + g: 16 values
+            const int64_t k = k0 + 16 * q;
+            const int j = j0 + gr;
+            const __nv_bfloat16* f = s.F + (a * r + j) * C + k;
             if (j < r && k < C) {
               if (vec) {
-                w[0] = __ldg(reinterpret_cast<const uint4*>(f));
-                w[1] = __ldg(reinterpret_cast<const uint4*>(f) + 1);
+                w[x][0] = __ldg(reinterpret_cast<const uint4*>(f));
+                w[x][1] = __ldg(reinterpret_cast<const uint4*>(f) + 1);
               } else {
                 uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                   if (k + i < C)
                     e[i >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(f) + i)) << (16 * (i & 1));
-                w[0] = make_uint4(e[0], e[1], e[2], e[3]);
-                w[1] = make_uint4(e[4], e[5], e[6], e[7]);
+                w[x][0] = make_uint4(e[0], e[1], e[2], e[3]);
+                w[x][1] = make_uint4(e[4], e[5], e[6], e[7]);
+              }
+            }
+          } else {  // B's rows k0 + lane and k0 + lane + 32: 8 values
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int64_t k = k0 + lane + 32 * h;
+              if (k >= C) continue;
+              const __nv_bfloat16* f = s.F + (a * C + k) * r + j0;
+              if (bvec) {
+                w[x][h] = __ldg(reinterpret_cast<const uint4*>(f));
+              } else {
+                uint32_t e[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (j0 + i < r)
+                    e[i >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(f) + i)) << (16 * (i & 1));
+                w[x][h] = make_uint4(e[0], e[1], e[2], e[3]);
               }
             }
           }
+        }
+        uint32_t own[4 / NT][2];
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
-            if (nonfinite8(wf[n][0]) || nonfinite8(wf[n][1])) {
+        for (int x = 0; x < 4 / NT; ++x) {
+          own[x][0] = own0 == lb + x ? 0xFFFFFFFFu : 0u;
+          own[x][1] = own1 == lb + x ? 0xFFFFFFFFu : 0u;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (nonfinite8(w[x][h])) {
               bad = true;
-              wf[n][0] = wf[n][1] = make_uint4(0, 0, 0, 0);
+              w[x][h] = make_uint4(0, 0, 0, 0);
             }
+        if constexpr (!V) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t xf[4];
-            raw.fragment(xf, i, 0, own);
+            raw.fragment(xf, i, 0);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              if (n >= nt) continue;
-              const uint4 w = wf[n][i >> 1];
-              const uint32_t lo = (i & 1) ? w.z : w.x, hi = (i & 1) ? w.w : w.y;
-              mma_bf16_16816(acc[n], xf[0], xf[1], xf[2], xf[3], __byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+            for (int x = 0; x < 4; ++x) {
+              if (lb + x / NT >= nad) continue;
+              const uint32_t k0m = own[x / NT][0], k1m = own[x / NT][1];
+              const uint4 f = w[x][i >> 1];
+              const uint32_t lo = (i & 1) ? f.z : f.x, hi = (i & 1) ? f.w : f.y;
+              mma_bf16_16816(acc[x % NT], xf[0] & k0m, xf[1] & k1m, xf[2] & k0m, xf[3] & k1m,
+                             __byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
             }
           }
         } else {
-          const __nv_bfloat16* f = s.F + (a * C + k0) * r + jb;
           __syncwarp();
-          if (bvec) {  // every load in flight at once
-            uint4 w[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              const int i = lane + 32 * x, n = i / nt, c = i - n * nt;
-              w[x] = x < 2 * nt && k0 + n < C ? __ldg(reinterpret_cast<const uint4*>(f + static_cast<int64_t>(n) * r) + c)
-                                              : make_uint4(0, 0, 0, 0);
-            }
+          for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              if (x >= 2 * nt) continue;
-              const int i = lane + 32 * x, n = i / nt, c = i - n * nt;
-              if (nonfinite8(w[x])) {
-                bad = true;
-                w[x] = make_uint4(0, 0, 0, 0);
-              }
-              *reinterpret_cast<uint4*>(stage + n * kUvPitch + 8 * c) = w[x];
-            }
-          } else {  // value by value, 16 in flight
-            const int cols = 8 * nt;
-#pragma unroll 1
-            for (int i0 = lane; i0 < 64 * cols; i0 += 512) {
-              uint16_t w[16];
-#pragma unroll
-              for (int x = 0; x < 16; ++x) {
-                const int i = i0 + 32 * x, n = i / cols, j = i - n * cols;
-                w[x] = k0 + n < C && jb + j < r
-                           ? __ldg(reinterpret_cast<const uint16_t*>(f) + static_cast<int64_t>(n) * r + j) : 0;
-              }
-#pragma unroll
-              for (int x = 0; x < 16; ++x) {
-                const int i = i0 + 32 * x, n = i / cols, j = i - n * cols;
-                if (nonfinite2(w[x])) {
-                  bad = true;
-                  w[x] = 0;
-                }
-                reinterpret_cast<uint16_t*>(stage)[n * kUvPitch + j] = w[x];
-              }
-            }
-          }
+            for (int h = 0; h < 2; ++h)
+              *reinterpret_cast<uint4*>(stage + (lane + 32 * h) * kUvPitch + 8 * x) = w[x][h];
           __syncwarp();
           // matrix lane / 8: rows of the contraction 0 1 4 5 .. (registers
-          // 0) or 2 3 6 7 .. (1), rank indices 0-7 or 8-15 of the pair
+          // 0) or 2 3 6 7 .. (1), slots 0 or 1 of the pair
           const int mat = lane >> 3, kk = lane & 7;
           const __nv_bfloat16* at = stage + (4 * (kk >> 1) + (kk & 1) + 2 * (mat & 1)) * kUvPitch + 8 * (mat >> 1);
 #pragma unroll 1
@@ -429,25 +509,26 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t xf[4];
-              raw.fragment(xf, i, part, own);
+              raw.fragment(xf, i, part);
 #pragma unroll
-              for (int n = 0; n < 4; n += 2) {
-                if (n >= nt) continue;
+              for (int x = 0; x < 4; x += 2) {
+                if (lb + x / NT >= nad) continue;
                 uint32_t d[4];
-                ldmatrix_x4_trans(d, at + 16 * i * kUvPitch + 8 * n);
-                mma_bf16_16816(acc[n], xf[0], xf[1], xf[2], xf[3], d[0], d[1]);
-                // an odd nt: the staged columns behind it hold anything, and
-                // neither do their sums go anywhere
-                mma_bf16_16816(acc[n + 1], xf[0], xf[1], xf[2], xf[3], d[2], d[3]);
+                ldmatrix_x4_trans(d, at + 16 * i * kUvPitch + 8 * x);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const uint32_t k0m = own[(x + y) / NT][0], k1m = own[(x + y) / NT][1];
+                  mma_bf16_16816(acc[(x + y) % NT], xf[0] & k0m, xf[1] & k1m, xf[2] & k0m, xf[3] & k1m, d[2 * y], d[2 * y + 1]);
+                }
               }
             }
         }
       }
-  }
+    }
     if (bad) *s_bad = 1.0f;
     __syncthreads();  // the staged rows are read
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         *reinterpret_cast<float2*>(red + (warp * 16 + 8 * h + gr) * kUvRedPitch + 8 * n + 2 * q) =
@@ -467,16 +548,18 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
         any = cluster_total(const_cast<float*>(s_bad), CS) != 0.0f;
       }
     }
-    const int m = tid >> 5, j = jb + (tid & 31), a = s_ids[m];
-    if (z == 0 && j < r && m0 + m < g.M) {
-      if (a >= 0) {
-        if (any) t = uv_plain<typename std::conditional<V, XT, float>::type>(g, s, m0 + m, a, j);
-        if constexpr (!V) t = __fmul_rn(t, div127_rn(s.eta[m0 + m]));
+    const int i = tid >> 5, j = tid & 31;
+    if (z == 0 && j < 8 * NT && jb + j < r && m0 + i < g.M) {
+      const int64_t m = token(i);
+      if (s_ids[i] >= 0) {
+        const int a = s_list[s_ids[i]];
+        if (any) t = uv_plain<typename std::conditional<V, XT, float>::type>(g, s, m, a, jb + j);
+        if constexpr (!V) t = __fmul_rn(t, div127_rn(s.eta[m]));
         t = __fmul_rn(t, g.scale[a]);
       } else {
         t = 0.0f;
       }
-      s.out[(m0 + m) * r + j] = t;
+      s.out[m * r + jb + j] = t;
     }
     if (CS > 1) cluster_sync_all();
     else __syncthreads();
@@ -484,7 +567,7 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
 }
 
 // Grid (tiles of 16 tokens, sides, CTAs of a cluster).
-template <typename DyT>
+template <typename DyT, int NT>
 __global__ void __launch_bounds__(kUvThreads, 1) k_adapter_uv(const __grid_constant__ UvArgs g) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int s_ids[32], s_list[32], s_cnt[8];
@@ -495,16 +578,16 @@ __global__ void __launch_bounds__(kUvThreads, 1) k_adapter_uv(const __grid_const
     s_bad = 0.0f;
   }
   const UvSide& s = g.side[blockIdx.y];
-  const int nad = tile_adapters(g.ids, static_cast<int64_t>(blockIdx.x) * 16, g.M, 16, g.L, s_ids, s_list, s_cnt);
-  if (s.is_v) uv_tile<DyT>(g, s, smem, s_ids, s_list, nad, &s_bad);
-  else uv_tile<int8_t>(g, s, smem, s_ids, s_list, nad, &s_bad);
+  const int nad = tile_adapters(g.ids, g.rows, static_cast<int64_t>(blockIdx.x) * 16, g.M, 16, g.L, s_ids, s_list, s_cnt);
+  if (s.is_v) uv_tile<DyT, NT>(g, s, smem, s_ids, s_list, nad, &s_bad);
+  else uv_tile<int8_t, NT>(g, s, smem, s_ids, s_list, nad, &s_bad);
 }
 
 // ---------------------------------------------------------------- dA and dB
 //
 // One CTA per adapter and 64 columns of A or B (a cluster splits the tokens
-// where there are few of these): it gathers the adapter's tokens out of ids
-// in windows, in order, then 64 of them at a time
+// where there are few of these): it takes the adapter's tokens
+// (k_adapter_sort) 64 at a time
 //   out[j][c] += coef[m][j] x[m][c],   dA: coef = v eta / 127, x = x~;
 //                                      dB: coef = u,           x = dy
 // on mma.sync, both operands transposed out of shared memory by ldmatrix.
@@ -522,8 +605,7 @@ struct DabSide {
 struct DabArgs {
   DabSide a, b;
   const float* eta;
-  const int32_t* ids;
-  int64_t M;
+  const int32_t *rows, *start;  // k_adapter_sort
   int r;
   unsigned slabs_a;  // blocks x below this: dA
 };
@@ -531,7 +613,6 @@ struct DabArgs {
 constexpr int kDabThreads = 128;
 constexpr int kDabTokens = 64;   // a chunk
 constexpr int kDabCols = 64;
-constexpr int kDabWindow = 2048;
 constexpr int kDabXPitch = kDabCols + 8;
 
 __host__ __device__ constexpr int dab_rows(int r) { return (r + 15) / 16 * 16; }
@@ -543,13 +624,13 @@ __host__ __device__ constexpr size_t dab_smem(int r, int parts, int xparts) {
 
 // JT: tiles of 16 rank indices (r <= 16 JT).
 template <typename XT, typename OutT, int JT>
-__device__ __forceinline__ void dab_tile(const DabArgs& g, const DabSide& s, int64_t c0, bool is_a, uint8_t* smem,
-                                         uint16_t* s_tok, int* s_cnt) {
+__device__ __forceinline__ void dab_tile(const DabArgs& g, const DabSide& s, int64_t c0, bool is_a, uint8_t* smem) {
   constexpr int P = sizeof(OutT) == 4 ? 3 : 2, PX = sizeof(XT) == 4 ? 3 : 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int CS = static_cast<int>(cluster_nctarank()), z = CS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int r = g.r, rows = dab_rows(r), cpitch = rows + 8;
   const int a = blockIdx.y;
+  const int from = g.start[a], to = g.start[a + 1];
   __nv_bfloat16* s_coef = reinterpret_cast<__nv_bfloat16*>(smem);          // [P][token][cpitch]
   __nv_bfloat16* s_x = s_coef + P * kDabTokens * cpitch;                   // [PX][token][kDabXPitch]
   float acc[JT][2][4];
@@ -568,9 +649,9 @@ __device__ __forceinline__ void dab_tile(const DabArgs& g, const DabSide& s, int
   uint32_t xr[kXRegs];
   float cf[kCoefs];
   const bool cvec = (r & 3) == 0;
-  auto load = [&](const uint16_t* tok, int left, int64_t w0) {
-    const bool in = xt < left;
-    const int64_t m = w0 + (in ? tok[xt] : 0);
+  auto load = [&](int at) {  // the 64 tokens from place `at` on
+    const bool in = at + xt < to;
+    const int64_t m = in ? g.rows[at + xt] : 0;
     const XT* src = static_cast<const XT*>(s.x) + m * s.C + c0 + 32 * xh;
     const int64_t cols = in ? s.C - c0 - 32 * xh : 0;
     constexpr int kPer = 16 / static_cast<int>(sizeof(XT));  // values of a 16-byte piece
@@ -659,72 +740,36 @@ __device__ __forceinline__ void dab_tile(const DabArgs& g, const DabSide& s, int
                        pack_bf16(bf16_part<P>(cf[i + 2], p), bf16_part<P>(cf[i + 3], p)));
     }
   };
-  int chunk0 = 0;                         // chunks of the windows before, for the turns of a cluster's CTAs
-  for (int64_t w0 = 0; w0 < g.M; w0 += kDabWindow) {
-    // the window's tokens of this adapter, in order
-    const int wn = static_cast<int>(min(static_cast<int64_t>(kDabWindow), g.M - w0));
-    constexpr int kEach = kDabWindow / kDabThreads;
-    unsigned mine = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int t = tid * kEach + i;
-      if (t < wn && __ldg(g.ids + w0 + t) == a) mine |= 1u << i;
-    }
-    const int n = __popc(mine);
-    int inc = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-      if (lane >= o) inc += up;
-    }
-    __syncthreads();  // the list and counts of the window before are read
-    if (lane == 31) s_cnt[warp] = inc;
+  int c = from + z * kDabTokens;  // this CTA's chunks: every CS-th
+  if (c < to) load(c);
+  for (; c < to; c += CS * kDabTokens) {
+    put();
     __syncthreads();
-    int at = inc - n, total = 0;
+    // the next chunk's rows are on their way while this one is multiplied
+    if (c + CS * kDabTokens < to) load(c + CS * kDabTokens);
+    const int kk = lane & 7, mat = lane >> 3;
 #pragma unroll
-    for (int w = 0; w < kDabThreads / 32; ++w) {
-      if (w < warp) at += s_cnt[w];
-      total += s_cnt[w];
-    }
-    while (mine) {
-      const int i = __ffs(mine) - 1;
-      mine &= mine - 1;
-      s_tok[at++] = static_cast<uint16_t>(tid * kEach + i);
-    }
-    __syncthreads();
-    const int chunks = (total + kDabTokens - 1) / kDabTokens;
-    int c = (z - chunk0 % CS + CS) % CS;  // this CTA's chunks: every CS-th
-    if (c < chunks) load(s_tok + c * kDabTokens, total - c * kDabTokens, w0);
-    for (; c < chunks; c += CS) {
-      put();
-      __syncthreads();
-      // the next chunk's rows are on their way while this one is multiplied
-      if (c + CS < chunks) load(s_tok + (c + CS) * kDabTokens, total - (c + CS) * kDabTokens, w0);
-      const int kk = lane & 7, mat = lane >> 3;
+    for (int ks = 0; ks < kDabTokens / 16; ++ks) {
+      uint32_t bx[PX][4];  // columns 16 warp + 0-7 (registers 0, 1) and 8-15 (2, 3)
 #pragma unroll
-      for (int ks = 0; ks < kDabTokens / 16; ++ks) {
-        uint32_t bx[PX][4];  // columns 16 warp + 0-7 (registers 0, 1) and 8-15 (2, 3)
+      for (int p = 0; p < PX; ++p)
+        ldmatrix_x4_trans(bx[p], s_x + (p * kDabTokens + 16 * ks + kk + 8 * (mat & 1)) * kDabXPitch + 16 * warp + 8 * (mat >> 1));
 #pragma unroll
-        for (int p = 0; p < PX; ++p)
-          ldmatrix_x4_trans(bx[p], s_x + (p * kDabTokens + 16 * ks + kk + 8 * (mat & 1)) * kDabXPitch + 16 * warp + 8 * (mat >> 1));
+      for (int t = 0; t < JT; ++t) {
+        if (16 * t >= rows) continue;
 #pragma unroll
-        for (int t = 0; t < JT; ++t) {
-          if (16 * t >= rows) continue;
+        for (int p = 0; p < P; ++p) {
+          uint32_t f[4];  // rows j 0-7, 8-15 at tokens 0-7, then at 8-15
+          ldmatrix_x4_trans(f, s_coef + (p * kDabTokens + 16 * ks + kk + 8 * (mat >> 1)) * cpitch + 16 * t + 8 * (mat & 1));
 #pragma unroll
-          for (int p = 0; p < P; ++p) {
-            uint32_t f[4];  // rows j 0-7, 8-15 at tokens 0-7, then at 8-15
-            ldmatrix_x4_trans(f, s_coef + (p * kDabTokens + 16 * ks + kk + 8 * (mat >> 1)) * cpitch + 16 * t + 8 * (mat & 1));
-#pragma unroll
-            for (int px = 0; px < PX; ++px) {
-              mma_bf16_16816(acc[t][0], f[0], f[1], f[2], f[3], bx[px][0], bx[px][1]);
-              mma_bf16_16816(acc[t][1], f[0], f[1], f[2], f[3], bx[px][2], bx[px][3]);
-            }
+          for (int px = 0; px < PX; ++px) {
+            mma_bf16_16816(acc[t][0], f[0], f[1], f[2], f[3], bx[px][0], bx[px][1]);
+            mma_bf16_16816(acc[t][1], f[0], f[1], f[2], f[3], bx[px][2], bx[px][3]);
           }
         }
       }
-      __syncthreads();
     }
-    chunk0 += chunks;
+    __syncthreads();
   }
 
   // out: the CTA's sums into shared memory, a cluster's added up by rows
@@ -760,14 +805,12 @@ __device__ __forceinline__ void dab_tile(const DabArgs& g, const DabSide& s, int
 template <typename DyT, typename OutT, int JT>
 __global__ void __launch_bounds__(kDabThreads) k_adapter_dab(const __grid_constant__ DabArgs g) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint16_t s_tok[kDabWindow];
-  __shared__ int s_cnt[kDabThreads / 32];
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
   if (blockIdx.x < g.slabs_a)
-    dab_tile<int8_t, OutT, JT>(g, g.a, static_cast<int64_t>(blockIdx.x) * kDabCols, true, smem, s_tok, s_cnt);
+    dab_tile<int8_t, OutT, JT>(g, g.a, static_cast<int64_t>(blockIdx.x) * kDabCols, true, smem);
   else
-    dab_tile<DyT, OutT, JT>(g, g.b, static_cast<int64_t>(blockIdx.x - g.slabs_a) * kDabCols, false, smem, s_tok, s_cnt);
+    dab_tile<DyT, OutT, JT>(g, g.b, static_cast<int64_t>(blockIdx.x - g.slabs_a) * kDabCols, false, smem);
 }
 
 }  // namespace bl

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
     const bool chunked = (r & 7) == 0;       // eight entries share adapter and part
     int entries = 0;
     if (zr == 0)
-      entries = tile_adapters(ad.ids, m0, M, BM, ad.L, s_ids, s_list, s_cnt, t,
+      entries = tile_adapters(ad.ids, nullptr, m0, M, BM, ad.L, s_ids, s_list, s_cnt, t,
                               [] { asm volatile("bar.sync 1, 256;" ::: "memory"); }) * group;
     if (t == 0) {
       *s_entries = entries;
@@ -333,13 +333,18 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
             va[wi] = __ldg(reinterpret_cast<const uint4*>(ad.B + (static_cast<int64_t>(s_list[li]) * N + n) * r + j));
           } else {
             uint32_t w[4] = {0, 0, 0, 0};
+            int li = e / group, j = (e - li * group) % r, left = group - (e - li * group);  // of this adapter's entries
 #pragma unroll
             for (int b = 0; b < 8; ++b)
               if (e + b < entries) {
-                const int li = (e + b) / group, j = (e + b - li * group) % r;
                 const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(ad.B) +
                                          (static_cast<int64_t>(s_list[li]) * N + n) * r + j);
                 w[b >> 1] |= h << (16 * (b & 1));
+                if (++j == r) j = 0;
+                if (--left == 0) {
+                  left = group;
+                  ++li;
+                }
               }
             va[wi] = make_uint4(w[0], w[1], w[2], w[3]);
           }
@@ -350,26 +355,21 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
         const int q = t + 32 * kTcAdWarps * y4;
         const int tok = q % BM, e = e0 + 8 * (q / BM);
         vu[y4] = make_uint4(0, 0, 0, 0);
-        const int id = s_ids[tok];
-        if (id < 0 || q >= BM * 8 || e >= entries) continue;
+        const int own = s_ids[tok] * group;
+        if (own < 0 || q >= BM * 8 || e + 8 <= own || e >= own + group) continue;
         const float* ut = ad.u + static_cast<int64_t>(m0 + tok) * r;
-        float f[8];
         if (chunked) {
-          const int li = e / group, rem = e - li * group, p = rem / r;
-          if (s_list[li] != id) continue;
-          const float4* x = reinterpret_cast<const float4*>(ut + rem - p * r);
+          const int i = e - own, p = i >= 2 * r ? 2 : i >= r ? 1 : 0;
+          const float4* x = reinterpret_cast<const float4*>(ut + i - p * r);
           const float4 lo = x[0], hi = x[1];
           const float g[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+          float f[8];
 #pragma unroll
           for (int b = 0; b < 8; ++b) f[b] = bf16_part<kParts>(g[b], p);
+          vu[y4] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
         } else {
-#pragma unroll
-          for (int b = 0; b < 8; ++b) {
-            const int li = (e + b) / group, rem = e + b - li * group, p = rem / r;
-            f[b] = e + b < entries && s_list[li] == id ? bf16_part<kParts>(ut[rem - p * r], p) : 0.0f;
-          }
+          vu[y4] = own_entries<kParts>(e, own, r, [&](int j) { return ut[j]; });
         }
-        vu[y4] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
       }
     };
     if (asteps > 0) load(0);

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kGiThreads, 1)
   }
   int entries = 0, ast = 0, alo = 0;  // entries of the tile's adapters, this CTA's steps of 64 of them
   if (a.v) {
-    entries = tile_adapters(a.ids, m0, a.M, 128 * H, a.L, s_ids, s_list, s_cnt) * kParts * a.r;
+    entries = tile_adapters(a.ids, nullptr, m0, a.M, 128 * H, a.L, s_ids, s_list, s_cnt) * kParts * a.r;
     const int asteps = (entries + kGiBK - 1) / kGiBK;
     alo = asteps * z / CS;
     ast = asteps * (z + 1) / CS - alo;
@@ -403,39 +403,32 @@ __global__ void __launch_bounds__(kGiThreads, 1)
       }
       // rows of v: a token's 64 entries (H = 1: two threads a token)
       constexpr int kPer = H == 2 ? 8 : 4;
-      const int tok = H == 2 ? t : t >> 1, c0 = H == 2 ? 0 : 4 * (t & 1), id = s_ids[tok];
+      const int tok = H == 2 ? t : t >> 1, c0 = H == 2 ? 0 : 4 * (t & 1), own = s_ids[tok] * group;
       const float* vr = a.v + static_cast<int64_t>(m0 + tok) * r;
       uint8_t* row = sA + s * Cfg::kABytes + (tok >> 3) * 1024 + (tok & 7) * 128;
 #pragma unroll
       for (int h4 = 0; h4 < kPer; h4 += 4) {
-        float f[4][8];
+        uint4 o[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int e = e0 + 8 * (c0 + h4 + c);
-#pragma unroll
-          for (int b = 0; b < 8; ++b) f[c][b] = 0.0f;
-          if (id < 0 || e >= entries) continue;
+          o[c] = make_uint4(0, 0, 0, 0);
+          if (own < 0 || e + 8 <= own || e >= own + group) continue;
           if (chunked) {
-            const int li = e / group, rem = e - li * group, p = rem / r;
-            if (s_list[li] != id) continue;
-            const float4* x = reinterpret_cast<const float4*>(vr + rem - p * r);
+            const int i = e - own, p = i >= 2 * r ? 2 : i >= r ? 1 : 0;
+            const float4* x = reinterpret_cast<const float4*>(vr + i - p * r);
             const float4 u = x[0], w = x[1];
             const float g[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+            float f[8];
 #pragma unroll
-            for (int b = 0; b < 8; ++b) f[c][b] = bf16_part<kParts>(__fmul_rn(g[b], inv_gamma), p);
+            for (int b = 0; b < 8; ++b) f[b] = bf16_part<kParts>(__fmul_rn(g[b], inv_gamma), p);
+            o[c] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
           } else {
-#pragma unroll
-            for (int b = 0; b < 8; ++b) {
-              const int li = (e + b) / group, rem = e + b - li * group, p = rem / r;
-              if (e + b < entries && s_list[li] == id) f[c][b] = bf16_part<kParts>(__fmul_rn(vr[rem - p * r], inv_gamma), p);
-            }
+            o[c] = own_entries<kParts>(e, own, r, [&](int j) { return __fmul_rn(vr[j], inv_gamma); });
           }
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(row + (((c0 + h4 + c) ^ (tok & 7)) << 4)) =
-              make_uint4(pack_bf16(f[c][0], f[c][1]), pack_bf16(f[c][2], f[c][3]), pack_bf16(f[c][4], f[c][5]),
-                         pack_bf16(f[c][6], f[c][7]));
+        for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(row + (((c0 + h4 + c) ^ (tok & 7)) << 4)) = o[c];
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -493,7 +486,7 @@ __global__ void __launch_bounds__(kGiThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j)
           if (k0 + c + j < a.K)
-            f[j] = __fadd_rn(f[j], gi_nonfinite(a.v, a.A, s_ids[trow + lane], a.r, static_cast<int>(m), k0 + c + j, a.K));
+            f[j] = __fadd_rn(f[j], gi_nonfinite(a.v, a.A, s_list[s_ids[trow + lane]], a.r, static_cast<int>(m), k0 + c + j, a.K));
       if constexpr (H == 1) {
 #pragma unroll
         for (int j = 0; j < 32; j += 4)

@@ -265,10 +265,27 @@ bl_status launch_u_few(const void* x, int8_t* xq, float* eta, int32_t* xsum, int
                     static_cast<int>(K), ad.A, ad.scale, ad.ids, ad.L, ad.r, static_cast<int>(group), u);
 }
 
-template <typename DyT>
-bl_status launch_uv_t(const bl::UvArgs& g, int sides, int64_t steps, int sms, cudaStream_t s) {
+// Scratch of k_adapter_sort.
+struct Order {
+  int32_t *rows, *start, *first;
+};
+
+inline Order order_scratch(int64_t M, int64_t L, Scratch* ws) {
+  Order o;
+  o.rows = static_cast<int32_t*>(ws->take(static_cast<size_t>(M * 4)));
+  o.start = static_cast<int32_t*>(ws->take(static_cast<size_t>((L + 1) * 4)));
+  o.first = L > 255 ? static_cast<int32_t*>(ws->take(static_cast<size_t>(M * 4))) : nullptr;
+  return o;
+}
+
+bl_status launch_sort(const AdapterSet& ad, int64_t M, const Order& o, cudaStream_t s) {
+  return launch_pdl(bl::k_adapter_sort, dim3(1), dim3(bl::kSortThreads), 0, s, ad.ids, M, ad.L, o.first, o.rows, o.start);
+}
+
+template <typename DyT, int NT>
+bl_status launch_uv_nt(const bl::UvArgs& g, int sides, int64_t steps, int sms, cudaStream_t s) {
   static int done[kMaxDevices] = {0};
-  auto kern = bl::k_adapter_uv<DyT>;
+  auto kern = bl::k_adapter_uv<DyT, NT>;
   if (!ensure_smem(kern, bl::kUvSmem, done)) return BL_ERR_CUDA;
   const int64_t tiles = (g.M + 15) / 16;
   if (tiles > INT32_MAX) return BL_ERR_UNSUPPORTED;
@@ -280,11 +297,18 @@ bl_status launch_uv_t(const bl::UvArgs& g, int sides, int64_t steps, int sms, cu
   return launch_pdl_cluster(kern, grid, dim3(bl::kUvThreads), bl::kUvSmem, s, grid.z, g);
 }
 
-// u (where out_u is given) and v (out_v) of any number of tokens.
+template <typename DyT>
+bl_status launch_uv_t(const bl::UvArgs& g, int sides, int64_t steps, int sms, cudaStream_t s) {
+  if (g.r <= 8) return launch_uv_nt<DyT, 1>(g, sides, steps, sms, s);
+  return g.r <= 16 ? launch_uv_nt<DyT, 2>(g, sides, steps, sms, s) : launch_uv_nt<DyT, 4>(g, sides, steps, sms, s);
+}
+
+// u (where out_u is given) and v (out_v) of any number of tokens, in the
+// order of `rows` where it is given.
 bl_status launch_uv(const void* dy, bl_dtype dydt, const int8_t* xq, const float* eta, int64_t M, int64_t K, int64_t N,
-                    const AdapterSet& ad, float* out_u, float* out_v, int sms, cudaStream_t s) {
+                    const AdapterSet& ad, const int32_t* rows, float* out_u, float* out_v, int sms, cudaStream_t s) {
   bl::UvArgs g = {};
-  g.scale = ad.scale; g.ids = ad.ids; g.M = M; g.L = ad.L; g.r = ad.r;
+  g.scale = ad.scale; g.ids = ad.ids; g.rows = rows; g.M = M; g.L = ad.L; g.r = ad.r;
   int n = 0;
   if (out_v) g.side[n++] = {1, dy, N, ad.B, nullptr, out_v, N % 4 == 0 ? 1 : 0};
   if (out_u) g.side[n++] = {0, xq, K, ad.A, eta, out_u, K % 16 == 0 ? 1 : 0};
@@ -304,12 +328,13 @@ bl_status launch_dab_jt(const bl::DabArgs& g, dim3 grid, cudaStream_t s) {
 
 template <typename DyT, typename OutT>
 bl_status launch_dab(const void* dy, const int8_t* xq, const float* eta, int64_t M, int64_t K, int64_t N,
-                     const AdapterSet& ad, const float* u, const float* v, void* dA, void* dB, int sms, cudaStream_t s) {
+                     const AdapterSet& ad, const Order& o, const float* u, const float* v, void* dA, void* dB, int sms,
+                     cudaStream_t s) {
   const int64_t sa = (K + bl::kDabCols - 1) / bl::kDabCols, sb = (N + bl::kDabCols - 1) / bl::kDabCols;
   bl::DabArgs g = {};
   g.a = {xq, K, v, dA, K % 16 == 0 ? 1 : 0};
   g.b = {dy, N, u, dB, N % (sizeof(DyT) == 4 ? 4 : 8) == 0 ? 1 : 0};
-  g.eta = eta; g.ids = ad.ids; g.M = M; g.r = ad.r; g.slabs_a = static_cast<unsigned>(sa);
+  g.eta = eta; g.rows = o.rows; g.start = o.start; g.r = ad.r; g.slabs_a = static_cast<unsigned>(sa);
   // CTAs of a cluster along the tokens: while there are fewer than four CTAs
   // an SM, and two chunks of tokens for each
   int cs = 1;
@@ -325,13 +350,16 @@ bl_status launch_dab(const void* dy, const int8_t* xq, const float* eta, int64_t
 // multiple of 64 (rows of x~ padded with zeros, which meet any code).
 struct FaScratch {
   float* u;
+  Order order;  // rows NULL: not sorted
   Rows x, w;
   Pads pads;
 };
 
-inline void fa_scratch(const int8_t* xq, const uint8_t* packed, int64_t M, int64_t K, int64_t N, int64_t r, Scratch* ws,
-                       FaScratch* f) {
+// Tokens are sorted where a tile of 16 could meet several adapters.
+inline void fa_scratch(const int8_t* xq, const uint8_t* packed, int64_t M, int64_t K, int64_t N, int64_t L, int64_t r,
+                       Scratch* ws, FaScratch* f) {
   f->u = static_cast<float*>(ws->take(static_cast<size_t>(M * r * 4)));
+  f->order = M > 16 && L > 1 ? order_scratch(M, L, ws) : Order{nullptr, nullptr, nullptr};
   if (K % 64 == 0) {
     f->x = {xq, K, 1};
     f->w = {packed, K / 4, 1};
@@ -345,6 +373,17 @@ inline void fa_scratch(const int8_t* xq, const uint8_t* packed, int64_t M, int64
   f->pads.job[0] = {reinterpret_cast<const uint8_t*>(xq), M, K, kp, x};
   f->pads.job[1] = {packed, N, (K + 3) / 4, kp / 4, w};
   f->pads.n = 2;
+}
+
+// u of the forward pass.
+bl_status run_u(const FaScratch& f, int8_t* xq, float* eta, int64_t M, int64_t K, int64_t N, const AdapterSet& ad, int sms,
+                cudaStream_t s) {
+  if (few_tokens_u(M, K)) return launch_u_few(nullptr, xq, eta, nullptr, M, K, ad, f.u, sms, s);
+  if (f.order.rows) {
+    const bl_status st = launch_sort(ad, M, f.order, s);
+    if (st != BL_OK) return st;
+  }
+  return launch_uv(nullptr, BL_BF16, xq, eta, M, K, N, ad, f.order.rows, f.u, nullptr, sms, s);
 }
 
 // The projection with adapters, u given in f.
@@ -502,7 +541,7 @@ size_t bitlinear_forward_adapters_workspace_bytes(int64_t M, int64_t K, int64_t 
   if (train_sizes(M, N, K) != BL_OK || adapter_sizes(L, r, N, K) != BL_OK) return 0;
   Scratch ws(nullptr);
   FaScratch f;
-  fa_scratch(nullptr, nullptr, M, K, N, r, &ws, &f);
+  fa_scratch(nullptr, nullptr, M, K, N, L, r, &ws, &f);
   return ws.used;
 }
 
@@ -523,10 +562,9 @@ bl_status bitlinear_forward_adapters(const int8_t* xq, const float* eta, const i
   const cudaStream_t s = as_stream(stream);
   Scratch ws(workspace);
   FaScratch f;
-  fa_scratch(xq, packed, M, K, N, r, &ws, &f);
+  fa_scratch(xq, packed, M, K, N, L, r, &ws, &f);
   const AdapterSet ad = adapter_set(A, B, scale, ids, L, r);
-  st = few_tokens_u(M, K) ? launch_u_few(nullptr, const_cast<int8_t*>(xq), const_cast<float*>(eta), nullptr, M, K, ad, f.u, sms, s)
-                          : launch_uv(nullptr, BL_BF16, xq, eta, M, K, N, ad, f.u, nullptr, sms, s);
+  st = run_u(f, const_cast<int8_t*>(xq), const_cast<float*>(eta), M, K, N, ad, sms, s);  // neither is written
   return st == BL_OK ? run_forward_adapters(f, eta, xsum, M, gamma, N, ad, y, ydt, flags, sms, s) : st;
 }
 
@@ -561,7 +599,7 @@ bl_status bitlinear_linear_adapters(const void* x, bl_dtype xdt, int64_t M, int6
   LaScratch q;
   la_scratch(M, K, &ws, &q);
   FaScratch f;
-  fa_scratch(q.xq, packed, M, K, N, r, &ws, &f);
+  fa_scratch(q.xq, packed, M, K, N, L, r, &ws, &f);
   const AdapterSet ad = adapter_set(A, B, scale, ids, L, r);
   if (!norm && xdt == BL_BF16 && aligned(x, 16) && few_tokens_u(M, K)) {
     RegGeom rg;
@@ -582,9 +620,7 @@ bl_status bitlinear_linear_adapters(const void* x, bl_dtype xdt, int64_t M, int6
     st = norm ? rmsnorm_quant_impl(x, xdt, M, K, q.xq, q.eta, q.xsum, nullptr, stream)
               : bitlinear_quant_act(x, xdt, M, K, q.xq, q.eta, q.xsum, stream);
     if (st != BL_OK) return st;
-    st = few_tokens_u(M, K) ? launch_u_few(nullptr, q.xq, q.eta, q.xsum, M, K, ad, f.u, sms, s)
-                            : launch_uv(nullptr, BL_BF16, q.xq, q.eta, M, K, N, ad, f.u, nullptr, sms, s);
-    if (st != BL_OK) return st;
+    if ((st = run_u(f, q.xq, q.eta, M, K, N, ad, sms, s)) != BL_OK) return st;
   }
   return run_forward_adapters(f, q.eta, q.xsum, M, gamma, N, ad, y, ydt, flags, sms, s);
 }
@@ -595,6 +631,7 @@ size_t bitlinear_adapters_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, 
   Scratch ws(nullptr);
   ws.take(static_cast<size_t>(M) * r * 4);  // u
   ws.take(static_cast<size_t>(M) * r * 4);  // v
+  order_scratch(M, L, &ws);
   return ws.used + bitlinear_grad_input_workspace_bytes(M, N, K, dydt);
 }
 
@@ -621,15 +658,20 @@ bl_status bitlinear_adapters_grad(const void* dy, bl_dtype dydt, const int8_t* x
   Scratch ws(workspace);
   float* u = static_cast<float*>(ws.take(static_cast<size_t>(M) * r * 4));
   float* v = static_cast<float*>(ws.take(static_cast<size_t>(M) * r * 4));
+  const Order order = order_scratch(M, L, &ws);
   const AdapterSet ad = adapter_set(A, B, scale, ids, L, r);
-  if (M > 0 && (st = launch_uv(dy, dydt, xq, eta, M, K, N, ad, dA ? u : nullptr, v, sms, s)) != BL_OK) return st;
+  const bool sorted = dA != nullptr || (M > 16 && L > 1);
+  if (sorted && (st = launch_sort(ad, M, order, s)) != BL_OK) return st;
+  if (M > 0 && (st = launch_uv(dy, dydt, xq, eta, M, K, N, ad, sorted ? order.rows : nullptr, dA ? u : nullptr, v, sms, s)) !=
+                   BL_OK)
+    return st;
   if (dA) {  // no tokens: zeros
     if (dydt == BL_F32)
-      st = dabdt == BL_F32 ? launch_dab<float, float>(dy, xq, eta, M, K, N, ad, u, v, dA, dB, sms, s)
-                           : launch_dab<float, __nv_bfloat16>(dy, xq, eta, M, K, N, ad, u, v, dA, dB, sms, s);
+      st = dabdt == BL_F32 ? launch_dab<float, float>(dy, xq, eta, M, K, N, ad, order, u, v, dA, dB, sms, s)
+                           : launch_dab<float, __nv_bfloat16>(dy, xq, eta, M, K, N, ad, order, u, v, dA, dB, sms, s);
     else
-      st = dabdt == BL_F32 ? launch_dab<__nv_bfloat16, float>(dy, xq, eta, M, K, N, ad, u, v, dA, dB, sms, s)
-                           : launch_dab<__nv_bfloat16, __nv_bfloat16>(dy, xq, eta, M, K, N, ad, u, v, dA, dB, sms, s);
+      st = dabdt == BL_F32 ? launch_dab<__nv_bfloat16, float>(dy, xq, eta, M, K, N, ad, order, u, v, dA, dB, sms, s)
+                           : launch_dab<__nv_bfloat16, __nv_bfloat16>(dy, xq, eta, M, K, N, ad, order, u, v, dA, dB, sms, s);
     if (st != BL_OK) return st;
   }
   if (!dx || M == 0) return BL_OK;

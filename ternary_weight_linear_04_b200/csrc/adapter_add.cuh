@@ -117,32 +117,35 @@ __device__ __forceinline__ float bf16_part(float x, int p) {
   return x;  // to be rounded to bf16
 }
 
-// Eight entries of a token's row of u (or v) in the tensor-core kernels: its
-// own `group` = P r entries (P parts of r values) begin at entry `own`, the
-// rest are zeros; value(j) gives its j-th value.
+// Entries of the adapters' contraction in the tensor-core kernels: for each
+// adapter of a tile P parts of its r values, padded to rp (a multiple of 8,
+// or 1, 2 or 4), so that eight entries from a multiple of 8 on are whole
+// pairs (adapter, part), or lie inside one, and need one division.
+__host__ __device__ constexpr int padded_rank(int r) { return r > 4 ? (r + 7) / 8 * 8 : r == 3 ? 4 : r; }
+
+// Eight entries from e on of a token's row: its own adapter's begin at entry
+// `own`, the rest are zeros; value(j) gives its j-th value.
 template <int P, typename F>
-__device__ __forceinline__ uint4 own_entries(int e, int own, int r, F value) {
+__device__ __forceinline__ uint4 own_entries(int e, int own, int r, int rp, F value) {
   float f[8];
 #pragma unroll
   for (int b = 0; b < 8; ++b) {
-    const int i = e + b - own, p = i >= 2 * r ? 2 : i >= r ? 1 : 0;
-    f[b] = i >= 0 && i < P * r ? bf16_part<P>(value(i - p * r), p) : 0.0f;
+    const int i = e + b - own, p = i >= 2 * rp ? 2 : i >= rp ? 1 : 0, j = i - p * rp;
+    f[b] = i >= 0 && i < P * rp && j < r ? bf16_part<P>(value(j), p) : 0.0f;
   }
   const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(f[0], f[1]), __floats2bfloat162_rn(f[2], f[3]),
                                __floats2bfloat162_rn(f[4], f[5]), __floats2bfloat162_rn(f[6], f[7])};
   return reinterpret_cast<const uint4&>(h);
 }
 
-// Whether a pair of bf16 holds an infinity or a NaN.  The tensor-core kernels
-// multiply a factor of one adapter by the zeros that stand for the tokens of
-// the others; zero times infinity is not zero, so such factors are replaced
-// by zeros there and the outputs taken from plain sums over each token's own
-// adapter instead (slow, and only then).
+// Which of a pair of bf16 are infinities or NaN (the top bit of each half).
+// The tensor-core kernels multiply a factor of one adapter by the zeros that
+// stand for the tokens of the others, and zero times infinity is NaN.  Where
+// a sum can be formed again cheaply they do so for what comes out not
+// finite; the input gradient, whose sums are long, leaves such values out and
+// adds their terms for their own tokens.
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
   return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-}
-__device__ __forceinline__ bool nonfinite8(const uint4& v) {
-  return (nonfinite2(v.x) | nonfinite2(v.y) | nonfinite2(v.z) | nonfinite2(v.w)) != 0;
 }
 
 }  // namespace bl

@@ -49,6 +49,20 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
   return reinterpret_cast<const uint32_t&>(d);
 }
 
+// n words from an address that need not be on four bytes (all of the n + 1
+// aligned words that cover them have to be readable).
+template <int n>
+__device__ __forceinline__ void load_words(const void* p, uint32_t* o) {
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(at & ~uint64_t{3});
+  const unsigned sh = 8 * static_cast<unsigned>(at & 3);
+  uint32_t in[n + 1];
+#pragma unroll
+  for (int i = 0; i <= n; ++i) in[i] = __ldg(w + i);
+#pragma unroll
+  for (int i = 0; i < n; ++i) o[i] = __funnelshift_r(in[i], in[i + 1], sh);
+}
+
 // ---------------------------------------------------------------- u of up to 16 tokens
 //
 // Few tokens: every (token, rank index) is a dot product over K that reads
@@ -298,7 +312,7 @@ constexpr int kUvPitch = 40;     // bf16 of a staged row of B, the same
 constexpr size_t kUvSmem = kUvWarps * 64 * kUvPitch * 2;  // staged rows; the sums (16 rows a warp) take half
 static_assert(kUvWarps * 16 * kUvRedPitch * 4 <= kUvSmem, "the sums in the staged rows' place");
 
-// The plain sum for one output, where a factor is not finite.
+// The plain sum for one output.
 template <typename DyT>
 __device__ __noinline__ float uv_plain(const UvArgs& g, const UvSide& s, int64_t m, int a, int j) {
   float t = 0.0f;
@@ -340,6 +354,8 @@ struct UvRaw {
               o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
             }
           }
+        } else if (sizeof(XT) == 1 && k + 20 <= C) {
+          load_words<kW>(p, o);
         } else {
 #pragma unroll
           for (int j = 0; j < kEach; ++j) {
@@ -378,7 +394,7 @@ struct UvRaw {
 // another); four such tiles are in flight, so 4 / NT adapters.
 template <typename XT, int NT>
 __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_t* smem, const int* s_ids,
-                                        const int* s_list, int nad, volatile float* s_bad) {
+                                        const int* s_list, int nad) {
   constexpr bool V = sizeof(XT) > 1;
   constexpr int PX = sizeof(XT) == 4 ? 3 : 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, q = lane & 3;
@@ -403,7 +419,6 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-    bool bad = false;
     constexpr bool kAhead = sizeof(XT) < 4;  // fp32 rows: not enough registers for two steps
     UvRaw<XT> next;
     const int64_t first = warp * CS + z;
@@ -436,6 +451,9 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
                 w[x][1] = __ldg(reinterpret_cast<const uint4*>(f) + 1);
               } else {
                 uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (k + 18 <= C)
+                  load_words<8>(f, e);
+                else
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                   if (k + i < C)
@@ -469,14 +487,6 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
           own[x][0] = own0 == lb + x ? 0xFFFFFFFFu : 0u;
           own[x][1] = own1 == lb + x ? 0xFFFFFFFFu : 0u;
         }
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (nonfinite8(w[x][h])) {
-              bad = true;
-              w[x][h] = make_uint4(0, 0, 0, 0);
-            }
         if constexpr (!V) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -525,7 +535,6 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
         }
       }
     }
-    if (bad) *s_bad = 1.0f;
     __syncthreads();  // the staged rows are read
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -539,21 +548,19 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
     float t = 0.0f;
 #pragma unroll
     for (int w = 0; w < kUvWarps; ++w) t = __fadd_rn(t, mine[w * 16 * kUvRedPitch]);
-    bool any = *s_bad != 0.0f;
     if (CS > 1) {  // CTA 0 adds the cluster's
       *mine = t;
       cluster_sync_all();
-      if (z == 0) {
-        t = cluster_total(mine, CS);
-        any = cluster_total(const_cast<float*>(s_bad), CS) != 0.0f;
-      }
+      if (z == 0) t = cluster_total(mine, CS);
     }
     const int i = tid >> 5, j = tid & 31;
     if (z == 0 && j < 8 * NT && jb + j < r && m0 + i < g.M) {
       const int64_t m = token(i);
       if (s_ids[i] >= 0) {
         const int a = s_list[s_ids[i]];
-        if (any) t = uv_plain<typename std::conditional<V, XT, float>::type>(g, s, m, a, jb + j);
+        // zero times another adapter's infinity or NaN: the plain sum, in
+        // which it has no part
+        if (__fsub_rn(t, t) != 0.0f) t = uv_plain<typename std::conditional<V, XT, float>::type>(g, s, m, a, jb + j);
         if constexpr (!V) t = __fmul_rn(t, div127_rn(s.eta[m]));
         t = __fmul_rn(t, g.scale[a]);
       } else {
@@ -571,16 +578,12 @@ template <typename DyT, int NT>
 __global__ void __launch_bounds__(kUvThreads, 1) k_adapter_uv(const __grid_constant__ UvArgs g) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int s_ids[32], s_list[32], s_cnt[8];
-  __shared__ float s_bad;  // not zero: a factor is not finite
   pdl_wait();
-  if (threadIdx.x == 0) {
-    pdl_trigger();
-    s_bad = 0.0f;
-  }
+  if (threadIdx.x == 0) pdl_trigger();
   const UvSide& s = g.side[blockIdx.y];
   const int nad = tile_adapters(g.ids, g.rows, static_cast<int64_t>(blockIdx.x) * 16, g.M, 16, g.L, s_ids, s_list, s_cnt);
-  if (s.is_v) uv_tile<DyT, NT>(g, s, smem, s_ids, s_list, nad, &s_bad);
-  else uv_tile<int8_t, NT>(g, s, smem, s_ids, s_list, nad, &s_bad);
+  if (s.is_v) uv_tile<DyT, NT>(g, s, smem, s_ids, s_list, nad);
+  else uv_tile<int8_t, NT>(g, s, smem, s_ids, s_list, nad);
 }
 
 // ---------------------------------------------------------------- dA and dB

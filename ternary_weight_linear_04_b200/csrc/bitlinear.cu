@@ -679,15 +679,30 @@ bl_status launch_tc_bm(const int8_t* xq, const float* eta, const int32_t* xsum, 
                             y_int, ks, wstatic, ad);
 }
 
+// Tokens per tile: as many as there are, up to 256.  With adapters the tiles
+// (each with steps over its tokens' adapters) are made smaller, down to 64,
+// while they and their K splits leave a quarter of the GPU idle.
+template <bool AD>
+int tc_tokens(int M, int K, int N, int sms) {
+  int bm = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+  if (AD) {
+    const int64_t kt = (K + bl::kTcBK - 1) / bl::kTcBK, splits = kt < 4 ? 1 : (kt < 16 ? kt / 2 : 8);
+    while (bm > 64 && ((N + bl::kTcBN - 1) / bl::kTcBN) * ((int64_t{M} + bm - 1) / bm) * splits * 4 < int64_t{3} * sms) bm /= 2;
+  }
+  return bm;
+}
+
 template <typename OutT, bool AD>
 bl_status launch_tc_ad(const int8_t* xq, const float* eta, const int32_t* xsum, int M, int K,
                        const uint8_t* packed, const float* gamma, int N, void* y, int32_t* y_int,
                        int sms, int ws, cudaStream_t st, const bl::AdapterAdd& ad) {
-  if (M <= 16) return launch_tc_bm<16, OutT, AD>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
-  if (M <= 32) return launch_tc_bm<32, OutT, AD>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
-  if (M <= 64) return launch_tc_bm<64, OutT, AD>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
-  if (M <= 128) return launch_tc_bm<128, OutT, AD>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
-  return launch_tc_bm<256, OutT, AD>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
+  switch (tc_tokens<AD>(M, K, N, sms)) {
+    case 16: return launch_tc_bm<16, OutT, AD>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
+    case 32: return launch_tc_bm<32, OutT, AD>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
+    case 64: return launch_tc_bm<64, OutT, AD>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
+    case 128: return launch_tc_bm<128, OutT, AD>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
+    default: return launch_tc_bm<256, OutT, AD>(xq, eta, xsum, M, K, packed, gamma, N, y, y_int, sms, ws, st, ad);
+  }
 }
 
 template <typename OutT>

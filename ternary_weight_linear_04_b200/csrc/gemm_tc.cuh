@@ -125,8 +125,7 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
   int* s_ids = s_xsum + BM;    // AD
   int* s_list = s_ids + BM;
   int* s_cnt = s_list + BM;
-  volatile int* s_bad = s_cnt + 8;  // a factor is not finite
-  volatile int* s_entries = s_bad + 1;
+  volatile int* s_entries = s_cnt + 8;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -156,7 +155,6 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
     if constexpr (AD) {
       mbar_init(counted, 1);
       mbar_init(unpacked, 1);
-      *s_bad = 0;
     }
     mbar_init_fence();
     tma_prefetch_desc(&tm_x);
@@ -305,8 +303,8 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
   } else if constexpr (AD) {
     // ---------------- adapter operands (warps 10..17), then epilogue
     const int t = threadIdx.x - kTcThreads;
-    const int r = ad.r, group = kParts * r;  // entries of one adapter
-    const bool chunked = (r & 7) == 0;       // eight entries share adapter and part
+    const int r = ad.r, rp = padded_rank(r), group = kParts * rp;  // entries of one adapter
+    const bool chunked = (r & 7) == 0;                             // eight of them in one load
     int entries = 0;
     if (zr == 0)
       entries = tile_adapters(ad.ids, nullptr, m0, M, BM, ad.L, s_ids, s_list, s_cnt, t,
@@ -316,47 +314,42 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
       mbar_arrive(counted);
     }
     const int asteps = (entries + 63) >> 6;
-    // thread: feature t / 2 and half of a step's entries; tokens in pieces of
-    // one token and 8 entries
-    constexpr int kEach = BM * 8 / (32 * kTcAdWarps) > 0 ? BM * 8 / (32 * kTcAdWarps) : 1;
-    const int frow = t >> 1, fhalf = t & 1;
+    // A thread takes the piece t % 8 (8 entries) of the rows t / 8 + 32 x, of
+    // features and of tokens, so that a row's pieces are read together.
+    constexpr int kEach = BM > 32 ? BM / 32 : 1;
+    const int piece = t & 7, row0 = t >> 3;
     uint4 va[4], vu[kEach];
     auto load = [&](int e0) {
-      const int64_t n = n0 + frow;
+      const int e = e0 + 8 * piece;
+      const int pair = e / rp, j0 = e - pair * rp;
 #pragma unroll
       for (int wi = 0; wi < 4; ++wi) {
-        const int e = e0 + 32 * fhalf + 8 * wi;
+        const int64_t n = n0 + row0 + 32 * wi;
         va[wi] = make_uint4(0, 0, 0, 0);
         if (n < N && e < entries) {
           if (chunked) {
-            const int li = e / group, j = (e - li * group) % r;
-            va[wi] = __ldg(reinterpret_cast<const uint4*>(ad.B + (static_cast<int64_t>(s_list[li]) * N + n) * r + j));
+            va[wi] = __ldg(reinterpret_cast<const uint4*>(ad.B + (static_cast<int64_t>(s_list[pair / kParts]) * N + n) * r + j0));
           } else {
-            uint32_t w[4] = {0, 0, 0, 0};
-            int li = e / group, j = (e - li * group) % r, left = group - (e - li * group);  // of this adapter's entries
+            const int in = min(rp, 8) - 1, lg = __popc(in);
+            uint32_t h[8];
 #pragma unroll
-            for (int b = 0; b < 8; ++b)
-              if (e + b < entries) {
-                const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(ad.B) +
-                                         (static_cast<int64_t>(s_list[li]) * N + n) * r + j);
-                w[b >> 1] |= h << (16 * (b & 1));
-                if (++j == r) j = 0;
-                if (--left == 0) {
-                  left = group;
-                  ++li;
-                }
-              }
-            va[wi] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int b = 0; b < 8; ++b) {
+              const int j = j0 + (b & in);
+              h[b] = e + b < entries && j < r
+                         ? __ldg(reinterpret_cast<const uint16_t*>(ad.B) +
+                                 (static_cast<int64_t>(s_list[(pair + (b >> lg)) / kParts]) * N + n) * r + j)
+                         : 0u;
+            }
+            va[wi] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
           }
         }
       }
 #pragma unroll
       for (int y4 = 0; y4 < kEach; ++y4) {
-        const int q = t + 32 * kTcAdWarps * y4;
-        const int tok = q % BM, e = e0 + 8 * (q / BM);
+        const int tok = row0 + 32 * y4;
         vu[y4] = make_uint4(0, 0, 0, 0);
-        const int own = s_ids[tok] * group;
-        if (own < 0 || q >= BM * 8 || e + 8 <= own || e >= own + group) continue;
+        const int own = tok < BM ? s_ids[tok] * group : -1;
+        if (own < 0 || e + 8 <= own || e >= own + group) continue;
         const float* ut = ad.u + static_cast<int64_t>(m0 + tok) * r;
         if (chunked) {
           const int i = e - own, p = i >= 2 * r ? 2 : i >= r ? 1 : 0;
@@ -368,7 +361,7 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
           for (int b = 0; b < 8; ++b) f[b] = bf16_part<kParts>(g[b], p);
           vu[y4] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
         } else {
-          vu[y4] = own_entries<kParts>(e, own, r, [&](int j) { return ut[j]; });
+          vu[y4] = own_entries<kParts>(e, own, r, rp, [&](int j) { return ut[j]; });
         }
       }
     };
@@ -383,23 +376,12 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + s, static_cast<uint32_t>(i / S - 1) & 1u, abort_flag));
         if (!ok) break;
       }
-      uint8_t* dst = sA + s * Cfg::kABytes + (frow >> 3) * 1024 + (frow & 7) * 128;
+      const int at = (row0 >> 3) * 1024 + (row0 & 7) * 128 + ((piece ^ (row0 & 7)) << 4);  // 32 rows: 4096 bytes
 #pragma unroll
-      for (int wi = 0; wi < 4; ++wi) {
-        if (nonfinite8(va[wi])) {
-          va[wi] = make_uint4(0, 0, 0, 0);
-          *s_bad = 1;
-        }
-        *reinterpret_cast<uint4*>(dst + (((fhalf * 4 + wi) ^ (frow & 7)) << 4)) = va[wi];
-      }
+      for (int wi = 0; wi < 4; ++wi) *reinterpret_cast<uint4*>(sA + s * Cfg::kABytes + at + 4096 * wi) = va[wi];
 #pragma unroll
-      for (int y4 = 0; y4 < kEach; ++y4) {
-        const int q = t + 32 * kTcAdWarps * y4;
-        const int tok = q % BM, c = q / BM;
-        if (q < BM * 8)
-          *reinterpret_cast<uint4*>(sB + s * Cfg::kBBytes + (tok >> 3) * 1024 + (tok & 7) * 128 + ((c ^ (tok & 7)) << 4)) =
-              vu[y4];
-      }
+      for (int y4 = 0; y4 < kEach; ++y4)
+        if (row0 + 32 * y4 < BM) *reinterpret_cast<uint4*>(sB + s * Cfg::kBBytes + at + 4096 * y4) = vu[y4];
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full_a + s);
@@ -457,7 +439,7 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
   if (zr == 0 && epi_cols && epi_ok) {
     tc_fence_after();
     const int n = n0 + row;
-    const bool added = AD && *s_entries > 0, plain = AD && *s_bad != 0;
+    const bool added = AD && *s_entries > 0;
 #pragma unroll 1
     for (int cc = col0; cc < col0 + kColsPerWarp; cc += 16) {
       uint32_t v[16];
@@ -483,14 +465,18 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
         }
 #pragma unroll
         for (int j = 0; j < 16; ++j) f[j] = added ? __uint_as_float(w[j]) : 0.0f;
-        if (plain) {
+        // zero times another adapter's infinity or NaN: the plain sum
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum = __fmaf_rn(f[j], 0.0f, sum);
+        if (sum != 0.0f) {
 #pragma unroll 1
           for (int j = 0; j < 16; ++j) {
             const int m = m0 + cc + j;
-            const float sum = m < M && n < N ? adapter_add(ad.u, ad.B, ad.ids, ad.L, ad.r, m, n, N, 0.0f) : 0.0f;
+            const float own = m < M && n < N ? adapter_add(ad.u, ad.B, ad.ids, ad.L, ad.r, m, n, N, 0.0f) : 0.0f;
 #pragma unroll
             for (int k = 0; k < 16; ++k)
-              if (k == j) f[k] = sum;
+              if (k == j) f[k] = own;
           }
         }
       }

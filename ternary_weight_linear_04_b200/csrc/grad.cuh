@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kGiThreads, 1)
   }
   int entries = 0, ast = 0, alo = 0;  // entries of the tile's adapters, this CTA's steps of 64 of them
   if (a.v) {
-    entries = tile_adapters(a.ids, nullptr, m0, a.M, 128 * H, a.L, s_ids, s_list, s_cnt) * kParts * a.r;
+    entries = tile_adapters(a.ids, nullptr, m0, a.M, 128 * H, a.L, s_ids, s_list, s_cnt) * kParts * padded_rank(a.r);
     const int asteps = (entries + kGiBK - 1) / kGiBK;
     alo = asteps * z / CS;
     ast = asteps * (z + 1) / CS - alo;
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kGiThreads, 1)
       if (lane == 0) mbar_arrive(full_b + s);
     }
     // ---------------- adapters
-    const int r = a.r, group = kParts * r;
+    const int r = a.r, rp = padded_rank(r), group = kParts * rp;
     const float inv_gamma = ok && i < nall ? __frcp_rn(*a.gamma) : 0.0f;
     const bool avec = (a.K & 7) == 0, chunked = (r & 7) == 0;
     for (; ok && i < nall; i += kGiGroups) {
@@ -381,54 +381,56 @@ __global__ void __launch_bounds__(kGiThreads, 1)
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + s, static_cast<uint32_t>(i / S - 1) & 1u, abort_flag));
         if (!ok) break;
       }
-      {  // a row of A: one entry, 64 inputs
-        const int e = e0 + n, li = e / group, j = (e - li * group) % r;
+      {  // A: entry t / 4, 16 inputs of each 64 (four lanes read 128 bytes of a row)
+        const int en = t >> 2, wi = t & 3, e = e0 + en, pair = e / rp, j = e - pair * rp;
         uint32_t o[4][8];
         bool bad = false;
 #pragma unroll
-        for (int wi = 0; wi < 4; ++wi) {
-          const int k = k0 + 64 * q + 16 * wi;
+        for (int x = 0; x < 4; ++x) {
+          const int k = k0 + 64 * x + 16 * wi;
 #pragma unroll
-          for (int b = 0; b < 8; ++b) o[wi][b] = 0;
-          if (e < entries && k < a.K)
-            bad |= load16_paired(a.A + (static_cast<int64_t>(s_list[li]) * r + j) * a.K + k, a.K - k, avec, o[wi]);
+          for (int b = 0; b < 8; ++b) o[x][b] = 0;
+          if (e < entries && j < r && k < a.K)
+            bad |= load16_paired(a.A + (static_cast<int64_t>(s_list[pair / kParts]) * r + j) * a.K + k, a.K - k, avec, o[x]);
         }
         if (bad) *s_bad = 1.0f;
-        uint8_t* dst = dst0 + s * Cfg::kBBytes;
+        uint8_t* dst = sB + s * Cfg::kBBytes + (en >> 3) * 1024 + (en & 7) * 128;
 #pragma unroll
-        for (int wi = 0; wi < 4; ++wi) {
-          *reinterpret_cast<uint4*>(dst + (((2 * wi) ^ (n & 7)) << 4)) = make_uint4(o[wi][0], o[wi][1], o[wi][2], o[wi][3]);
-          *reinterpret_cast<uint4*>(dst + (((2 * wi + 1) ^ (n & 7)) << 4)) = make_uint4(o[wi][4], o[wi][5], o[wi][6], o[wi][7]);
+        for (int x = 0; x < 4; ++x) {
+          *reinterpret_cast<uint4*>(dst + x * (kGiBK * 128) + (((2 * wi) ^ (en & 7)) << 4)) =
+              make_uint4(o[x][0], o[x][1], o[x][2], o[x][3]);
+          *reinterpret_cast<uint4*>(dst + x * (kGiBK * 128) + (((2 * wi + 1) ^ (en & 7)) << 4)) =
+              make_uint4(o[x][4], o[x][5], o[x][6], o[x][7]);
         }
       }
-      // rows of v: a token's 64 entries (H = 1: two threads a token)
-      constexpr int kPer = H == 2 ? 8 : 4;
-      const int tok = H == 2 ? t : t >> 1, c0 = H == 2 ? 0 : 4 * (t & 1), own = s_ids[tok] * group;
-      const float* vr = a.v + static_cast<int64_t>(m0 + tok) * r;
-      uint8_t* row = sA + s * Cfg::kABytes + (tok >> 3) * 1024 + (tok & 7) * 128;
+      // v: piece t % 8 (8 entries) of the tokens t / 8 + 32 x
+      constexpr int kEach = 128 * H / 32;
+      const int piece = t & 7, tok0 = t >> 3, e = e0 + 8 * piece;
+      uint8_t* row = sA + s * Cfg::kABytes + (tok0 >> 3) * 1024 + (tok0 & 7) * 128 + ((piece ^ (tok0 & 7)) << 4);
 #pragma unroll
-      for (int h4 = 0; h4 < kPer; h4 += 4) {
+      for (int x4 = 0; x4 < kEach; x4 += 4) {
         uint4 o[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int e = e0 + 8 * (c0 + h4 + c);
+          const int tok = tok0 + 32 * (x4 + c), own = s_ids[tok] * group;
+          const float* vr = a.v + static_cast<int64_t>(m0 + tok) * r;
           o[c] = make_uint4(0, 0, 0, 0);
           if (own < 0 || e + 8 <= own || e >= own + group) continue;
           if (chunked) {
             const int i = e - own, p = i >= 2 * r ? 2 : i >= r ? 1 : 0;
-            const float4* x = reinterpret_cast<const float4*>(vr + i - p * r);
-            const float4 u = x[0], w = x[1];
+            const float4* y = reinterpret_cast<const float4*>(vr + i - p * r);
+            const float4 u = y[0], w = y[1];
             const float g[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
             float f[8];
 #pragma unroll
             for (int b = 0; b < 8; ++b) f[b] = bf16_part<kParts>(__fmul_rn(g[b], inv_gamma), p);
             o[c] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
           } else {
-            o[c] = own_entries<kParts>(e, own, r, [&](int j) { return __fmul_rn(vr[j], inv_gamma); });
+            o[c] = own_entries<kParts>(e, own, r, rp, [&](int j) { return __fmul_rn(vr[j], inv_gamma); });
           }
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(row + (((c0 + h4 + c) ^ (tok & 7)) << 4)) = o[c];
+        for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(row + 4096 * (x4 + c)) = o[c];
       }
       fence_proxy_async_smem();
       __syncwarp();

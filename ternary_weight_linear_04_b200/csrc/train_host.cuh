@@ -283,30 +283,32 @@ bl_status launch_sort(const AdapterSet& ad, int64_t M, const Order& o, cudaStrea
 }
 
 template <typename DyT, int NT>
-bl_status launch_uv_nt(const bl::UvArgs& g, int sides, int64_t steps, int sms, cudaStream_t s) {
-  static int done[kMaxDevices] = {0};
+bl_status launch_uv_nt(const bl::UvArgs& g, int sides, int64_t steps, cudaStream_t s) {
+  static int done[kMaxDevices] = {0}, room[kMaxDevices][9] = {{0}};
   auto kern = bl::k_adapter_uv<DyT, NT>;
   if (!ensure_smem(kern, bl::kUvSmem, done)) return BL_ERR_CUDA;
   const int64_t tiles = (g.M + 15) / 16;
   if (tiles > INT32_MAX) return BL_ERR_UNSUPPORTED;
-  // CTAs of a cluster along the contraction: while they fit beside one
-  // another and a warp keeps two steps
+  // CTAs of a cluster along the contraction: while the GPU has room for all
+  // of them at once and there are steps for all their warps
   int cs = 1;
-  while (cs < 4 && tiles * sides * cs * 2 <= sms && steps >= 4 * bl::kUvWarps * cs) cs *= 2;
+  while (cs < 8 && steps > bl::kUvWarps * cs &&
+         tiles * sides <= cluster_room(kern, bl::kUvThreads, bl::kUvSmem, 2 * cs, room))
+    cs *= 2;
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(sides), static_cast<unsigned>(cs));
   return launch_pdl_cluster(kern, grid, dim3(bl::kUvThreads), bl::kUvSmem, s, grid.z, g);
 }
 
 template <typename DyT>
-bl_status launch_uv_t(const bl::UvArgs& g, int sides, int64_t steps, int sms, cudaStream_t s) {
-  if (g.r <= 8) return launch_uv_nt<DyT, 1>(g, sides, steps, sms, s);
-  return g.r <= 16 ? launch_uv_nt<DyT, 2>(g, sides, steps, sms, s) : launch_uv_nt<DyT, 4>(g, sides, steps, sms, s);
+bl_status launch_uv_t(const bl::UvArgs& g, int sides, int64_t steps, cudaStream_t s) {
+  if (g.r <= 8) return launch_uv_nt<DyT, 1>(g, sides, steps, s);
+  return g.r <= 16 ? launch_uv_nt<DyT, 2>(g, sides, steps, s) : launch_uv_nt<DyT, 4>(g, sides, steps, s);
 }
 
 // u (where out_u is given) and v (out_v) of any number of tokens, in the
 // order of `rows` where it is given.
 bl_status launch_uv(const void* dy, bl_dtype dydt, const int8_t* xq, const float* eta, int64_t M, int64_t K, int64_t N,
-                    const AdapterSet& ad, const int32_t* rows, float* out_u, float* out_v, int sms, cudaStream_t s) {
+                    const AdapterSet& ad, const int32_t* rows, float* out_u, float* out_v, cudaStream_t s) {
   bl::UvArgs g = {};
   g.scale = ad.scale; g.ids = ad.ids; g.rows = rows; g.M = M; g.L = ad.L; g.r = ad.r;
   int n = 0;
@@ -314,7 +316,7 @@ bl_status launch_uv(const void* dy, bl_dtype dydt, const int8_t* xq, const float
   if (out_u) g.side[n++] = {0, xq, K, ad.A, eta, out_u, K % 16 == 0 ? 1 : 0};
   int64_t steps = out_v ? (N + 63) / 64 : 0;
   if (out_u && (K + 63) / 64 > steps) steps = (K + 63) / 64;
-  return out_v && dydt == BL_F32 ? launch_uv_t<float>(g, n, steps, sms, s) : launch_uv_t<__nv_bfloat16>(g, n, steps, sms, s);
+  return out_v && dydt == BL_F32 ? launch_uv_t<float>(g, n, steps, s) : launch_uv_t<__nv_bfloat16>(g, n, steps, s);
 }
 
 template <typename DyT, typename OutT, int JT>
@@ -383,7 +385,7 @@ bl_status run_u(const FaScratch& f, int8_t* xq, float* eta, int64_t M, int64_t K
     const bl_status st = launch_sort(ad, M, f.order, s);
     if (st != BL_OK) return st;
   }
-  return launch_uv(nullptr, BL_BF16, xq, eta, M, K, N, ad, f.order.rows, f.u, nullptr, sms, s);
+  return launch_uv(nullptr, BL_BF16, xq, eta, M, K, N, ad, f.order.rows, f.u, nullptr, s);
 }
 
 // The projection with adapters, u given in f.
@@ -662,7 +664,7 @@ bl_status bitlinear_adapters_grad(const void* dy, bl_dtype dydt, const int8_t* x
   const AdapterSet ad = adapter_set(A, B, scale, ids, L, r);
   const bool sorted = dA != nullptr || (M > 16 && L > 1);
   if (sorted && (st = launch_sort(ad, M, order, s)) != BL_OK) return st;
-  if (M > 0 && (st = launch_uv(dy, dydt, xq, eta, M, K, N, ad, sorted ? order.rows : nullptr, dA ? u : nullptr, v, sms, s)) !=
+  if (M > 0 && (st = launch_uv(dy, dydt, xq, eta, M, K, N, ad, sorted ? order.rows : nullptr, dA ? u : nullptr, v, s)) !=
                    BL_OK)
     return st;
   if (dA) {  // no tokens: zeros

@@ -7,6 +7,7 @@ Names follow the C entry points: ``pack_weights``, ``quant_act``,
 """
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -392,20 +393,26 @@ def _check(name, t, shape, *dtypes):
             str(t.dtype).replace("torch.", ""), tuple(t.shape)))
 
 
-def _out(out, shape, dtype, dev, name="out"):
-    """The caller's output, checked, or a new one."""
+def _out(out, shape, dtype, like, name="out"):
+    """The caller's output, checked, or a new one on the device of `like`."""
     if dtype not in _DTYPES:
         raise ValueError("%s must be float32 or bfloat16" % name)
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     _check(name, out, shape, *_DTYPES)
-    if not out.is_cuda or out.device != dev or not out.is_contiguous() or out.data_ptr() % 16:
+    if not out.is_cuda or out.device != like.device or not out.is_contiguous() or out.data_ptr() % 16:
         raise ValueError("%s must be contiguous, on the inputs' device and 16-byte aligned" % name)
     return out
 
 
-def _scratch(nbytes, dev):
-    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+def _scratch(nbytes, like):
+    return like.new_empty((nbytes,), dtype=torch.uint8) if nbytes else None
+
+
+@functools.lru_cache(maxsize=4096)
+def _ws_bytes(call, *sizes):
+    """bitlinear_<call>_workspace_bytes(*sizes), a function of the sizes alone."""
+    return getattr(_lib.lib(), "bitlinear_%s_workspace_bytes" % call)(*sizes)
 
 
 def _codes(xq, eta, M):
@@ -440,11 +447,11 @@ def grad_input(dy, packed, gamma, K, out_dtype=torch.bfloat16, stream=None, out=
     M, N = dy.shape
     _packed(packed, gamma, N, K)
     with _place(stream, dy, packed, gamma):
-        dx = _out(out, (M, K), out_dtype, dy.device)
+        dx = _out(out, (M, K), out_dtype, dy)
         L = _lib.lib()
         dt = _DTYPES[dy.dtype]
-        nws = L.bitlinear_grad_input_workspace_bytes(M, N, K, dt)
-        ws = _scratch(nws, dy.device)
+        nws = _ws_bytes("grad_input", M, N, K, dt)
+        ws = _scratch(nws, dy)
         dy, packed = _al16(dy), _al16(packed)
         check(L.bitlinear_grad_input(_ptr(dy), dt, M, N, _ptr(packed), _ptr(gamma), K, _ptr(dx),
                                      _DTYPES[dx.dtype], _ptr(ws), nws, _stream(None)), "bitlinear_grad_input")
@@ -460,11 +467,11 @@ def grad_weight(dy, xq, eta, out_dtype=torch.float32, stream=None, out=None):
     _codes(xq, eta, M)
     K = xq.shape[1]
     with _place(stream, dy, xq, eta):
-        dw = _out(out, (N, K), out_dtype, dy.device)
+        dw = _out(out, (N, K), out_dtype, dy)
         L = _lib.lib()
         dt, wt = _DTYPES[dy.dtype], _DTYPES[dw.dtype]
-        nws = L.bitlinear_grad_weight_workspace_bytes(M, N, K, dt, wt)
-        ws = _scratch(nws, dy.device)
+        nws = _ws_bytes("grad_weight", M, N, K, dt, wt)
+        ws = _scratch(nws, dy)
         dy, xq = _al16(dy), _al16(xq)
         check(L.bitlinear_grad_weight(_ptr(dy), dt, _ptr(xq), _ptr(eta), M, N, K, _ptr(dw), wt, _ptr(ws), nws,
                                       _stream(None)), "bitlinear_grad_weight")
@@ -482,7 +489,7 @@ def rmsnorm_grad(dn, xq, eta, rstd, out_dtype=torch.bfloat16, stream=None, out=N
     _check("xq", xq, (M, K), torch.int8)
     _check("rstd", rstd, (M,), torch.float32)
     with _place(stream, dn, xq, eta, rstd):
-        dx = _out(out, (M, K), out_dtype, dn.device)
+        dx = _out(out, (M, K), out_dtype, dn)
         check(_lib.lib().bitlinear_rmsnorm_grad(_ptr(dn), _DTYPES[dn.dtype], _ptr(xq), _ptr(eta), _ptr(rstd),
                                                 M, K, _ptr(dx), _DTYPES[dx.dtype], _stream(None)),
               "bitlinear_rmsnorm_grad")
@@ -503,10 +510,10 @@ def forward_adapters(xq, eta, xsum, packed, gamma, N, A, B, scale, ids, out_dtyp
     _packed(packed, gamma, N, K)
     n_ad, r = _adapters(A, B, scale, ids, M, N, K)
     with _place(stream, xq, eta, xsum, packed, gamma, A, B, scale, ids):
-        y = _out(out, (M, N), out_dtype, xq.device)
+        y = _out(out, (M, N), out_dtype, xq)
         L = _lib.lib()
-        nws = L.bitlinear_forward_adapters_workspace_bytes(M, K, N, n_ad, r)
-        ws = _scratch(nws, xq.device)
+        nws = _ws_bytes("forward_adapters", M, K, N, n_ad, r)
+        ws = _scratch(nws, xq)
         xq, packed, A, B = _al16(xq), _al16(packed), _al16(A), _al16(B)
         check(L.bitlinear_forward_adapters(
             _ptr(xq), _ptr(eta), _ptr(xsum), M, K, _ptr(packed), _ptr(gamma), N, _ptr(A), _ptr(B),
@@ -525,10 +532,10 @@ def linear_adapters(x, packed, gamma, N, A, B, scale, ids, out_dtype=torch.bfloa
     _packed(packed, gamma, N, K)
     n_ad, r = _adapters(A, B, scale, ids, M, N, K)
     with _place(stream, x, packed, gamma, A, B, scale, ids):
-        y = _out(out, (M, N), out_dtype, x.device)
+        y = _out(out, (M, N), out_dtype, x)
         L = _lib.lib()
-        nws = L.bitlinear_linear_adapters_workspace_bytes(M, K, N, n_ad, r)
-        ws = _scratch(nws, x.device)
+        nws = _ws_bytes("linear_adapters", M, K, N, n_ad, r)
+        ws = _scratch(nws, x)
         packed, A, B = _al16(packed), _al16(A), _al16(B)
         flags = (_lib.BL_FLAG_WEIGHTS_STATIC if weights_static else 0) | (_lib.BL_FLAG_RMSNORM if rmsnorm else 0)
         check(L.bitlinear_linear_adapters(
@@ -553,14 +560,13 @@ def adapters_grad(dy, xq, eta, packed, gamma, A, B, scale, ids, out_dtype=torch.
         _packed(packed, gamma, N, K)
     n_ad, r = _adapters(A, B, scale, ids, M, N, K)
     with _place(stream, dy, xq, eta, packed, gamma, A, B, scale, ids):
-        dev = dy.device
-        dx = _out(None, (M, K), out_dtype, dev) if want_dx else None
-        dA = _out(None, A.shape, grad_dtype, dev) if want_dab else None
-        dB = _out(None, B.shape, grad_dtype, dev) if want_dab else None
+        dx = _out(None, (M, K), out_dtype, dy) if want_dx else None
+        dA = _out(None, A.shape, grad_dtype, dy) if want_dab else None
+        dB = _out(None, B.shape, grad_dtype, dy) if want_dab else None
         L = _lib.lib()
         dt = _DTYPES[dy.dtype]
-        nws = L.bitlinear_adapters_grad_workspace_bytes(M, N, K, n_ad, r, dt)
-        ws = _scratch(nws, dev)
+        nws = _ws_bytes("adapters_grad", M, N, K, n_ad, r, dt)
+        ws = _scratch(nws, dy)
         dy, xq, packed, A, B = _al16(dy), _al16(xq), _al16(packed), _al16(A), _al16(B)
         check(L.bitlinear_adapters_grad(
             _ptr(dy), dt, _ptr(xq), _ptr(eta), M, N, K, _ptr(packed), _ptr(gamma), _ptr(A), _ptr(B),

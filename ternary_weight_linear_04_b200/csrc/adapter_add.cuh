@@ -10,8 +10,11 @@
 
 namespace bl {
 
+// u and v are kept with rows of rank_stride(r) values, zeros past r.
+__host__ __device__ constexpr int rank_stride(int r) { return (r + 3) / 4 * 4; }
+
 struct AdapterAdd {
-  const float* u;  // M x r; NULL: no adapters
+  const float* u;  // M x rank_stride(r); NULL: no adapters
   const __nv_bfloat16* B;  // L x N x r
   const int32_t* ids;
   int L, r;
@@ -30,7 +33,7 @@ __device__ __noinline__ float adapter_add(const float* u, const __nv_bfloat16* B
   const int a = adapter_of(ids, m, L);
   if (a < 0) return base;
   const __nv_bfloat16* b = B + (static_cast<int64_t>(a) * N + n) * r;
-  u += static_cast<int64_t>(m) * r;
+  u += static_cast<int64_t>(m) * rank_stride(r);
   float s = 0.0f;
   int j = 0;
   if ((r & 7) == 0) {
@@ -117,6 +120,20 @@ __device__ __forceinline__ float bf16_part(float x, int p) {
   return x;  // to be rounded to bf16
 }
 
+// n words from an address that need not be on four bytes (all of the n + 1
+// aligned words that cover them have to be readable).
+template <int n>
+__device__ __forceinline__ void load_words(const void* p, uint32_t* o) {
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(at & ~uint64_t{3});
+  const unsigned sh = 8 * static_cast<unsigned>(at & 3);
+  uint32_t in[n + 1];
+#pragma unroll
+  for (int i = 0; i <= n; ++i) in[i] = __ldg(w + i);
+#pragma unroll
+  for (int i = 0; i < n; ++i) o[i] = __funnelshift_r(in[i], in[i + 1], sh);
+}
+
 // Entries of the adapters' contraction in the tensor-core kernels: for each
 // adapter of a tile P parts of its r values, padded to rp (a multiple of 8,
 // or 1, 2 or 4), so that eight entries from a multiple of 8 on are whole
@@ -124,17 +141,29 @@ __device__ __forceinline__ float bf16_part(float x, int p) {
 __host__ __device__ constexpr int padded_rank(int r) { return r > 4 ? (r + 7) / 8 * 8 : r == 3 ? 4 : r; }
 
 // Eight entries from e on of a token's row: its own adapter's begin at entry
-// `own`, the rest are zeros; value(j) gives its j-th value.
-template <int P, typename F>
-__device__ __forceinline__ uint4 own_entries(int e, int own, int r, int rp, F value) {
-  float f[8];
+// `own`, the rest are zeros.  x: the token's row of u (or v), scaled by f.
+template <int P>
+__device__ __forceinline__ uint4 own_entries(int e, int own, int r, int rp, const float* x, float f) {
+  const int i0 = e - own, rs = rank_stride(r);
+  float v[8];
+  if (rp >= 8) {  // all of one part
+    const int p = i0 >= 2 * rp ? 2 : i0 >= rp ? 1 : 0, j = i0 - p * rp;
+    const float4 lo = *reinterpret_cast<const float4*>(x + j);
+    const float4 hi = j + 4 < rs ? *reinterpret_cast<const float4*>(x + j + 4) : make_float4(0, 0, 0, 0);
+    const float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-  for (int b = 0; b < 8; ++b) {
-    const int i = e + b - own, p = i >= 2 * rp ? 2 : i >= rp ? 1 : 0, j = i - p * rp;
-    f[b] = i >= 0 && i < P * rp && j < r ? bf16_part<P>(value(j), p) : 0.0f;
+    for (int b = 0; b < 8; ++b) v[b] = bf16_part<P>(__fmul_rn(y[b], f), p);
+  } else {
+    const float4 y = *reinterpret_cast<const float4*>(x);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const int i = i0 + b, p = i >= 2 * rp ? 2 : i >= rp ? 1 : 0, j = i - p * rp;
+      const float w = j == 0 ? y.x : j == 1 ? y.y : j == 2 ? y.z : y.w;  // zero past r
+      v[b] = i >= 0 && i < P * rp ? bf16_part<P>(__fmul_rn(w, f), p) : 0.0f;
+    }
   }
-  const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(f[0], f[1]), __floats2bfloat162_rn(f[2], f[3]),
-                               __floats2bfloat162_rn(f[4], f[5]), __floats2bfloat162_rn(f[6], f[7])};
+  const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3]),
+                               __floats2bfloat162_rn(v[4], v[5]), __floats2bfloat162_rn(v[6], v[7])};
   return reinterpret_cast<const uint4&>(h);
 }
 

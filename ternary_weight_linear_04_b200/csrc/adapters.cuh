@@ -49,20 +49,6 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
   return reinterpret_cast<const uint32_t&>(d);
 }
 
-// n words from an address that need not be on four bytes (all of the n + 1
-// aligned words that cover them have to be readable).
-template <int n>
-__device__ __forceinline__ void load_words(const void* p, uint32_t* o) {
-  const uint64_t at = reinterpret_cast<uint64_t>(p);
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(at & ~uint64_t{3});
-  const unsigned sh = 8 * static_cast<unsigned>(at & 3);
-  uint32_t in[n + 1];
-#pragma unroll
-  for (int i = 0; i <= n; ++i) in[i] = __ldg(w + i);
-#pragma unroll
-  for (int i = 0; i < n; ++i) o[i] = __funnelshift_r(in[i], in[i + 1], sh);
-}
-
 // ---------------------------------------------------------------- u of up to 16 tokens
 //
 // Few tokens: every (token, rank index) is a dot product over K that reads
@@ -89,9 +75,11 @@ __global__ void __launch_bounds__(kAuThreads)
   if (tid == 0) pdl_trigger();
   const int a = adapter_of(ids, m, L);
   const bool writes = FUSE && xq != nullptr && blockIdx.x == 0;
+  const int rs = rank_stride(r);
+  if (blockIdx.x == 0 && r + tid < rs) u[m * rs + r + tid] = 0.0f;
   if (a < 0) {
     for (int j = blockIdx.x * group + tid; j < min(r, static_cast<int>(blockIdx.x + 1) * group); j += kAuThreads)
-      u[m * r + j] = 0.0f;
+      u[m * rs + j] = 0.0f;
     if (!writes) return;
   }
   uint2 q[kAuChunks];
@@ -182,7 +170,7 @@ __global__ void __launch_bounds__(kAuThreads)
     if (tid == 0) {
       s = 0.0f;
       for (int w = 0; w < kAuThreads / 32; ++w) s += s_red[(jj & 1) ^ 1][w];
-      u[m * r + j] = __fmul_rn(__fmul_rn(s, f), sc);
+      u[m * rs + j] = __fmul_rn(__fmul_rn(s, f), sc);
     }
   }
 }
@@ -292,7 +280,7 @@ struct UvSide {
   int64_t C;               // contraction
   const __nv_bfloat16* F;
   const float* eta;        // u
-  float* out;              // M x r
+  float* out;              // M x rank_stride(r)
   int vec;                 // rows of x (and of A) can be read in vectors
 };
 
@@ -554,19 +542,19 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
       if (z == 0) t = cluster_total(mine, CS);
     }
     const int i = tid >> 5, j = tid & 31;
-    if (z == 0 && j < 8 * NT && jb + j < r && m0 + i < g.M) {
+    if (z == 0 && j < 8 * NT && jb + j < rank_stride(r) && m0 + i < g.M) {
       const int64_t m = token(i);
       if (s_ids[i] >= 0) {
         const int a = s_list[s_ids[i]];
         // zero times another adapter's infinity or NaN: the plain sum, in
         // which it has no part
-        if (__fsub_rn(t, t) != 0.0f) t = uv_plain<typename std::conditional<V, XT, float>::type>(g, s, m, a, jb + j);
+        if (__fsub_rn(t, t) != 0.0f && jb + j < r) t = uv_plain<typename std::conditional<V, XT, float>::type>(g, s, m, a, jb + j);
         if constexpr (!V) t = __fmul_rn(t, div127_rn(s.eta[m]));
         t = __fmul_rn(t, g.scale[a]);
       } else {
         t = 0.0f;
       }
-      s.out[m * r + jb + j] = t;
+      s.out[m * rank_stride(r) + jb + j] = jb + j < r ? t : 0.0f;
     }
     if (CS > 1) cluster_sync_all();
     else __syncthreads();
@@ -600,7 +588,7 @@ __global__ void __launch_bounds__(kUvThreads, 1) k_adapter_uv(const __grid_const
 struct DabSide {
   const void* x;     // M x C: codes (dA) or dy (dB)
   int64_t C;
-  const float* coef;  // M x r
+  const float* coef;  // M x rank_stride(r)
   void* out;
   int vec;           // rows of x can be read in 16-byte pieces
 };
@@ -651,7 +639,6 @@ __device__ __forceinline__ void dab_tile(const DabArgs& g, const DabSide& s, int
   constexpr int kCoefs = 8 * JT;
   uint32_t xr[kXRegs];
   float cf[kCoefs];
-  const bool cvec = (r & 3) == 0;
   auto load = [&](int at) {  // the 64 tokens from place `at` on
     const bool in = at + xt < to;
     const int64_t m = in ? g.rows[at + xt] : 0;
@@ -682,21 +669,11 @@ __device__ __forceinline__ void dab_tile(const DabArgs& g, const DabSide& s, int
       }
     }
     const float f = in && is_a ? div127_rn(__ldg(g.eta + m)) : 1.0f;
-    const float* cp = s.coef + m * r;
+    const float* cp = s.coef + m * rank_stride(r);
 #pragma unroll
     for (int i = 0; i < kCoefs; i += 4) {
       const int j = xh * (rows / 2) + i;  // rows / 2 <= kCoefs; what passes it is not stored
-      float4 v = make_float4(0, 0, 0, 0);
-      if (in && i < rows / 2) {
-        if (cvec) {
-          if (j < r) v = *reinterpret_cast<const float4*>(cp + j);
-        } else {
-          if (j < r) v.x = cp[j];
-          if (j + 1 < r) v.y = cp[j + 1];
-          if (j + 2 < r) v.z = cp[j + 2];
-          if (j + 3 < r) v.w = cp[j + 3];
-        }
-      }
+      const float4 v = in && i < rows / 2 && j < r ? *reinterpret_cast<const float4*>(cp + j) : make_float4(0, 0, 0, 0);
       cf[i] = __fmul_rn(v.x, f);
       cf[i + 1] = __fmul_rn(v.y, f);
       cf[i + 2] = __fmul_rn(v.z, f);

@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
     const int t = threadIdx.x - kTcThreads;
     const int r = ad.r, rp = padded_rank(r), group = kParts * rp;  // entries of one adapter
     const bool chunked = (r & 7) == 0;                             // eight of them in one load
+    const int64_t total = static_cast<int64_t>(ad.L) * N * r;
     int entries = 0;
     if (zr == 0)
       entries = tile_adapters(ad.ids, nullptr, m0, M, BM, ad.L, s_ids, s_list, s_cnt, t,
@@ -330,17 +331,24 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
           if (chunked) {
             va[wi] = __ldg(reinterpret_cast<const uint4*>(ad.B + (static_cast<int64_t>(s_list[pair / kParts]) * N + n) * r + j0));
           } else {
-            const int in = min(rp, 8) - 1, lg = __popc(in);
-            uint32_t h[8];
+            const int64_t at = (static_cast<int64_t>(s_list[pair / kParts]) * N + n) * r + j0;
+            if (rp >= 8 && at + 10 <= total) {  // with the next row's first values, which meet zeros of u
+              uint32_t w[4];
+              load_words<4>(ad.B + at, w);
+              va[wi] = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+              const int in = min(rp, 8) - 1, lg = __popc(in);
+              uint32_t h[8];
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
-              const int j = j0 + (b & in);
-              h[b] = e + b < entries && j < r
-                         ? __ldg(reinterpret_cast<const uint16_t*>(ad.B) +
-                                 (static_cast<int64_t>(s_list[(pair + (b >> lg)) / kParts]) * N + n) * r + j)
-                         : 0u;
+              for (int b = 0; b < 8; ++b) {
+                const int j = j0 + (b & in);
+                h[b] = e + b < entries && j < r
+                           ? __ldg(reinterpret_cast<const uint16_t*>(ad.B) +
+                                   (static_cast<int64_t>(s_list[(pair + (b >> lg)) / kParts]) * N + n) * r + j)
+                           : 0u;
+              }
+              va[wi] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
             }
-            va[wi] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
           }
         }
       }
@@ -350,19 +358,7 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
         vu[y4] = make_uint4(0, 0, 0, 0);
         const int own = tok < BM ? s_ids[tok] * group : -1;
         if (own < 0 || e + 8 <= own || e >= own + group) continue;
-        const float* ut = ad.u + static_cast<int64_t>(m0 + tok) * r;
-        if (chunked) {
-          const int i = e - own, p = i >= 2 * r ? 2 : i >= r ? 1 : 0;
-          const float4* x = reinterpret_cast<const float4*>(ut + i - p * r);
-          const float4 lo = x[0], hi = x[1];
-          const float g[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-          float f[8];
-#pragma unroll
-          for (int b = 0; b < 8; ++b) f[b] = bf16_part<kParts>(g[b], p);
-          vu[y4] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-        } else {
-          vu[y4] = own_entries<kParts>(e, own, r, rp, [&](int j) { return ut[j]; });
-        }
+        vu[y4] = own_entries<kParts>(e, own, r, rp, ad.u + static_cast<int64_t>(m0 + tok) * rank_stride(r), 1.0f);
       }
     };
     if (asteps > 0) load(0);

@@ -153,7 +153,7 @@ struct GiArgs {
   void* dx;
   int vec;           // rows of dx take 16-byte stores
   // adapters (v NULL: none)
-  const float* v;    // M x r
+  const float* v;    // M x rank_stride(r)
   const __nv_bfloat16* A;  // L x r x K
   const int32_t* ids;
   int L, r;
@@ -194,7 +194,7 @@ __device__ __noinline__ float gi_nonfinite(const float* v, const __nv_bfloat16* 
   float s = 0.0f;
   for (int j = 0; j < r; ++j) {
     const float w = __bfloat162float(A[(static_cast<int64_t>(a) * r + j) * K + k]);
-    if (__fsub_rn(w, w) != 0.0f) s = __fmaf_rn(v[static_cast<int64_t>(m) * r + j], w, s);
+    if (__fsub_rn(w, w) != 0.0f) s = __fmaf_rn(v[static_cast<int64_t>(m) * rank_stride(r) + j], w, s);
   }
   return s;
 }
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kGiThreads, 1)
     // ---------------- adapters
     const int r = a.r, rp = padded_rank(r), group = kParts * rp;
     const float inv_gamma = ok && i < nall ? __frcp_rn(*a.gamma) : 0.0f;
-    const bool avec = (a.K & 7) == 0, chunked = (r & 7) == 0;
+    const bool avec = (a.K & 7) == 0;
     for (; ok && i < nall; i += kGiGroups) {
       const int s = i % S, e0 = (alo + i - nst) * kGiBK;
       if (i >= S) {
@@ -413,21 +413,9 @@ __global__ void __launch_bounds__(kGiThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int tok = tok0 + 32 * (x4 + c), own = s_ids[tok] * group;
-          const float* vr = a.v + static_cast<int64_t>(m0 + tok) * r;
           o[c] = make_uint4(0, 0, 0, 0);
           if (own < 0 || e + 8 <= own || e >= own + group) continue;
-          if (chunked) {
-            const int i = e - own, p = i >= 2 * r ? 2 : i >= r ? 1 : 0;
-            const float4* y = reinterpret_cast<const float4*>(vr + i - p * r);
-            const float4 u = y[0], w = y[1];
-            const float g[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-            float f[8];
-#pragma unroll
-            for (int b = 0; b < 8; ++b) f[b] = bf16_part<kParts>(__fmul_rn(g[b], inv_gamma), p);
-            o[c] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-          } else {
-            o[c] = own_entries<kParts>(e, own, r, rp, [&](int j) { return __fmul_rn(vr[j], inv_gamma); });
-          }
+          o[c] = own_entries<kParts>(e, own, r, rp, a.v + static_cast<int64_t>(m0 + tok) * rank_stride(r), inv_gamma);
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(row + 4096 * (x4 + c)) = o[c];

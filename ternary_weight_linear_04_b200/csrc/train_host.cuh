@@ -360,7 +360,7 @@ struct FaScratch {
 // Tokens are sorted where a tile of 16 could meet several adapters.
 inline void fa_scratch(const int8_t* xq, const uint8_t* packed, int64_t M, int64_t K, int64_t N, int64_t L, int64_t r,
                        Scratch* ws, FaScratch* f) {
-  f->u = static_cast<float*>(ws->take(static_cast<size_t>(M * r * 4)));
+  f->u = static_cast<float*>(ws->take(static_cast<size_t>(M * bl::rank_stride(static_cast<int>(r)) * 4)));
   f->order = M > 16 && L > 1 ? order_scratch(M, L, ws) : Order{nullptr, nullptr, nullptr};
   if (K % 64 == 0) {
     f->x = {xq, K, 1};
@@ -631,8 +631,7 @@ size_t bitlinear_adapters_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, 
                                                bl_dtype dydt) {
   if (train_sizes(M, N, K) != BL_OK || adapter_sizes(L, r, N, K) != BL_OK || !dtype_ok(dydt)) return 0;
   Scratch ws(nullptr);
-  ws.take(static_cast<size_t>(M) * r * 4);  // u
-  ws.take(static_cast<size_t>(M) * r * 4);  // v
+  for (int i = 0; i < 2; ++i) ws.take(static_cast<size_t>(M) * bl::rank_stride(static_cast<int>(r)) * 4);  // u, v
   order_scratch(M, L, &ws);
   return ws.used + bitlinear_grad_input_workspace_bytes(M, N, K, dydt);
 }
@@ -658,8 +657,9 @@ bl_status bitlinear_adapters_grad(const void* dy, bl_dtype dydt, const int8_t* x
   if ((st = device_info(&sms)) != BL_OK) return st;
   const cudaStream_t s = as_stream(stream);
   Scratch ws(workspace);
-  float* u = static_cast<float*>(ws.take(static_cast<size_t>(M) * r * 4));
-  float* v = static_cast<float*>(ws.take(static_cast<size_t>(M) * r * 4));
+  const size_t rank_bytes = static_cast<size_t>(M) * bl::rank_stride(static_cast<int>(r)) * 4;
+  float* u = static_cast<float*>(ws.take(rank_bytes));
+  float* v = static_cast<float*>(ws.take(rank_bytes));
   const Order order = order_scratch(M, L, &ws);
   const AdapterSet ad = adapter_set(A, B, scale, ids, L, r);
   const bool sorted = dA != nullptr || (M > 16 && L > 1);

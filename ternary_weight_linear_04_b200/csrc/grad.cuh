@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kGiThreads, 1)
     if (CS > 1) cluster_sync_all();
     else __syncthreads();
     // this CTA's rows of the finished tile, four columns a thread
-    const int rows = 128 / CS, row0 = z * rows;
+    const int row0 = 128 * z / CS, rows = 128 * (z + 1) / CS - row0;
     if (*abort_flag == 0)
       for (int e = threadIdx.x; e < rows * (kGiBN / 4); e += kGiThreads) {
         const int row = row0 + e / (kGiBN / 4), c = e % (kGiBN / 4) * 4, k = k0 + c;

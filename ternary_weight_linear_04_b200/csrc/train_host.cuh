@@ -149,12 +149,13 @@ bl_status launch_gi(const CUtensorMap& tdy, const CUtensorMap& tw, const bl::GiA
   if (tiles > INT32_MAX) return BL_ERR_UNSUPPORTED;
   int split = 1;
   if (H == 1) {
-    // as many CTAs along the contraction as the GPU has room for beside the
-    // tiles (a power of two, so that they share the tile's rows evenly), four
-    // steps each at least.  77 x 3200 x 8640, 34 tiles: 32 us with one CTA a
-    // tile, 21 with two, 27 with four, which do not all fit
+    // as many CTAs along the contraction, up to 8, as the GPU has room for
+    // beside the tiles, four steps each at least.  77 x 3200 x 8640, 34 tiles:
+    // 32 us with one CTA a tile, 21 with two, 27 with four, which do not all
+    // fit
     const int64_t steps = (int64_t{a.N} + bl::kGiBK - 1) / bl::kGiBK * a.planes;
-    while (split < 8 && steps >= 8 * split && tiles <= cluster_room(kern, bl::kGiThreads, smem, 2 * split, room)) split *= 2;
+    split = steps >= 32 ? 8 : steps >= 8 ? static_cast<int>(steps / 4) : 1;
+    while (split > 1 && tiles > cluster_room(kern, bl::kGiThreads, smem, split, room)) --split;
   }
   const dim3 grid(static_cast<unsigned>(tiles), 1, static_cast<unsigned>(split));
   return launch_pdl_cluster(kern, grid, dim3(bl::kGiThreads), smem, s, grid.z, tdy, tw, a);

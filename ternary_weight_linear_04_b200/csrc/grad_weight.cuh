@@ -5,11 +5,11 @@
 // as an exact integer contraction on the tensor core (tcgen05 kind::i8).
 //
 // The tokens are int8 already.  The other factor, g[m,n] = dy[m,n] f_m, is
-// held in fixed point: over each chunk of 512 tokens a column n gets the
+// held in fixed point: over each chunk of 1024 tokens a column n gets the
 // power of two that brings its largest |g| just below the top of ND signed
 // base-256 digits (k_gw_operands), q = round(g 2^e) = sum_j d_j 256^j with
 // d_j in [-128, 127].  The MMA sums d_j x~ over a chunk without any rounding
-// (at most 512 * 128 * 127 < 2^23), and the epilogue adds D_j 256^j 2^-e to
+// (at most 1024 * 128 * 127 < 2^24, so exact in fp32 too), and the epilogue adds D_j 256^j 2^-e to
 // fp32 accumulators in registers.  ND = 3 (23 bits beside the column's
 // largest value in the chunk) for fp32 results, ND = 2 (15 bits, against
 // the 8 of the result) for bf16 ones.
@@ -33,12 +33,13 @@
 
 namespace bl {
 
-constexpr int kGwChunk = 512;  // tokens that share a column's exponent
+constexpr int kGwChunk = 1024;  // tokens that share a column's exponent
+constexpr int kGdTokens = 512;  // of a CTA that makes digits; two CTAs share a chunk
 
 // ---------------------------------------------------------------- operands
 
-// Digits of a 64-column, 512-token tile: lane = two neighbouring columns, a
-// warp takes 32 tokens, held as they were read (two bf16 in a register)
+// Digits of a 64-column, 512-token tile (a cluster of two CTAs makes a chunk's
+// and shares its maxima): lane = two neighbouring columns, a warp takes 32 tokens, held as they were read (two bf16 in a register)
 // between the column's maximum and the digits.  digits: ND planes of N x Mp
 // bytes (Mp a multiple of 16, zero past M); scale[chunk * N + n] = 2^-e, or
 // NaN where the column holds an infinity or a NaN (its whole gradient row is
@@ -113,18 +114,19 @@ __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
   constexpr int kRegs = sizeof(DyT) == 2 ? 1 : 2;
   extern __shared__ __align__(16) uint8_t smem[];  // ND x 64 columns x 512 bytes, words XORed with the lane
   __shared__ uint32_t s_max[16][kGdCols];
-  __shared__ float s_f[kGwChunk];
+  __shared__ uint32_t s_col[kGdCols];
+  __shared__ float s_f[kGdTokens];
   __shared__ uint32_t s_codes[64][33];
   uint32_t* words = reinterpret_cast<uint32_t*>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t ntiles = (N + kGdCols - 1) / kGdCols;
-  const int64_t chunk = blockIdx.x / ntiles;
-  const int64_t n0 = (blockIdx.x % ntiles) * kGdCols, n = n0 + 2 * lane;
-  const int64_t mc = chunk * kGwChunk;
+  const int64_t chunk = (blockIdx.x >> 1) / ntiles;
+  const int64_t n0 = ((blockIdx.x >> 1) % ntiles) * kGdCols, n = n0 + 2 * lane;
+  const int64_t mc = chunk * kGwChunk + (blockIdx.x & 1) * kGdTokens;
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
   if (blockIdx.x >= digit_blocks) {
-    gw_codes_tile(xq, M, K, Mp, blockIdx.x - digit_blocks, s_codes, xt);
+    if (blockIdx.x - digit_blocks < (K + 63) / 64 * ((M + 127) / 128)) gw_codes_tile(xq, M, K, Mp, blockIdx.x - digit_blocks, s_codes, xt);
     return;
   }
   uint32_t raw[32][kRegs];
@@ -173,11 +175,21 @@ __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
   }
   *reinterpret_cast<uint2*>(&s_max[warp][2 * lane]) = make_uint2(mx[0], mx[1]);
   __syncthreads();
+  if (threadIdx.x < kGdCols) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) t = max(t, s_max[w][threadIdx.x]);
+    s_col[threadIdx.x] = t;
+  }
+  cluster_sync_all();
+  const uint32_t other = cluster_ctarank() ^ 1u;
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    mx[c] = max(s_col[2 * lane + c], __float_as_uint(ld_cluster_f32(cluster_map(&s_col[2 * lane + c], other))));
+  cluster_sync_all();  // the other CTA has read this one's
   float up[2];
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-#pragma unroll
-    for (int w = 0; w < 16; ++w) mx[c] = max(mx[c], s_max[w][2 * lane + c]);
     // 2^e with the largest |g| 2^e in [2^kBits, 2^(kBits+1)), one less if that
     // passes kTop; kept where 2^e and 2^-e are normal numbers
     int e = kBits + 127 - static_cast<int>(mx[c] >> 23);
@@ -185,7 +197,7 @@ __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
     if (__fmul_rn(__uint_as_float(mx[c]), __uint_as_float(static_cast<uint32_t>(e + 127) << 23)) > kTop) --e;
     const bool finite = mx[c] < 0x7F800000u;
     up[c] = finite ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 0.0f;
-    if (warp == 0 && n + c < N)
+    if (warp == 0 && n + c < N && (blockIdx.x & 1) == 0)
       scale[chunk * N + n + c] = finite ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : __uint_as_float(0x7FC00000u);
   }
 #pragma unroll
@@ -219,25 +231,30 @@ __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
 
 // ---------------------------------------------------------------- product
 //
-// Persistent CTAs, tiles of 128 outputs n (TMEM lanes) by 256 inputs k
-// (columns).  For each chunk of 512 tokens the codes' four 256 x 128-token
-// blocks stay in shared memory while the ND digit planes pass through a ring
-// of 128 x 128-token tiles against them: one digit of one chunk is a pass of
-// four steps into one of two TMEM accumulators, and eight warps add the
-// finished pass to their registers (128 values a thread) while the next one
-// runs into the other.  Digits go from high to low.
+// Persistent pairs of CTAs, tiles of 256 outputs n (128 TMEM lanes of each
+// CTA) by 256 inputs k (columns).  For each chunk of 1024 tokens the codes'
+// eight 256 x 128-token blocks (half in each CTA) stay in shared memory while
+// the ND digit planes pass through a ring of 128 x 128-token tiles against
+// them: one digit of one chunk is a pass of eight steps into one of two TMEM
+// accumulators, and eight warps of each CTA add the finished pass to their
+// registers (128 values a thread) while the next one runs into the other.
+// Digits go from high to low.  One CTA a tile (128 x 256) reads 12 KB of
+// shared memory for each MMA of 128 cycles beside 4 KB that TMA writes, all
+// that it can; a pair reads 8 KB in each.
 
 constexpr int kGwBM = 128;   // tokens per step
 constexpr int kGwBN = 256;   // inputs per tile
-constexpr int kGwSlots = 4;  // code blocks held
+constexpr int kGwRows = 256;  // outputs per tile
+constexpr int kGwPer = kGwChunk / kGwBM;  // blocks of codes in a chunk
+constexpr int kGwSlots = kGwPer;  // blocks held: a chunk's, each replaced by the next one's after its last digit
 constexpr int kGwStages = 5;
-constexpr int kGwThreads = 32 * 10;
-constexpr int kGwABytes = 128 * kGwBM, kGwBBytes = kGwBN * kGwBM;
+constexpr int kGwAddWarps = 8;  // accumulate: 128 columns each
+constexpr int kGwThreads = 32 * (2 + kGwAddWarps);
+constexpr int kGwABytes = 128 * kGwBM, kGwBBytes = kGwBN / 2 * kGwBM;  // of one CTA
 constexpr int kGwBars = 2 * kGwStages + 2 * kGwSlots + 4 + 1;
-constexpr int kGwPatch = 32 * 17;  // floats of a warp's 32 x 16 outputs, turned for rows that take no vectors
-constexpr size_t kGwSmem = 1024 + kGwStages * kGwABytes + kGwSlots * kGwBBytes + 8 * 4 * kGwPatch + 8 * kGwBars + 16;
+constexpr int kGwPatch = 32 * 17;  // floats of a warp's 32 x 16 outputs, turned for the stores
+constexpr size_t kGwSmem = 1024 + kGwStages * kGwABytes + kGwSlots * kGwBBytes + kGwAddWarps * 4 * kGwPatch + 8 * kGwBars + 16;
 static_assert(kGwSmem <= 227 * 1024, "shared memory per CTA");
-static_assert(kGwChunk == kGwSlots * kGwBM, "a chunk's codes are held whole");
 
 // Position in a ring of n barriers: slot and phase parity.  A consumer waits
 // for `full` with the parity, a producer for `empty` with its opposite (a
@@ -253,55 +270,37 @@ struct Ring {
   }
 };
 
-// acc += v sc for 16 sums of a pass.  Sums below 2^22 (all but freak ones;
-// the bound is 2^23) become fp32 by adding the bits of 1.5 2^23 and taking it
-// off again, two adds instead of a conversion at a quarter of their rate.
-__device__ __forceinline__ void add_pass(const uint32_t (&v)[16], float sc, float* acc) {
-  int hi = static_cast<int>(v[0]), lo = hi;
-#pragma unroll
-  for (int x = 1; x < 16; ++x) {
-    hi = max(hi, static_cast<int>(v[x]));
-    lo = min(lo, static_cast<int>(v[x]));
-  }
-  if (__any_sync(0xFFFFFFFFu, hi >= (1 << 22) || lo < -(1 << 22))) {
-#pragma unroll
-    for (int x = 0; x < 16; ++x) acc[x] = __fmaf_rn(__int2float_rn(static_cast<int>(v[x])), sc, acc[x]);
-  } else {
-#pragma unroll
-    for (int x = 0; x < 16; ++x)
-      acc[x] = __fmaf_rn(__fsub_rn(__uint_as_float(v[x] + 0x4B400000u), 12582912.0f), sc, acc[x]);
-  }
-}
-
 template <int ND, typename OutT>
 __global__ void __launch_bounds__(kGwThreads, 1)
     k_grad_weight(const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_x,
-                  const float* __restrict__ scale, int M, int N, int K, void* __restrict__ dw, int vec) {
+                  const float* __restrict__ scale, int M, int N, int K, void* __restrict__ dw) {
   constexpr int S = kGwStages, SB = kGwSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sA = base;
   uint8_t* sB = sA + S * kGwABytes;
   float* patches = reinterpret_cast<float*>(sB + SB * kGwBBytes);
-  uint64_t* full_a = reinterpret_cast<uint64_t*>(patches + 8 * kGwPatch);
+  uint64_t* full_a = reinterpret_cast<uint64_t*>(patches + kGwAddWarps * kGwPatch);
   uint64_t* empty_a = full_a + S;
   uint64_t* full_b = empty_a + S;
   uint64_t* empty_b = full_b + SB;
   uint64_t* acc_full = empty_b + SB;   // [2] a pass is in TMEM
-  uint64_t* acc_empty = acc_full + 2;  // [2] it has been read (8 warps)
+  uint64_t* acc_empty = acc_full + 2;  // [2] CTA 0: it has been read (8 warps of each CTA)
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ktiles = (K + kGwBN - 1) / kGwBN;
-  const int64_t tiles = static_cast<int64_t>(ktiles) * ((N + 127) / 128);
+  const int64_t tiles = static_cast<int64_t>(ktiles) * ((N + kGwRows - 1) / kGwRows);
+  const int rank = static_cast<int>(cluster_ctarank());  // in the pair
+  const int64_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
   const int chunks = (M + kGwChunk - 1) / kGwChunk;
   const int steps = (M + kGwBM - 1) / kGwBM;  // of 128 tokens
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(full_a + s, 1);
+      mbar_init(full_a + s, 1);  // CTA 0's: the tiles of both are in
       mbar_init(empty_a + s, 1);
     }
     for (int s = 0; s < SB; ++s) {
@@ -310,20 +309,21 @@ __global__ void __launch_bounds__(kGwThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full + b, 1);
-      mbar_init(acc_empty + b, 8);
+      mbar_init(acc_empty + b, 2 * kGwAddWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
+    tmem2_alloc(tmem_slot, 512);
+    tmem2_relinquish();
   }
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers are there
   tc_fence_after();
   const uint32_t tmem_d = *tmem_slot;
   Ring mine;  // warp 0: the lane's next slot
@@ -331,39 +331,42 @@ __global__ void __launch_bounds__(kGwThreads, 1)
   if (warp == 0) {
     if (lane == 0) {  // digit tiles
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const int n0 = static_cast<int>(t / ktiles) * 128;
+      for (int64_t t = first; ok && t < tiles; t += stride) {
+        const int n0 = static_cast<int>(t / ktiles) * kGwRows + 128 * rank;
         for (int c = 0; ok && c < chunks; ++c)
           for (int j = ND - 1; ok && j >= 0; --j)
-            for (int st = c * SB; st < steps && st < (c + 1) * SB; ++st, mine.next(S)) {
+            for (int st = c * kGwPer; st < steps && st < (c + 1) * kGwPer; ++st, mine.next(S)) {
               ok = mbar_wait(empty_a + mine.s, mine.ph ^ 1u, abort_flag);
               if (!ok) break;
-              mbar_arrive_expect_tx(full_a + mine.s, kGwABytes);
-              tma_load_3d(sA + mine.s * kGwABytes, &tm_d, full_a + mine.s, st * kGwBM, n0, j);
+              if (rank == 0) mbar_arrive_expect_tx(full_a + mine.s, 2 * kGwABytes);
+              tma2_load_3d(sA + mine.s * kGwABytes, &tm_d, full_a + mine.s, st * kGwBM, n0, j);
             }
       }
+      // the other CTA's commits have arrived here before this one may exit
+      for (int i = 0; ok && i < S; ++i, mine.next(S)) ok = mbar_wait(empty_a + mine.s, mine.ph ^ 1u, abort_flag);
     } else if (lane == 1) {  // code blocks
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const int k0 = static_cast<int>(t % ktiles) * kGwBN;
+      for (int64_t t = first; ok && t < tiles; t += stride) {
+        const int k0 = static_cast<int>(t % ktiles) * kGwBN + kGwBN / 2 * rank;
         for (int st = 0; st < steps; ++st, mine.next(SB)) {
           ok = mbar_wait(empty_b + mine.s, mine.ph ^ 1u, abort_flag);
           if (!ok) break;
-          mbar_arrive_expect_tx(full_b + mine.s, kGwBBytes);
-          tma_load_2d(sB + mine.s * kGwBBytes, &tm_x, full_b + mine.s, st * kGwBM, k0);
+          if (rank == 0) mbar_arrive_expect_tx(full_b + mine.s, 2 * kGwBBytes);
+          tma2_load_2d(sB + mine.s * kGwBBytes, &tm_x, full_b + mine.s, st * kGwBM, k0);
         }
       }
+      for (int i = 0; ok && i < SB; ++i, mine.next(SB)) ok = mbar_wait(empty_b + mine.s, mine.ph ^ 1u, abort_flag);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = make_idesc_i8(128, kGwBN);
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = make_idesc_i8(kGwRows, kGwBN);
       const uint64_t a_desc0 = make_sw128_kmajor_desc(smem_u32(sA));
       const uint64_t b_desc0 = make_sw128_kmajor_desc(smem_u32(sB));
       Ring ra, rb, acc;  // rb: the chunk's first block
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x)
+      for (int64_t t = first; ok && t < tiles; t += stride)
         for (int c = 0; ok && c < chunks; ++c) {
-          const int nst = min(SB, steps - c * SB);
+          const int nst = min(kGwPer, steps - c * kGwPer);
           Ring b = rb;
           for (int j = ND - 1; ok && j >= 0; --j, acc.next(2)) {
             ok = mbar_wait(acc_empty + acc.s, acc.ph ^ 1u, abort_flag);
@@ -378,16 +381,16 @@ __global__ void __launch_bounds__(kGwThreads, 1)
               const uint64_t bd = b_desc0 + static_cast<uint64_t>(b.s * (kGwBBytes >> 4));
 #pragma unroll
               for (int kk = 0; kk < kGwBM / 32; ++kk)
-                tc_mma_i8_ss(tmem_d + 256 * acc.s, ad + 2 * kk, bd + 2 * kk, idesc, st != 0 || kk != 0 ? 1u : 0u);
-              tc_commit(empty_a + ra.s);
-              if (j == 0) tc_commit(empty_b + b.s);
+                tc2_mma_i8_ss(tmem_d + 256 * acc.s, ad + 2 * kk, bd + 2 * kk, idesc, st != 0 || kk != 0 ? 1u : 0u);
+              tc2_commit_both(empty_a + ra.s);
+              if (j == 0) tc2_commit_both(empty_b + b.s);
             }
-            if (ok) tc_commit(acc_full + acc.s);
+            if (ok) tc2_commit_both(acc_full + acc.s);
           }
           rb = b;
         }
       if (!ok) {  // let the MMAs in flight finish before TMEM is freed
-        tc_commit(drain);
+        tc2_commit(drain);
         mbar_drain(drain, 0);
       }
     }
@@ -395,17 +398,20 @@ __global__ void __launch_bounds__(kGwThreads, 1)
     // ---------------- accumulate and store: lane = output n, 128 columns
     const int qd = warp & 3, part = (warp - 2) >> 2;
     const uint32_t trow = tmem_d + 128 * part + (static_cast<uint32_t>(qd * 32) << 16);
+    float* patch = patches + (warp - 2) * kGwPatch;
+    const int64_t nlast = N - 1;
     Ring pass;
     bool ok = true;
-    for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const int k0 = static_cast<int>(t % ktiles) * kGwBN + 128 * part;
-      const int64_t n = t / ktiles * 128 + 32 * qd + lane;
+#pragma unroll 1
+    for (int t = static_cast<int>(first); ok && t < tiles; t += static_cast<int>(stride)) {
+      const int nw = t / ktiles * kGwRows + 128 * rank + 32 * qd;
+      const float* sp = scale + min(static_cast<int64_t>(nw + lane), nlast);  // rows past N repeat the last, unused
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-      for (int c = 0; ok && c < chunks; ++c) {
-        float sc = n < N ? __ldg(scale + static_cast<int64_t>(c) * N + n) : 0.0f;
-        sc = __fmul_rn(sc, ND == 3 ? 65536.0f : 256.0f);
+#pragma unroll 1
+      for (int c = 0; ok && c < chunks; ++c, sp += N) {
+        float sc = __fmul_rn(__ldg(sp), ND == 3 ? 65536.0f : 256.0f);
 #pragma unroll 1
         for (int j = 0; j < ND; ++j, pass.next(2)) {
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full + pass.s, pass.ph, abort_flag));
@@ -416,39 +422,33 @@ __global__ void __launch_bounds__(kGwThreads, 1)
             uint32_t v[16];
             tmem_ld_32x32b_x16(trow + 256 * pass.s + i, v);
             tmem_ld_wait();
-            add_pass(v, sc, acc + i);
+#pragma unroll
+            for (int x = 0; x < 16; ++x)  // at most 2^24: exact in fp32
+              acc[i + x] = __fmaf_rn(__int2float_rn(static_cast<int32_t>(v[x])), sc, acc[i + x]);
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(acc_empty + pass.s);
+          if (lane == 0) mbar_arrive_remote(acc_empty + pass.s, 0);
           sc = __fmul_rn(sc, 0.00390625f);
         }
       }
-      if (ok && vec) {
-        if (n < N)
-#pragma unroll
-          for (int i = 0; i < 128; i += 16) {
-            float f[16];
-#pragma unroll
-            for (int x = 0; x < 16; ++x) f[x] = acc[i + x];
-            store16<OutT>(dw, n * K, k0 + i, K, f, true);
-          }
-      } else if (ok) {
-        // rows that start anywhere: 16 columns of two rows a store (one value
-        // a lane and 32 rows would take 32 sectors each: 43 us for 129 x 901 x 1501)
-        float* patch = patches + (warp - 2) * kGwPatch;
-        const int64_t nw = t / ktiles * 128 + 32 * qd;
-        const int rows = static_cast<int>(min(static_cast<int64_t>(32), N - nw)), col = lane & 15;
+      if (ok) {
+        // turned 16 columns at a time, so that a store takes 16 columns of
+        // two rows and not one of 32 (which is 32 sectors)
+        const int k0 = t % ktiles * kGwBN + 128 * part, col = lane & 15;
+        const int rows = min(32, N - nw);  // may be < 1
 #pragma unroll
         for (int i = 0; i < 128; i += 16) {
           __syncwarp();
 #pragma unroll
           for (int x = 0; x < 16; ++x) patch[lane * 17 + x] = acc[i + x];
           __syncwarp();
-          if (k0 + i + col < K)
+          if (k0 + i + col < K) {
+            int64_t at = static_cast<int64_t>(nw + (lane >> 4)) * K + k0 + i + col;
 #pragma unroll 4
-            for (int r = lane >> 4; r < rows; r += 2)
-              store_out<OutT>(dw, (nw + r) * K + k0 + i + col, patch[r * 17 + col]);
+            for (int r = lane >> 4; r < rows; r += 2, at += 2 * static_cast<int64_t>(K))
+              store_out<OutT>(dw, at, patch[r * 17 + col]);
+          }
         }
       }
     }
@@ -456,18 +456,19 @@ __global__ void __launch_bounds__(kGwThreads, 1)
 
   __syncwarp();
   __syncthreads();
-  if (warp == 0 && lane < 2 && *abort_flag) {
+  if (rank == 0 && warp == 0 && lane < 2 && *abort_flag) {
     // loads that can still be in flight: the last one into each slot (a slot
     // that never had one passes at once)
     uint64_t* bars = lane == 0 ? full_a : full_b;
     const int ring = lane == 0 ? S : SB;
     for (int i = 0; i < ring; ++i) mbar_drain(bars + i, i < mine.s ? mine.ph : mine.ph ^ 1u);
   }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync_all();  // the pair's MMAs, reads of TMEM and arrivals are done
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_d, 512);
+    tmem2_dealloc(tmem_d, 512);
   }
 }
 

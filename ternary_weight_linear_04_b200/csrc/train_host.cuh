@@ -186,16 +186,42 @@ bl_status run_grad_input(const void* dyp, bl_dtype dydt, const uint8_t* packed, 
   return dxdt == BL_F32 ? launch_gi<1, float>(tdy, tw, a, s) : launch_gi<1, __nv_bfloat16>(tdy, tw, a, s);
 }
 
+// Launch of `blocks` (an even number) CTAs in clusters of two along x, with
+// programmatic dependent launch allowed.
+template <typename... KArgs, typename... Args>
+bl_status launch_pdl_pairs(void (*kern)(KArgs...), unsigned blocks, int threads, size_t smem, cudaStream_t st,
+                           Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return BL_ERR_CUDA;
+  }
+  return launch_status();
+}
+
 template <int ND, typename OutT>
 bl_status launch_gw(const CUtensorMap& td, const CUtensorMap& tx, const float* scale, int M, int N, int K, void* dw,
-                    int vec, int sms, cudaStream_t s) {
+                    int sms, cudaStream_t s) {
   static int done[kMaxDevices] = {0};
   auto kern = bl::k_grad_weight<ND, OutT>;
   if (!ensure_smem(kern, bl::kGwSmem, done)) return BL_ERR_CUDA;
-  const int64_t tiles = ((int64_t{K} + bl::kGwBN - 1) / bl::kGwBN) * ((int64_t{N} + 127) / 128);
-  const int64_t grid = tiles < sms ? tiles : sms;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(bl::kGwThreads), bl::kGwSmem, s, td, tx, scale, M, N,
-                    K, dw, vec);
+  const int64_t tiles = ((int64_t{K} + bl::kGwBN - 1) / bl::kGwBN) * ((int64_t{N} + bl::kGwRows - 1) / bl::kGwRows);
+  if (tiles > INT32_MAX / 2) return BL_ERR_UNSUPPORTED;
+  const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+  return launch_pdl_pairs(kern, static_cast<unsigned>(2 * pairs), bl::kGwThreads, bl::kGwSmem, s, td, tx, scale, M, N, K, dw);
 }
 
 // Workspace of grad_weight: the digit planes, their exponents, the codes.
@@ -219,13 +245,12 @@ bl_status launch_gw_operands(const void* dy, const int8_t* xq, const float* eta,
                              const GwScratch& g, cudaStream_t s) {
   static int done[kMaxDevices] = {0};
   auto kern = bl::k_gw_operands<DyT, ND>;
-  constexpr size_t smem = ND * bl::kGdCols * bl::kGwChunk;
+  constexpr size_t smem = ND * bl::kGdCols * bl::kGdTokens;
   if (!ensure_smem(kern, smem, done)) return BL_ERR_CUDA;
-  const int64_t digits = ((N + bl::kGdCols - 1) / bl::kGdCols) * ((M + bl::kGwChunk - 1) / bl::kGwChunk);
-  const int64_t blocks = digits + ((K + 63) / 64) * ((M + 127) / 128);
+  const int64_t digits = 2 * ((N + bl::kGdCols - 1) / bl::kGdCols) * ((M + bl::kGwChunk - 1) / bl::kGwChunk);
+  const int64_t blocks = round_up(digits + ((K + 63) / 64) * ((M + 127) / 128), 2);
   if (blocks > INT32_MAX) return BL_ERR_UNSUPPORTED;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(bl::kGdThreads), smem, s,
-                    static_cast<unsigned>(digits), xq, K, g.codes, static_cast<const DyT*>(dy), eta, M, N, g.Mp,
+  return launch_pdl_pairs(kern, static_cast<unsigned>(blocks), bl::kGdThreads, smem, s, static_cast<unsigned>(digits), xq, K, g.codes, static_cast<const DyT*>(dy), eta, M, N, g.Mp,
                     N % 2 == 0 ? 1 : 0, g.digits, g.scale);
 }
 
@@ -511,13 +536,12 @@ bl_status bitlinear_grad_weight(const void* dy, bl_dtype dydt, const int8_t* xq,
   CUtensorMap td, tx;
   if (!make_tmap(&td, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.digits, g.Mp, N, nd, g.Mp, bl::kGwBM, 128,
                  CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.codes, g.Mp, K, 0, g.Mp, bl::kGwBM, bl::kGwBN,
+      !make_tmap(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.codes, g.Mp, K, 0, g.Mp, bl::kGwBM, bl::kGwBN / 2,
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return BL_ERR_CUDA;
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
-  const int vec = vec_rows(K, dwdt);
-  return nd == 3 ? launch_gw<3, float>(td, tx, g.scale, m, n, k, dw, vec, sms, s)
-                 : launch_gw<2, __nv_bfloat16>(td, tx, g.scale, m, n, k, dw, vec, sms, s);
+  return nd == 3 ? launch_gw<3, float>(td, tx, g.scale, m, n, k, dw, sms, s)
+                 : launch_gw<2, __nv_bfloat16>(td, tx, g.scale, m, n, k, dw, sms, s);
 }
 
 bl_status bitlinear_rmsnorm_grad(const void* dn, bl_dtype dndt, const int8_t* xq, const float* eta,

@@ -571,6 +571,9 @@ bl_status bitlinear_device_error(int32_t* code, void* stream);
  *   dy      in   M x N, fp32 or bf16.
  *   packed, gamma   in   as written by bitlinear_pack_weights for N x K.
  *   dx      out  M x K, fp32 or bf16.
+ * bf16 products (an fp32 dy as three parts that hold all of it) summed in
+ * fp32.  K of a multiple of 64 and N of 8 are read in place; other sizes are
+ * copied once into the workspace.
  */
 size_t bitlinear_grad_input_workspace_bytes(int64_t M, int64_t N, int64_t K, bl_dtype dydt);
 bl_status bitlinear_grad_input(const void* dy, bl_dtype dydt, int64_t M, int64_t N, const uint8_t* packed,
@@ -584,6 +587,13 @@ bl_status bitlinear_grad_input(const void* dy, bl_dtype dydt, int64_t M, int64_t
  *   xq, eta   in   as written by bitlinear_quant_act or
  *                  bitlinear_rmsnorm_quant_act (M x K, M).
  *   dw        out  N x K, fp32 or bf16.
+ * The sum is one of integers: over each 1024 tokens the values dy eta / 127 of
+ * an output n are rounded to 23 bits (fp32 dW) or 15 bits (bf16 dW) below the
+ * largest of them, the products with x~ are then exact.  An error is thus
+ * relative to that largest value: fp32 results of like-sized gradients come
+ * out 2e-7 off in the 2-norm, and a token's gradients below 2^-23 (2^-15) of
+ * the column's largest round to zero.  An infinity or a NaN in column n of dy
+ * makes row n of dW NaN.
  */
 size_t bitlinear_grad_weight_workspace_bytes(int64_t M, int64_t N, int64_t K, bl_dtype dydt, bl_dtype dwdt);
 bl_status bitlinear_grad_weight(const void* dy, bl_dtype dydt, const int8_t* xq, const float* eta, int64_t M,
@@ -662,6 +672,9 @@ bl_status bitlinear_linear_adapters(const void* x, bl_dtype xdt, int64_t M, int6
  *   dx   = dy W^ + v A_a                      M x K
  *   dA_a = sum over the tokens of a: v^T x^   L x r x K
  *   dB_a = sum over the tokens of a: dy^T u   L x N x r
+ * v and u enter their products as two bf16 parts (16 bits of them; three,
+ * all of them, where the result is fp32).  What an adapter's factors hold,
+ * infinities and NaN too, reaches its own tokens and its own gradients only.
  * An adapter that no token uses gets zeros.  dx may be NULL (not computed;
  * packed and gamma may then be NULL too), and so may dA and dB together.
  *   dabdt   in   type of dA and dB, fp32 or bf16.

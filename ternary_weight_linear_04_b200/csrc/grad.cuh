@@ -117,7 +117,11 @@ __global__ void __launch_bounds__(256)
 // H = 2 shares one expanded tile between two MMAs of 128 tokens and fills
 // TMEM, for token counts that fill the GPU; H = 1 is for the rest, where a
 // cluster splits the steps and adds the tiles through distributed shared
-// memory.
+// memory.  2048 x 11008 x 4096 (H = 2): 124 us on warm inputs, 143 on
+// rotating ones, 1.5 and 1.3 PFLOP/s of the 1.64 that a library product
+// reaches.  It reads 12 KB of shared memory for an MMA of 128 cycles and
+// writes 8 KB beside it, which is all that an SM can.  77 x 3200 x 8640
+// (H = 1): 17 us, about 8 of them before and after the steps.
 //
 // Adapters: behind the steps over n come steps of 64 entries, an entry being
 // one (adapter of the tile's tokens, part of v, rank index): v (each token's

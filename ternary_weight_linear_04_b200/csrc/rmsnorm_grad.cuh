@@ -11,7 +11,9 @@
 // kRgHeld of them) in registers between the sum and the result, so rows of up
 // to 16384 values are read once and longer ones twice (the second time from
 // L2).  Rows that do not start on 16 bytes are read value by value in the
-// same order, so a row's result does not depend on where it lies.
+// same order, so a row's result does not depend on where it lies.  2048 x 8640
+// bf16: 20.4 us on rotating inputs, 4.3 TB/s of the 6.5 a copy reaches (the
+// sum and the result of a row do not overlap; the CTAs beside it fill in).
 #pragma once
 
 #include "common.cuh"

@@ -673,8 +673,8 @@ bl_status bitlinear_adapters_grad(const void* dy, bl_dtype dydt, const int8_t* x
   if ((dA == nullptr) != (dB == nullptr) || (dx && (!packed || !gamma))) return BL_ERR_INVALID_ARG;
   if (st != BL_OK || sa != BL_OK) return BL_ERR_UNSUPPORTED;
   const size_t need = bitlinear_adapters_grad_workspace_bytes(M, N, K, L, r, dydt);
-  if (M > 0 && (!dy || !xq || !eta || !ids || !workspace)) return BL_ERR_INVALID_ARG;
-  if (workspace_bytes < need) return BL_ERR_INVALID_ARG;
+  if (M > 0 && (!dy || !xq || !eta || !ids)) return BL_ERR_INVALID_ARG;
+  if ((need && !workspace) || workspace_bytes < need) return BL_ERR_INVALID_ARG;
   if (!adapters_aligned(packed, gamma, A, B, scale, ids) || !aligned(dy, 16) || !aligned(xq, 16) ||
       !aligned(dx, 16) || !aligned(dA, 16) || !aligned(dB, 16) || !aligned(eta, 4) || !aligned(workspace, 256))
     return BL_ERR_ALIGNMENT;

@@ -170,3 +170,37 @@ def test_tensors_of_two_devices_are_refused(monkeypatch):
         device = torch.device("cuda", 0)
     with pytest.raises(ValueError, match="stream"):
         bl._place(Stream(), FakeTensor(1))
+
+
+LA = dict(p_x=F, xdt=1, M=4, K=64, p_packed=F, p_gamma=F, N=64, p_A=F, p_B=F, p_scale=F, p_ids=F, L=2, r=8, p_y=F,
+          ydt=1, p_ws=F, nws=BIG, flags=0, p_s=None)
+
+
+@pytest.mark.parametrize("status,changes", [
+    (BAD, [dict(p_x=None), dict(p_packed=None), dict(p_gamma=None), dict(p_A=None), dict(p_B=None), dict(p_scale=None),
+           dict(p_ids=None), dict(p_y=None), dict(p_ws=None), dict(xdt=2), dict(ydt=5), dict(L=0), dict(r=0), dict(M=-1),
+           dict(N=0), dict(K=0), dict(nws=0)]),
+    (UNS, [dict(L=65536), dict(r=129), dict(M=1 << 30), dict(K=1 << 25), dict(xdt=0, flags=2),
+           dict(K=((1 << 31) - 1) // 127)]),
+    (ALN, [dict(p_x=F + 1), dict(p_packed=F + 8), dict(p_A=F + 2), dict(p_B=F + 8), dict(p_y=F + 2), dict(p_ids=F + 2),
+           dict(p_scale=F + 2), dict(p_gamma=F + 2), dict(p_ws=F + 8)])])
+def test_linear_adapters_refused_before_a_launch(L, status, changes):
+    for change in changes:
+        assert call(L.bitlinear_linear_adapters, LA, **change) == status, change
+
+
+def test_linear_adapters_of_no_tokens_and_its_workspace(L):
+    assert call(L.bitlinear_linear_adapters, LA, M=0, p_x=None, p_ids=None, p_y=None, p_ws=None, nws=0) == OK
+    for K in (64, 61):
+        fwd = L.bitlinear_forward_adapters_workspace_bytes(40, K, 63, 2, 8)
+        need = L.bitlinear_linear_adapters_workspace_bytes(40, K, 63, 2, 8)
+        assert need >= fwd + 40 * K + 2 * 4 * 40
+        assert call(L.bitlinear_linear_adapters, LA, M=40, K=K, N=63, nws=need - 1) == BAD
+    assert L.bitlinear_linear_adapters_workspace_bytes(4, 64, 64, 2, 129) == 0
+
+
+def test_adapter_gradients_of_no_tokens_still_need_the_workspace(L):
+    need = L.bitlinear_adapters_grad_workspace_bytes(0, 64, 64, 2, 8, 1)
+    assert need > 0
+    assert call(L.bitlinear_adapters_grad, AG, M=0, p_ws=None) == BAD
+    assert call(L.bitlinear_adapters_grad, AG, M=0, nws=need - 1) == BAD

@@ -192,7 +192,7 @@ constexpr int kSortThreads = 1024;
 
 __global__ void __launch_bounds__(kSortThreads)
     k_adapter_sort(const int32_t* __restrict__ ids, int64_t M, int L, int32_t* first, int32_t* rows,
-                   int32_t* __restrict__ start) {
+                   int32_t* __restrict__ start, const PadJob pad0, const PadJob pad1) {
   __shared__ int s_count[32][257];  // a warp's tokens with a digit, then where the next of them goes
   __shared__ int s_sum[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -200,6 +200,10 @@ __global__ void __launch_bounds__(kSortThreads)
   const int passes = L > 255 ? 2 : 1;
   pdl_wait();
   if (tid == 0) pdl_trigger();
+  if (blockIdx.x > 0) {
+    pad_rows(pad0, pad1, (blockIdx.x - 1) * int64_t{kSortThreads} + tid, (gridDim.x - 1) * int64_t{kSortThreads});
+    return;
+  }
   auto key_of = [&](int64_t m) {
     const int a = adapter_of(ids, m, L);
     return a < 0 ? L : a;

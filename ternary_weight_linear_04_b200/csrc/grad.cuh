@@ -41,11 +41,10 @@ struct PadJob {
   uint8_t* dst;
 };
 
-__global__ void __launch_bounds__(256) k_pad_rows(const PadJob first, const PadJob second) {
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_trigger();
+// Item `at` and every `step`-th after it (16 bytes each).
+__device__ __forceinline__ void pad_rows(const PadJob& first, const PadJob& second, int64_t at, int64_t step) {
   const int64_t n1 = first.rows * (first.stride / 16), n2 = second.rows * (second.stride / 16);
-  for (int64_t it = blockIdx.x * 256ll + threadIdx.x; it < n1 + n2; it += gridDim.x * 256ll) {
+  for (int64_t it = at; it < n1 + n2; it += step) {
     const PadJob& job = it < n1 ? first : second;
     const int64_t i = it < n1 ? it : it - n1;
     const uint8_t* src = job.src;
@@ -77,6 +76,12 @@ __global__ void __launch_bounds__(256) k_pad_rows(const PadJob first, const PadJ
     }
     *reinterpret_cast<uint4*>(job.dst + row * job.stride + c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+
+__global__ void __launch_bounds__(256) k_pad_rows(const PadJob first, const PadJob second) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
+  pad_rows(first, second, blockIdx.x * 256ll + threadIdx.x, gridDim.x * 256ll);
 }
 
 // fp32 rows as three bf16 planes (rows x cols_pad each, zero past cols) whose

@@ -87,10 +87,13 @@ inline void pad_rows(const void* src, int64_t rows, int64_t bytes, int64_t multi
   pads->job[pads->n++] = {static_cast<const uint8_t*>(src), rows, bytes, out->stride, static_cast<uint8_t*>(dst)};
 }
 
+inline int64_t pad_items(const Pads& pads) {
+  return pads.job[0].rows * (pads.job[0].stride / 16) + pads.job[1].rows * (pads.job[1].stride / 16);
+}
+
 inline bl_status run_pads(const Pads& pads, int sms, cudaStream_t s) {
   if (!pads.n) return BL_OK;
-  const int64_t n = pads.job[0].rows * (pads.job[0].stride / 16) + pads.job[1].rows * (pads.job[1].stride / 16);
-  return launch_pdl(bl::k_pad_rows, dim3(grid_for(n, 256, sms)), dim3(256), 0, s, pads.job[0], pads.job[1]);
+  return launch_pdl(bl::k_pad_rows, dim3(grid_for(pad_items(pads), 256, sms)), dim3(256), 0, s, pads.job[0], pads.job[1]);
 }
 
 // dy as bf16 planes: one, or three of an fp32 dy.
@@ -161,15 +164,22 @@ bl_status launch_gi(const CUtensorMap& tdy, const CUtensorMap& tw, const bl::GiA
   return launch_pdl_cluster(kern, grid, dim3(bl::kGiThreads), smem, s, grid.z, tdy, tw, a);
 }
 
-// dx = gamma dy W~ (+ v A where a.v is given); the operands' copies come out of ws.
-bl_status run_grad_input(const void* dyp, bl_dtype dydt, const uint8_t* packed, bl_dtype dxdt, bl::GiArgs a,
-                         Scratch* ws, int sms, cudaStream_t s) {
+// The operands of dx as TMA reads them; `pads`: the copies to be made first.
+struct GiOperands {
   Rows dy, w;
   Pads pads;
-  bl_status st = dy_rows(dyp, dydt, a.M, a.N, ws, &dy, &pads, sms, s);
-  if (st != BL_OK) return st;
-  pad_rows(packed, a.N, (a.K + 3) / 4, 16, ws, &w, &pads);
-  if ((st = run_pads(pads, sms, s)) != BL_OK) return st;
+};
+
+bl_status gi_operands(const void* dy, bl_dtype dydt, const uint8_t* packed, int64_t M, int64_t N, int64_t K, Scratch* ws,
+                      GiOperands* o, int sms, cudaStream_t s) {
+  const bl_status st = dy_rows(dy, dydt, M, N, ws, &o->dy, &o->pads, sms, s);
+  pad_rows(packed, N, (K + 3) / 4, 16, ws, &o->w, &o->pads);
+  return st;
+}
+
+// dx = gamma dy W~ (+ v A where a.v is given), the copies made.
+bl_status run_grad_input(const GiOperands& o, bl_dtype dxdt, bl::GiArgs a, int sms, cudaStream_t s) {
+  const Rows &dy = o.dy, &w = o.w;
   // 256 tokens a tile where such tiles fill most of the GPU, else 128
   const int64_t ktiles = (a.K + bl::kGiBN - 1) / bl::kGiBN;
   const int H = a.M > 128 && ktiles * ((a.M + 255) / 256) * 4 > int64_t{3} * sms ? 2 : 1;
@@ -304,8 +314,12 @@ inline Order order_scratch(int64_t M, int64_t L, Scratch* ws) {
   return o;
 }
 
-bl_status launch_sort(const AdapterSet& ad, int64_t M, const Order& o, cudaStream_t s) {
-  return launch_pdl(bl::k_adapter_sort, dim3(1), dim3(bl::kSortThreads), 0, s, ad.ids, M, ad.L, o.first, o.rows, o.start);
+// With the copies of `pads` in the same launch.
+bl_status launch_sort(const AdapterSet& ad, int64_t M, const Order& o, const Pads& pads, int sms, cudaStream_t s) {
+  const int64_t n = pad_items(pads);
+  const unsigned grid = 1 + (n ? grid_for(n, bl::kSortThreads, sms) : 0);
+  return launch_pdl(bl::k_adapter_sort, dim3(grid), dim3(bl::kSortThreads), 0, s, ad.ids, M, ad.L, o.first, o.rows,
+                    o.start, pads.job[0], pads.job[1]);
 }
 
 template <typename DyT, int NT>
@@ -403,14 +417,15 @@ inline void fa_scratch(const int8_t* xq, const uint8_t* packed, int64_t M, int64
   f->pads.n = 2;
 }
 
-// u of the forward pass.
+// u of the forward pass, and the operands' copies.
 bl_status run_u(const FaScratch& f, int8_t* xq, float* eta, int64_t M, int64_t K, int64_t N, const AdapterSet& ad, int sms,
                 cudaStream_t s) {
-  if (few_tokens_u(M, K)) return launch_u_few(nullptr, xq, eta, nullptr, M, K, ad, f.u, sms, s);
-  if (f.order.rows) {
-    const bl_status st = launch_sort(ad, M, f.order, s);
-    if (st != BL_OK) return st;
+  if (few_tokens_u(M, K)) {
+    const bl_status st = launch_u_few(nullptr, xq, eta, nullptr, M, K, ad, f.u, sms, s);
+    return st == BL_OK ? run_pads(f.pads, sms, s) : st;
   }
+  const bl_status st = f.order.rows ? launch_sort(ad, M, f.order, f.pads, sms, s) : run_pads(f.pads, sms, s);
+  if (st != BL_OK) return st;
   return launch_uv(nullptr, BL_BF16, xq, eta, M, K, N, ad, f.order.rows, f.u, nullptr, s);
 }
 
@@ -418,8 +433,6 @@ bl_status run_u(const FaScratch& f, int8_t* xq, float* eta, int64_t M, int64_t K
 bl_status run_forward_adapters(const FaScratch& f, const float* eta, const int32_t* xsum, int64_t M, const float* gamma,
                                int64_t N, const AdapterSet& ad, void* y, bl_dtype ydt, unsigned flags, int sms,
                                cudaStream_t s) {
-  const bl_status st = run_pads(f.pads, sms, s);
-  if (st != BL_OK) return st;
   if (f.pads.n) flags &= ~static_cast<unsigned>(BL_FLAG_WEIGHTS_STATIC);  // the copy is new
   const bl::AdapterAdd add = {f.u, ad.B, ad.ids, ad.L, ad.r};
   return forward_impl(static_cast<const int8_t*>(f.x.p), eta, xsum, M, f.x.stride, static_cast<const uint8_t*>(f.w.p),
@@ -468,10 +481,8 @@ extern "C" {
 size_t bitlinear_grad_input_workspace_bytes(int64_t M, int64_t N, int64_t K, bl_dtype dydt) {
   if (train_sizes(M, N, K) != BL_OK || !dtype_ok(dydt)) return 0;
   Scratch ws(nullptr);
-  Rows r;
-  Pads pads;
-  dy_rows(nullptr, dydt, M, N, &ws, &r, &pads, 1, nullptr);
-  pad_rows(nullptr, N, (K + 3) / 4, 16, &ws, &r, &pads);
+  GiOperands o;
+  gi_operands(nullptr, dydt, nullptr, M, N, K, &ws, &o, 1, nullptr);
   return ws.used;
 }
 
@@ -493,7 +504,10 @@ bl_status bitlinear_grad_input(const void* dy, bl_dtype dydt, int64_t M, int64_t
   Scratch ws(workspace);
   bl::GiArgs a = {};
   a.gamma = gamma; a.M = static_cast<int>(M); a.N = static_cast<int>(N); a.K = static_cast<int>(K); a.dx = dx;
-  return run_grad_input(dy, dydt, packed, dxdt, a, &ws, sms, s);
+  GiOperands o;
+  if ((st = gi_operands(dy, dydt, packed, M, N, K, &ws, &o, sms, s)) != BL_OK) return st;
+  if ((st = run_pads(o.pads, sms, s)) != BL_OK) return st;
+  return run_grad_input(o, dxdt, a, sms, s);
 }
 
 size_t bitlinear_grad_weight_workspace_bytes(int64_t M, int64_t N, int64_t K, bl_dtype dydt, bl_dtype dwdt) {
@@ -643,6 +657,7 @@ bl_status bitlinear_linear_adapters(const void* x, bl_dtype xdt, int64_t M, int6
       a.ad = {f.u, ad.B, ids, ad.L, ad.r};
       return launch_decode_reg(a, rg, s);
     }
+    if ((st = run_pads(f.pads, sms, s)) != BL_OK) return st;
   } else {
     st = norm ? rmsnorm_quant_impl(x, xdt, M, K, q.xq, q.eta, q.xsum, nullptr, stream)
               : bitlinear_quant_act(x, xdt, M, K, q.xq, q.eta, q.xsum, stream);
@@ -687,8 +702,10 @@ bl_status bitlinear_adapters_grad(const void* dy, bl_dtype dydt, const int8_t* x
   float* v = static_cast<float*>(ws.take(rank_bytes));
   const Order order = order_scratch(M, L, &ws);
   const AdapterSet ad = adapter_set(A, B, scale, ids, L, r);
-  const bool sorted = dA != nullptr || (M > 16 && L > 1);
-  if (sorted && (st = launch_sort(ad, M, order, s)) != BL_OK) return st;
+  const bool sorted = dA != nullptr || (M > 16 && L > 1), has_dx = dx && M > 0;
+  GiOperands o;
+  if (has_dx && (st = gi_operands(dy, dydt, packed, M, N, K, &ws, &o, sms, s)) != BL_OK) return st;
+  if ((st = sorted ? launch_sort(ad, M, order, o.pads, sms, s) : run_pads(o.pads, sms, s)) != BL_OK) return st;
   if (M > 0 && (st = launch_uv(dy, dydt, xq, eta, M, K, N, ad, sorted ? order.rows : nullptr, dA ? u : nullptr, v, s)) !=
                    BL_OK)
     return st;
@@ -701,11 +718,11 @@ bl_status bitlinear_adapters_grad(const void* dy, bl_dtype dydt, const int8_t* x
                            : launch_dab<__nv_bfloat16, __nv_bfloat16>(dy, xq, eta, M, K, N, ad, order, u, v, dA, dB, sms, s);
     if (st != BL_OK) return st;
   }
-  if (!dx || M == 0) return BL_OK;
+  if (!has_dx) return BL_OK;
   bl::GiArgs g = {};
   g.gamma = gamma; g.M = static_cast<int>(M); g.N = static_cast<int>(N); g.K = static_cast<int>(K); g.dx = dx;
   g.v = v; g.A = ad.A; g.ids = ids; g.L = ad.L; g.r = ad.r;
-  return run_grad_input(dy, dydt, packed, dxdt, g, &ws, sms, s);
+  return run_grad_input(o, dxdt, g, sms, s);
 }
 
 }  // extern "C"

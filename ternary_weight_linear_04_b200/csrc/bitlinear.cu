@@ -652,12 +652,54 @@ int tc_split(int64_t tiles, int64_t K, int sms) {
   return static_cast<int>(ks);
 }
 
+// How many clusters of cs CTAs of a kernel the device holds at once (clusters
+// stay within a part of the GPU: 16 CTAs' worth of eight do not fit 148 SMs
+// where each takes one).  Asked once per device and size.
+template <typename Kern>
+int cluster_room(Kern kern, int threads, size_t smem, int cs, int (*known)[9]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 1;
+  int& room = known[dev][cs];
+  if (room) return room;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1, 1, static_cast<unsigned>(cs));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = static_cast<unsigned>(cs);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    n = 1;
+  }
+  return room = n;
+}
+
+// K split of the kernel with adapters: 16 K tiles a CTA at least (the
+// cluster's partial tiles cost about as much as 8), and no more clusters than
+// fit.  38 x 3136 x 3648, 29 tiles, without an adapter in use: 14.6 us in two
+// parts, 15.1 in one, 27.7 in five, which do not fit at once.
+template <int BM, typename Kern>
+int tc_split_adapters(Kern kern, size_t smem, int64_t tiles, int64_t K, int (*room)[9]) {
+  const int64_t KT = (K + bl::kTcBK - 1) / bl::kTcBK;
+  const int forced = g_force_split.load(std::memory_order_relaxed);
+  int64_t ks = forced > 0 ? (forced < KT ? forced : KT) : KT / 16;
+  if (ks > bl::TcCfg<BM>::kMaxSplit) ks = bl::TcCfg<BM>::kMaxSplit;
+  while (forced <= 0 && ks > 1 && tiles > cluster_room(kern, bl::tc_threads(true), smem, static_cast<int>(ks), room)) --ks;
+  return static_cast<int>(ks < 1 ? 1 : ks);
+}
+
 template <int BM, typename OutT, bool AD>
 bl_status launch_tc_bm(const int8_t* xq, const float* eta, const int32_t* xsum, int M, int K,
                        const uint8_t* packed, const float* gamma, int N, void* y, int32_t* y_int,
                        int sms, int wstatic, cudaStream_t st, const bl::AdapterAdd& ad) {
   using Cfg = bl::TcCfg<BM>;
-  static int smem_done[kMaxDevices] = {0};
+  static int smem_done[kMaxDevices] = {0}, room[kMaxDevices][9] = {{0}};
   auto kern = bl::k_gemm_tc<BM, OutT, AD>;
   constexpr size_t smem = AD ? Cfg::kSmemAdapters : Cfg::kSmem;
   if (!ensure_smem(kern, smem, smem_done)) return BL_ERR_CUDA;
@@ -669,7 +711,8 @@ bl_status launch_tc_bm(const int8_t* xq, const float* eta, const int32_t* xsum, 
     return BL_ERR_CUDA;
   dim3 grid((N + bl::kTcBN - 1) / bl::kTcBN, (M + BM - 1) / BM);
   if (grid.y > 65535) return BL_ERR_UNSUPPORTED;
-  const int ks = tc_split<BM>(grid.x * grid.y, K, sms);
+  const int64_t tiles = int64_t{grid.x} * grid.y;
+  const int ks = AD ? tc_split_adapters<BM>(kern, smem, tiles, K, room) : tc_split<BM>(tiles, K, sms);
   if (ks <= 1)
     return launch_pdl(kern, grid, dim3(bl::tc_threads(AD)), smem, st, tm_x, tm_w, eta, xsum,
                       gamma, M, K, N, y, y_int, 1, wstatic, ad);
@@ -686,7 +729,7 @@ template <bool AD>
 int tc_tokens(int M, int K, int N, int sms) {
   int bm = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
   if (AD) {
-    const int64_t kt = (K + bl::kTcBK - 1) / bl::kTcBK, splits = kt < 4 ? 1 : (kt < 16 ? kt / 2 : 8);
+    const int64_t kt = (K + bl::kTcBK - 1) / bl::kTcBK, splits = kt < 32 ? 1 : (kt < 128 ? kt / 16 : 8);
     while (bm > 64 && ((N + bl::kTcBN - 1) / bl::kTcBN) * ((int64_t{M} + bm - 1) / bm) * splits * 4 < int64_t{3} * sms) bm /= 2;
   }
   return bm;

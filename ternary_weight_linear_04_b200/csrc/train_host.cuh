@@ -111,34 +111,6 @@ inline bl_status dy_rows(const void* dy, bl_dtype dydt, int64_t M, int64_t N, Sc
                     static_cast<const float*>(dy), M, N, cols, static_cast<__nv_bfloat16*>(dst));
 }
 
-// How many clusters of cs CTAs of a kernel the device holds at once (clusters
-// stay within a part of the GPU: 16 CTAs' worth of eight do not fit 148 SMs
-// where each takes one).  Asked once per device and size.
-template <typename Kern>
-int cluster_room(Kern kern, int threads, size_t smem, int cs, int (*known)[9]) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 1;
-  int& room = known[dev][cs];
-  if (room) return room;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1, 1, static_cast<unsigned>(cs));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = static_cast<unsigned>(cs);
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
-    (void)cudaGetLastError();
-    n = 1;
-  }
-  return room = n;
-}
-
 // Whether rows of `cols` values of type dt take 16-byte stores.
 inline int vec_rows(int64_t cols, bl_dtype dt) { return cols % (16 / dtype_bytes(dt)) == 0 ? 1 : 0; }
 

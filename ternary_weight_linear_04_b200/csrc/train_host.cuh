@@ -350,8 +350,9 @@ bl_status launch_dab(const void* dy, const int8_t* xq, const float* eta, int64_t
   g.b = {dy, N, u, dB, N % (sizeof(DyT) == 4 ? 4 : 8) == 0 ? 1 : 0};
   g.eta = eta; g.rows = o.rows; g.start = o.start; g.r = ad.r; g.slabs_a = static_cast<unsigned>(sa);
   // CTAs of a cluster along the tokens: while there are fewer than four CTAs
-  // an SM, and two chunks of tokens for each
-  int cs = 1;
+  // an SM, and two chunks of tokens for each; two where one adapter may have
+  // more than 16 chunks (2048 tokens: dA and dB 3 us less)
+  int cs = M > 16 * bl::kDabTokens ? 2 : 1;
   while (cs < 8 && (sa + sb) * ad.L * cs < 4 * sms && M >= 4 * bl::kDabTokens * cs) cs *= 2;
   const dim3 grid(static_cast<unsigned>(sa + sb), static_cast<unsigned>(ad.L), static_cast<unsigned>(cs));
   if (ad.r <= 16) return launch_dab_jt<DyT, OutT, 1>(g, grid, s);

@@ -169,10 +169,10 @@ __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
   };
   uint32_t mx[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    mx[0] = max(mx[0], __float_as_uint(g_of(i, 0)) & 0x7FFFFFFFu);  // orders magnitudes, infinities and NaN last
-    mx[1] = max(mx[1], __float_as_uint(g_of(i, 1)) & 0x7FFFFFFFu);
-  }
+  for (int i = 0; i < 32; i += 2)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)  // orders magnitudes, infinities and NaN last
+      mx[c] = __vimax3_u32(mx[c], __float_as_uint(g_of(i, c)) & 0x7FFFFFFFu, __float_as_uint(g_of(i + 1, c)) & 0x7FFFFFFFu);
   *reinterpret_cast<uint2*>(&s_max[warp][2 * lane]) = make_uint2(mx[0], mx[1]);
   __syncthreads();
   if (threadIdx.x < kGdCols) {
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
     e = min(max(e, -113), 120);
     if (__fmul_rn(__uint_as_float(mx[c]), __uint_as_float(static_cast<uint32_t>(e + 127) << 23)) > kTop) --e;
     const bool finite = mx[c] < 0x7F800000u;
-    up[c] = finite ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 0.0f;
+    up[c] = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);  // not finite: the digits do not matter
     if (warp == 0 && n + c < N && (blockIdx.x & 1) == 0)
       scale[chunk * N + n + c] = finite ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : __uint_as_float(0x7FC00000u);
   }
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
     for (int c = 0; c < 2; ++c) {
       uint32_t u[4], o[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) u[b] = up[c] != 0.0f ? biased_round<ND>(__fmul_rn(g_of(i + b, c), up[c])) : 0x808080u;
+      for (int b = 0; b < 4; ++b) u[b] = biased_round<ND>(__fmul_rn(g_of(i + b, c), up[c]));
       transpose4x4_bytes(u[0], u[1], u[2], u[3], o[0], o[1], o[2], o[3]);
 #pragma unroll
       for (int j = 0; j < ND; ++j)

@@ -228,3 +228,25 @@ def test_a_large_gradient_does_not_wipe_out_the_others():
         # of two had to be halved), and fp32 rounds g itself and the sums of the chunk
         off = top[:, None] * 2.0 ** -bits * c.xq.to(F64).abs().sum(0)[None, :] + S * 2 ** -22 + val.abs() * torch.finfo(out).eps
         assert ((got - val).abs() <= off).all()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_gradients_that_are_not_finite_stay_in_their_rows(dt, bad):
+    c = Case(1100, 200, 70, 2, 4, dy_dtype=dt)
+    clean = [bl.grad_weight(c.dy, c.xq, c.eta, out_dtype=o) for o in (F32, BF)]
+    dx = bl.grad_input(c.dy, c.packed, c.gamma, 200)
+    grads = bl.adapters_grad(c.dy, c.xq, c.eta, c.packed, c.gamma, c.A, c.B, c.scale, c.ids)
+    c.ids[1030] = -1
+    without = bl.adapters_grad(c.dy, c.xq, c.eta, c.packed, c.gamma, c.A, c.B, c.scale, c.ids)
+    c.dy[1030, 33] = bad
+    for o, w in zip((F32, BF), clean):
+        got = bl.grad_weight(c.dy, c.xq, c.eta, out_dtype=o)
+        assert got[33].isnan().all()
+        assert torch.equal(got[torch.arange(70, device="cuda") != 33], w[torch.arange(70, device="cuda") != 33])
+    others = torch.arange(1100, device="cuda") != 1030
+    assert torch.equal(bl.grad_input(c.dy, c.packed, c.gamma, 200)[others], dx[others])
+    # the token has no adapter: dA and dB do not meet it
+    got = bl.adapters_grad(c.dy, c.xq, c.eta, c.packed, c.gamma, c.A, c.B, c.scale, c.ids)
+    assert torch.equal(got[0][others], grads[0][others])
+    assert torch.equal(got[1], without[1]) and torch.equal(got[2], without[2])

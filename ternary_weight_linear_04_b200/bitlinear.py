@@ -366,9 +366,9 @@ def _place(stream, *ts):
     for t in ts:
         if t is None:
             continue
-        if not (t.is_cuda and t.is_contiguous()):
+        at = t.get_device()  # -1: not a CUDA tensor
+        if at < 0 or not t.is_contiguous():
             raise ValueError("tensors must be contiguous CUDA tensors")
-        at = t.get_device()
         if at != index:
             if index >= 0:
                 raise ValueError("tensors must be on one device")
@@ -378,6 +378,11 @@ def _place(stream, *ts):
             raise ValueError("stream must be on the tensors' device")
         return torch.cuda.stream(stream)
     return _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+
+def _stream_of(t):
+    """The current stream of the tensor's device (which _place made current)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _al16(t):
@@ -398,7 +403,7 @@ def _out(out, shape, dtype, like, name="out"):
     if dtype not in _DTYPES:
         raise ValueError("%s must be float32 or bfloat16" % name)
     if out is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
     _check(name, out, shape, *_DTYPES)
     if not out.is_cuda or out.device != like.device or not out.is_contiguous() or out.data_ptr() % 16:
         raise ValueError("%s must be contiguous, on the inputs' device and 16-byte aligned" % name)
@@ -416,6 +421,8 @@ def _ws_bytes(call, *sizes):
 
 
 def _codes(xq, eta, M):
+    if xq.dtype is torch.int8 and eta.dtype is torch.float32 and eta.shape == (M,) and xq.dim() == 2 and xq.shape[0] == M:
+        return
     if xq.dim() != 2 or xq.shape[0] != M:
         raise ValueError("xq must be int8 with %d rows" % M)
     _check("xq", xq, xq.shape, torch.int8)
@@ -423,6 +430,9 @@ def _codes(xq, eta, M):
 
 
 def _packed(packed, gamma, N, K):
+    if (packed.dtype is torch.uint8 and gamma.dtype is torch.float32 and packed.shape == (N, (K + 3) // 4)
+            and gamma.shape == (1,)):
+        return
     _check("packed", packed, (N, (K + 3) // 4), torch.uint8)
     _check("gamma", gamma, (1,), torch.float32)
 
@@ -431,7 +441,10 @@ def _adapters(A, B, scale, ids, M, N, K):
     """(L, r) of an adapter set whose shapes fit."""
     if A.dim() != 3 or B.dim() != 3:
         raise ValueError("A must be L x r x K and B L x N x r")
-    L, r = A.shape[:2]
+    L, r, k = A.shape
+    if (A.dtype is torch.bfloat16 and B.dtype is torch.bfloat16 and scale.dtype is torch.float32
+            and ids.dtype is torch.int32 and k == K and B.shape == (L, N, r) and scale.shape == (L,) and ids.shape == (M,)):
+        return L, r
     _check("A", A, (L, r, K), torch.bfloat16)
     _check("B", B, (L, N, r), torch.bfloat16)
     _check("scale", scale, (L,), torch.float32)
@@ -454,7 +467,7 @@ def grad_input(dy, packed, gamma, K, out_dtype=torch.bfloat16, stream=None, out=
         ws = _scratch(nws, dy)
         dy, packed = _al16(dy), _al16(packed)
         check(L.bitlinear_grad_input(_ptr(dy), dt, M, N, _ptr(packed), _ptr(gamma), K, _ptr(dx),
-                                     _DTYPES[dx.dtype], _ptr(ws), nws, _stream(None)), "bitlinear_grad_input")
+                                     _DTYPES[dx.dtype], _ptr(ws), nws, _stream_of(dy)), "bitlinear_grad_input")
     return dx
 
 
@@ -474,7 +487,7 @@ def grad_weight(dy, xq, eta, out_dtype=torch.float32, stream=None, out=None):
         ws = _scratch(nws, dy)
         dy, xq = _al16(dy), _al16(xq)
         check(L.bitlinear_grad_weight(_ptr(dy), dt, _ptr(xq), _ptr(eta), M, N, K, _ptr(dw), wt, _ptr(ws), nws,
-                                      _stream(None)), "bitlinear_grad_weight")
+                                      _stream_of(dy)), "bitlinear_grad_weight")
     return dw
 
 
@@ -491,7 +504,7 @@ def rmsnorm_grad(dn, xq, eta, rstd, out_dtype=torch.bfloat16, stream=None, out=N
     with _place(stream, dn, xq, eta, rstd):
         dx = _out(out, (M, K), out_dtype, dn)
         check(_lib.lib().bitlinear_rmsnorm_grad(_ptr(dn), _DTYPES[dn.dtype], _ptr(xq), _ptr(eta), _ptr(rstd),
-                                                M, K, _ptr(dx), _DTYPES[dx.dtype], _stream(None)),
+                                                M, K, _ptr(dx), _DTYPES[dx.dtype], _stream_of(dn)),
               "bitlinear_rmsnorm_grad")
     return dx
 
@@ -518,7 +531,7 @@ def forward_adapters(xq, eta, xsum, packed, gamma, N, A, B, scale, ids, out_dtyp
         check(L.bitlinear_forward_adapters(
             _ptr(xq), _ptr(eta), _ptr(xsum), M, K, _ptr(packed), _ptr(gamma), N, _ptr(A), _ptr(B),
             _ptr(scale), _ptr(ids), n_ad, r, _ptr(y), _DTYPES[y.dtype], _ptr(ws), nws,
-            _lib.BL_FLAG_WEIGHTS_STATIC if weights_static else 0, _stream(None)), "bitlinear_forward_adapters")
+            _lib.BL_FLAG_WEIGHTS_STATIC if weights_static else 0, _stream_of(xq)), "bitlinear_forward_adapters")
     return y
 
 
@@ -540,7 +553,7 @@ def linear_adapters(x, packed, gamma, N, A, B, scale, ids, out_dtype=torch.bfloa
         flags = (_lib.BL_FLAG_WEIGHTS_STATIC if weights_static else 0) | (_lib.BL_FLAG_RMSNORM if rmsnorm else 0)
         check(L.bitlinear_linear_adapters(
             _ptr(x), _DTYPES[x.dtype], M, K, _ptr(packed), _ptr(gamma), N, _ptr(A), _ptr(B), _ptr(scale), _ptr(ids),
-            n_ad, r, _ptr(y), _DTYPES[y.dtype], _ptr(ws), nws, flags, _stream(None)), "bitlinear_linear_adapters")
+            n_ad, r, _ptr(y), _DTYPES[y.dtype], _ptr(ws), nws, flags, _stream_of(x)), "bitlinear_linear_adapters")
     return y
 
 
@@ -571,7 +584,7 @@ def adapters_grad(dy, xq, eta, packed, gamma, A, B, scale, ids, out_dtype=torch.
         check(L.bitlinear_adapters_grad(
             _ptr(dy), dt, _ptr(xq), _ptr(eta), M, N, K, _ptr(packed), _ptr(gamma), _ptr(A), _ptr(B),
             _ptr(scale), _ptr(ids), n_ad, r, _ptr(dx), _DTYPES[out_dtype], _ptr(dA), _ptr(dB),
-            _DTYPES[grad_dtype], _ptr(ws), nws, _stream(None)), "bitlinear_adapters_grad")
+            _DTYPES[grad_dtype], _ptr(ws), nws, _stream_of(dy)), "bitlinear_adapters_grad")
     return dx, dA, dB
 
 

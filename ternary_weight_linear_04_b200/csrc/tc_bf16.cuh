@@ -139,12 +139,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return reinterpret_cast<const uint32_t&>(p);
 }
 
-// (lo, hi) minus their bf16 pair, rounded to a bf16 pair: what the first
-// rounding left (the difference is exact), so that pair + rest hold 16 bits.
-__device__ __forceinline__ uint32_t pack_bf16_rest(float lo, float hi, uint32_t pair) {
-  return pack_bf16(__fsub_rn(lo, __uint_as_float(pair << 16)), __fsub_rn(hi, __uint_as_float(pair & 0xFFFF0000u)));
-}
-
 // Sixteen values of one output row at `col`, to fp32 or bf16; `vec`: 16-byte
 // stores are aligned and the sixteen are inside the row, else one by one up
 // to `cols`.

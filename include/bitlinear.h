@@ -628,11 +628,10 @@ bl_status bitlinear_rmsnorm_grad(const void* dn, bl_dtype dndt, const int8_t* xq
  *   y = x^ W^T + scale_a (x^ A_a^T) B_a^T
  * (the projection alone where ids[m] is outside [0, L), -1 by convention).
  * The adapters read the same 8-bit tokens as the projection; x^ A^T is
- * summed in fp32, and enters the second product as it is (up to 16 tokens),
- * as three bf16 parts that hold all of it (fp32 y), or as two that hold 16
- * bits of it (bf16 y).  A token's output depends on no other token's adapter,
- * whatever that one holds (infinities and NaN too).  No counterpart on the
- * pages.
+ * summed in fp32 and enters the second product as it is or as three bf16
+ * parts that hold all of it.  A token's output depends on no other token's
+ * adapter, whatever that one holds (infinities and NaN too).  No counterpart
+ * on the pages.
  *   xq, eta, xsum, packed, gamma, flags   in   as for bitlinear_forward_path.
  *   A       in   bf16, L x r x K.
  *   B       in   bf16, L x N x r.
@@ -672,11 +671,11 @@ bl_status bitlinear_linear_adapters(const void* x, bl_dtype xdt, int64_t M, int6
  *   dx   = dy W^ + v A_a                      M x K
  *   dA_a = sum over the tokens of a: v^T x^   L x r x K
  *   dB_a = sum over the tokens of a: dy^T u   L x N x r
- * v and u enter their products as two bf16 parts (16 bits of them; three,
- * all of them, where the result is fp32).  What an adapter's factors hold,
- * infinities and NaN too, reaches its own tokens and its own gradients only.
- * An adapter that no token uses gets zeros.  dx may be NULL (not computed;
- * packed and gamma may then be NULL too), and so may dA and dB together.
+ * v and u enter their products as three bf16 parts that hold all of them.
+ * What an adapter's factors hold, infinities and NaN too, reaches its own
+ * tokens and its own gradients only.  An adapter that no token uses gets
+ * zeros.  dx may be NULL (not computed; packed and gamma may then be NULL
+ * too), and so may dA and dB together.
  *   dabdt   in   type of dA and dB, fp32 or bf16.
  *   other arguments as for bitlinear_forward_adapters and
  *   bitlinear_grad_input.

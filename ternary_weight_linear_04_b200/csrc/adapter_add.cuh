@@ -107,6 +107,11 @@ __device__ __forceinline__ int tile_adapters(const int32_t* ids, const int32_t* 
   return tile_adapters(ids, rows, m0, M, BM, L, s_ids, s_list, s_cnt, static_cast<int>(threadIdx.x), [] { __syncthreads(); });
 }
 
+// u and v enter the tensor cores' products as this many bf16 values whose sum
+// they are (8 of the 24 bits each): two would drop 2^-17 of them, which shows
+// in a bf16 result wherever terms cancel.
+constexpr int kFactorParts = 3;
+
 // Part p of the bf16 values x0 + x1 + x2 that hold an fp32 (8 bits each, the
 // differences exact).
 template <int P>
@@ -135,15 +140,15 @@ __device__ __forceinline__ void load_words(const void* p, uint32_t* o) {
 }
 
 // Entries of the adapters' contraction in the tensor-core kernels: for each
-// adapter of a tile P parts of its r values, padded to rp (a multiple of 8,
+// adapter of a tile three parts of its r values, padded to rp (a multiple of 8,
 // or 1, 2 or 4), so that eight entries from a multiple of 8 on are whole
 // pairs (adapter, part), or lie inside one, and need one division.
 __host__ __device__ constexpr int padded_rank(int r) { return r > 4 ? (r + 7) / 8 * 8 : r == 3 ? 4 : r; }
 
 // Eight entries from e on of a token's row: its own adapter's begin at entry
 // `own`, the rest are zeros.  x: the token's row of u (or v), scaled by f.
-template <int P>
 __device__ __forceinline__ uint4 own_entries(int e, int own, int r, int rp, const float* x, float f) {
+  constexpr int P = kFactorParts;
   const int i0 = e - own, rs = rank_stride(r);
   float v[8];
   if (rp >= 8) {  // all of one part

@@ -590,8 +590,8 @@ __global__ void __launch_bounds__(kUvThreads, 1) k_adapter_uv(const __grid_const
 //   out[j][c] += coef[m][j] x[m][c],   dA: coef = v eta / 127, x = x~;
 //                                      dB: coef = u,           x = dy
 // on mma.sync, both operands transposed out of shared memory by ldmatrix.
-// The coefficients go in as P bf16 parts (two for bf16 results, three for
-// fp32 ones); the next chunk's rows are loaded while one is multiplied.
+// The coefficients go in as three bf16 parts; the next chunk's rows are loaded
+// while one is multiplied.
 // Bound by the longest adapter's chain of chunks.  2048 tokens of 4 adapters,
 // K 4096, N 11008: 38 us (x~ and dy are 53 MB: 8 us).
 
@@ -617,8 +617,8 @@ constexpr int kDabCols = 64;
 constexpr int kDabXPitch = kDabCols + 8;
 
 __host__ __device__ constexpr int dab_rows(int r) { return (r + 15) / 16 * 16; }
-__host__ __device__ constexpr size_t dab_smem(int r, int parts, int xparts) {
-  const size_t tiles = static_cast<size_t>(kDabTokens) * 2 * (parts * (dab_rows(r) + 8) + xparts * kDabXPitch);
+__host__ __device__ constexpr size_t dab_smem(int r, int xparts) {
+  const size_t tiles = static_cast<size_t>(kDabTokens) * 2 * (kFactorParts * (dab_rows(r) + 8) + xparts * kDabXPitch);
   const size_t out = static_cast<size_t>(dab_rows(r)) * (kDabCols + 4) * 4;
   return tiles > out ? tiles : out;
 }
@@ -626,7 +626,7 @@ __host__ __device__ constexpr size_t dab_smem(int r, int parts, int xparts) {
 // JT: tiles of 16 rank indices (r <= 16 JT).
 template <typename XT, typename OutT, int JT>
 __device__ __forceinline__ void dab_tile(const DabArgs& g, const DabSide& s, int64_t c0, bool is_a, uint8_t* smem) {
-  constexpr int P = sizeof(OutT) == 4 ? 3 : 2, PX = sizeof(XT) == 4 ? 3 : 1;
+  constexpr int P = kFactorParts, PX = sizeof(XT) == 4 ? 3 : 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int CS = static_cast<int>(cluster_nctarank()), z = CS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int r = g.r, rows = dab_rows(r), cpitch = rows + 8;

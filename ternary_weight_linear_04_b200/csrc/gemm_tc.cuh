@@ -84,8 +84,8 @@ struct TcCfg {
 // of 64 entries of a second contraction (kind::f16, bf16 with fp32 sums, its
 // own TMEM columns): an entry is one (adapter of the tile's tokens, part of
 // u, rank index), its weight-side row B_a and its token-side row the part of
-// u, zero for the tokens of other adapters.  u (fp32) is split into two bf16
-// parts for bf16 outputs (2^-17 of it) and three for fp32 ones (all of it).
+// u, zero for the tokens of other adapters.  u (fp32) is split into three
+// bf16 parts, which hold all of it.
 // Eight more warps write both operands: they find the tile's adapters and
 // hold the first step's values in registers while the K loop runs (built by
 // the unpack warps behind the loop, 16 us a tile of 256 tokens were left
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
               const float* __restrict__ gamma_p, int M, int K, int N, void* __restrict__ y,
               int32_t* __restrict__ y_int, int ksplit, int wstatic, const AdapterAdd ad) {
   using Cfg = TcCfg<BM>;
-  constexpr int kParts = sizeof(OutT) == 4 ? 3 : 2;
+  constexpr int kParts = kFactorParts;
   constexpr int S = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte aligned base (the swizzle atom), by pointer arithmetic on the
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
         vu[y4] = make_uint4(0, 0, 0, 0);
         const int own = tok < BM ? s_ids[tok] * group : -1;
         if (own < 0 || e + 8 <= own || e >= own + group) continue;
-        vu[y4] = own_entries<kParts>(e, own, r, rp, ad.u + static_cast<int64_t>(m0 + tok) * rank_stride(r), 1.0f);
+        vu[y4] = own_entries(e, own, r, rp, ad.u + static_cast<int64_t>(m0 + tok) * rank_stride(r), 1.0f);
       }
     };
     if (asteps > 0) load(0);

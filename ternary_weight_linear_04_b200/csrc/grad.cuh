@@ -131,8 +131,8 @@ __global__ void __launch_bounds__(256)
 // Adapters: behind the steps over n come steps of 64 entries, an entry being
 // one (adapter of the tile's tokens, part of v, rank index): v (each token's
 // row masked to its own adapter, divided by gamma because the sum is
-// multiplied by it at the end; three bf16 parts for fp32 results, two for
-// bf16 ones) against A_a's row, written by the expanding warps.
+// multiplied by it at the end; three bf16 parts) against A_a's row, written
+// by the expanding warps.
 
 constexpr int kGiBK = 64;    // n per step
 constexpr int kGiBN = 256;   // inputs k per tile
@@ -213,7 +213,7 @@ template <int H, typename OutT>
 __global__ void __launch_bounds__(kGiThreads, 1)
     k_grad_input(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_w, const GiArgs a) {
   using Cfg = GiCfg<H>;
-  constexpr int S = Cfg::kStages, SP = Cfg::kPStages, kParts = sizeof(OutT) == 4 ? 3 : 2;
+  constexpr int S = Cfg::kStages, SP = Cfg::kPStages, kParts = kFactorParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sA = base;
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kGiThreads, 1)
           const int tok = tok0 + 32 * (x4 + c), own = s_ids[tok] * group;
           o[c] = make_uint4(0, 0, 0, 0);
           if (own < 0 || e + 8 <= own || e >= own + group) continue;
-          o[c] = own_entries<kParts>(e, own, r, rp, a.v + static_cast<int64_t>(m0 + tok) * rank_stride(r), inv_gamma);
+          o[c] = own_entries(e, own, r, rp, a.v + static_cast<int64_t>(m0 + tok) * rank_stride(r), inv_gamma);
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(row + 4096 * (x4 + c)) = o[c];

@@ -335,9 +335,9 @@ template <typename DyT, typename OutT, int JT>
 bl_status launch_dab_jt(const bl::DabArgs& g, dim3 grid, cudaStream_t s) {
   static int done[kMaxDevices] = {0};
   auto kern = bl::k_adapter_dab<DyT, OutT, JT>;
-  constexpr int parts = sizeof(OutT) == 4 ? 3 : 2, xparts = sizeof(DyT) == 4 ? 3 : 1;
-  if (!ensure_smem(kern, bl::dab_smem(16 * JT, parts, xparts), done)) return BL_ERR_CUDA;
-  return launch_pdl_cluster(kern, grid, dim3(bl::kDabThreads), bl::dab_smem(g.r, parts, xparts), s, grid.z, g);
+  constexpr int xparts = sizeof(DyT) == 4 ? 3 : 1;
+  if (!ensure_smem(kern, bl::dab_smem(16 * JT, xparts), done)) return BL_ERR_CUDA;
+  return launch_pdl_cluster(kern, grid, dim3(bl::kDabThreads), bl::dab_smem(g.r, xparts), s, grid.z, g);
 }
 
 template <typename DyT, typename OutT>

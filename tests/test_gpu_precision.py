@@ -1,0 +1,89 @@
+"""What the sums of the backward pass and the adapters hold.
+
+Inputs for which every term and every partial sum is exact, built so that a
+value with fewer bits than fp32's, or a sum that is cut off instead of
+rounded, gives another result than the formula's.
+"""
+import pytest
+import torch
+
+from ternary_weight_linear_04_b200 import bitlinear as bl
+from ternary_weight_linear_04_b200 import build as libbuild
+from test_gpu_train import BF, F32, F64, Case, pack  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    libbuild.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    yield
+    assert bl.device_error() == 0
+
+
+def still(M, K, N, L=1, r=2):
+    """A case whose every input is zero, of unit scales."""
+    c = Case(M, K, N, L, r)
+    for t in (c.xq, c.xsum, c.dy, c.A, c.B, c.t):
+        t.zero_()
+    c.packed = pack(c.t)
+    c.gamma.fill_(1)
+    c.eta.fill_(127)
+    c.scale.fill_(1)
+    c.ids.zero_()
+    return c
+
+
+# 1 + 2^-10 + 2^-20 has 21 bits in three groups: no two bf16 values hold it
+LONG = (1.0, 2.0 ** -10, 2.0 ** -20)
+SHORT = (1.0, 2.0 ** -10, 0.0)
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("M,K,N", [(1, 64, 64), (16, 64, 64), (17, 64, 64), (40, 70, 33), (300, 64, 9000), (600, 64, 72)])
+def test_u_enters_y_whole(M, K, N, out):
+    """u = (1 + 2^-10 + 2^-20, -1 - 2^-10) against B = (1, 1): 2^-20 is left."""
+    c = still(M, K, N)
+    c.xq[:, :3] = 1
+    c.xsum[:] = 3
+    c.A[0, 0, :3] = torch.tensor(LONG).to(BF)
+    c.A[0, 1, :3] = -torch.tensor(SHORT).to(BF)
+    c.B.fill_(1)
+    y = bl.forward_adapters(c.xq, c.eta, c.xsum, c.packed, c.gamma, N, c.A, c.B, c.scale, c.ids, out_dtype=out)
+    assert (y == 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("M,K,N", [(1, 64, 64), (40, 70, 33), (300, 9000, 64), (1800, 4096, 64)])
+def test_v_enters_dx_whole(M, K, N, dt, out):
+    c = still(M, K, N)
+    c.dy = c.dy.to(dt)
+    c.dy[:, :3] = torch.tensor(LONG).to(dt)
+    c.B[0, :3, 0] = 1
+    c.B[0, :2, 1] = -1
+    c.A.fill_(1)
+    dx = bl.adapters_grad(c.dy, c.xq, c.eta, c.packed, c.gamma, c.A, c.B, c.scale, c.ids, out_dtype=out, want_dab=False)[0]
+    assert (dx == 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("M", [2, 32, 128, 1024])
+@pytest.mark.parametrize("r", [2, 40, 128])
+def test_u_and_v_enter_the_factors_gradients_whole(M, r, out):
+    """Every other token's u and v are -(1 + 2^-10): M / 2 times 2^-20 are left."""
+    c = still(M, 64, 72, 1, r)
+    c.xq[0::2, :3] = 1
+    c.xq[1::2, :2] = -1
+    c.A[0, 0, :3] = torch.tensor(LONG).to(BF)
+    c.dy[:, 5] = 1
+    dB = bl.adapters_grad(c.dy, c.xq, c.eta, c.packed, c.gamma, c.A, c.B, c.scale, c.ids, grad_dtype=out, want_dx=False)[2]
+    assert (dB[0, 5, 0] == M / 2 * 2.0 ** -20) and dB.count_nonzero() == 1
+    c = still(M, 64, 72, 1, r)
+    c.dy[0::2, :3] = torch.tensor(LONG).to(BF)
+    c.dy[1::2, :3] = -torch.tensor(SHORT).to(BF)
+    c.B[0, :3, 0] = 1
+    c.xq[:, 7] = 1
+    dA = bl.adapters_grad(c.dy, c.xq, c.eta, c.packed, c.gamma, c.A, c.B, c.scale, c.ids, grad_dtype=out, want_dx=False)[1]
+    assert (dA[0, 0, 7] == M / 2 * 2.0 ** -20) and dA.count_nonzero() == 1

@@ -112,17 +112,23 @@ __device__ __forceinline__ int tile_adapters(const int32_t* ids, const int32_t* 
 // in a bf16 result wherever terms cancel.
 constexpr int kFactorParts = 3;
 
-// Part p of the bf16 values x0 + x1 + x2 that hold an fp32 (8 bits each, the
-// differences exact).
-template <int P>
+// The bf16 values x0 + x1 + x2 that hold an fp32: its top 16 bits, those of
+// the rest, and the last 8 bits (differences exact).  Cutting off instead of
+// rounding takes no conversion, and the top of a large number stays finite;
+// an infinity has no rest.
+__device__ __forceinline__ float bf16_top(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
+__device__ __forceinline__ float bf16_rest(float x) {
+  const float h = bf16_top(x);
+  return x == h ? 0.0f : __fsub_rn(x, h);
+}
+// Its part p, in the top half of the word.
 __device__ __forceinline__ float bf16_part(float x, int p) {
-#pragma unroll
-  for (int i = 1; i < P; ++i)
-    if (p >= i) {
-      const float h = __bfloat162float(__float2bfloat16_rn(x));
-      x = __fsub_rn(h, h) == 0.0f ? __fsub_rn(x, h) : 0.0f;  // an infinity has no rest
-    }
-  return x;  // to be rounded to bf16
+  if (p >= 1) x = bf16_rest(x);
+  return p >= 2 ? bf16_rest(x) : x;
+}
+// Two parts as a bf16 pair (lo in the low half).
+__device__ __forceinline__ uint32_t pack_tops(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
 
 // n words from an address that need not be on four bytes (all of the n + 1
@@ -157,19 +163,17 @@ __device__ __forceinline__ uint4 own_entries(int e, int own, int r, int rp, cons
     const float4 hi = j + 4 < rs ? *reinterpret_cast<const float4*>(x + j + 4) : make_float4(0, 0, 0, 0);
     const float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-    for (int b = 0; b < 8; ++b) v[b] = bf16_part<P>(__fmul_rn(y[b], f), p);
+    for (int b = 0; b < 8; ++b) v[b] = bf16_part(__fmul_rn(y[b], f), p);
   } else {
     const float4 y = *reinterpret_cast<const float4*>(x);
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
       const int i = i0 + b, p = i >= 2 * rp ? 2 : i >= rp ? 1 : 0, j = i - p * rp;
       const float w = j == 0 ? y.x : j == 1 ? y.y : j == 2 ? y.z : y.w;  // zero past r
-      v[b] = i >= 0 && i < P * rp ? bf16_part<P>(__fmul_rn(w, f), p) : 0.0f;
+      v[b] = i >= 0 && i < P * rp ? bf16_part(__fmul_rn(w, f), p) : 0.0f;
     }
   }
-  const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3]),
-                               __floats2bfloat162_rn(v[4], v[5]), __floats2bfloat162_rn(v[6], v[7])};
-  return reinterpret_cast<const uint4&>(h);
+  return make_uint4(pack_tops(v[0], v[1]), pack_tops(v[2], v[3]), pack_tops(v[4], v[5]), pack_tops(v[6], v[7]));
 }
 
 // Which of a pair of bf16 are infinities or NaN (the top bit of each half).

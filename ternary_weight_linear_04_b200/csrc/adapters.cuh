@@ -378,9 +378,9 @@ struct UvRaw {
       } else {
         float f[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = bf16_part<3>(__uint_as_float(w[h][4 * i + j]), part);
-        xf[h] = pack_bf16(f[0], f[1]);
-        xf[2 + h] = pack_bf16(f[2], f[3]);
+        for (int j = 0; j < 4; ++j) f[j] = bf16_part(__uint_as_float(w[h][4 * i + j]), part);
+        xf[h] = pack_tops(f[0], f[1]);
+        xf[2 + h] = pack_tops(f[2], f[3]);
       }
     }
   }
@@ -715,8 +715,8 @@ __device__ __forceinline__ void dab_tile(const DabArgs& g, const DabSide& s, int
           uint32_t o[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            o[k] = pack_bf16(bf16_part<PX>(__uint_as_float(xr[8 * i + 2 * k]), p),
-                             bf16_part<PX>(__uint_as_float(xr[8 * i + 2 * k + 1]), p));
+            o[k] = pack_tops(bf16_part(__uint_as_float(xr[8 * i + 2 * k]), p),
+                             bf16_part(__uint_as_float(xr[8 * i + 2 * k + 1]), p));
           dst[p * (kDabTokens * kDabXPitch / 8) + i] = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
@@ -726,8 +726,8 @@ __device__ __forceinline__ void dab_tile(const DabArgs& g, const DabSide& s, int
 #pragma unroll
       for (int p = 0; p < P; ++p)
         *reinterpret_cast<uint2*>(s_coef + (p * kDabTokens + xt) * cpitch + xh * (rows / 2) + i) =
-            make_uint2(pack_bf16(bf16_part<P>(cf[i], p), bf16_part<P>(cf[i + 1], p)),
-                       pack_bf16(bf16_part<P>(cf[i + 2], p), bf16_part<P>(cf[i + 3], p)));
+            make_uint2(pack_tops(bf16_part(cf[i], p), bf16_part(cf[i + 1], p)),
+                       pack_tops(bf16_part(cf[i + 2], p), bf16_part(cf[i + 3], p)));
     }
   };
   int c = from + z * kDabTokens;  // this CTA's chunks: every CS-th

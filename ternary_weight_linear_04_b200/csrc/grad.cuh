@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(256) k_pad_rows(const PadJob first, const PadJ
 }
 
 // fp32 rows as three bf16 planes (rows x cols_pad each, zero past cols) whose
-// sum is the fp32 value: 8 bits each of its 24, the differences exact.
+// sum is the fp32 value (bf16_part).
 __global__ void __launch_bounds__(256)
     k_split_planes(const float* __restrict__ src, int64_t rows, int64_t cols, int64_t cols_pad,
                    __nv_bfloat16* __restrict__ dst) {
@@ -95,12 +95,8 @@ __global__ void __launch_bounds__(256)
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < plane; i += gridDim.x * 256ll) {
     const int64_t row = i / cols_pad, c = i - row * cols_pad;
     const float f = c < cols ? src[row * cols + c] : 0.0f;
-    const __nv_bfloat16 a = __float2bfloat16_rn(f);
-    const float fa = __fsub_rn(f, __bfloat162float(a));
-    const __nv_bfloat16 b = __float2bfloat16_rn(fa);
-    dst[i] = a;
-    dst[plane + i] = b;
-    dst[2 * plane + i] = __float2bfloat16_rn(__fsub_rn(fa, __bfloat162float(b)));
+#pragma unroll
+    for (int p = 0; p < 3; ++p) dst[p * plane + i] = __ushort_as_bfloat16(static_cast<unsigned short>(__float_as_uint(bf16_part(f, p)) >> 16));
   }
 }
 

@@ -87,3 +87,41 @@ def test_u_and_v_enter_the_factors_gradients_whole(M, r, out):
     c.xq[:, 7] = 1
     dA = bl.adapters_grad(c.dy, c.xq, c.eta, c.packed, c.gamma, c.A, c.B, c.scale, c.ids, grad_dtype=out, want_dx=False)[1]
     assert (dA[0, 0, 7] == M / 2 * 2.0 ** -20) and dA.count_nonzero() == 1
+
+
+TOP = torch.finfo(F32).max  # rounds to infinity in bf16
+
+
+@pytest.mark.parametrize("M,K,N", [(3, 64, 64), (40, 130, 70), (300, 9000, 72)])
+@pytest.mark.parametrize("big", [float("inf"), -float("inf"), TOP, -TOP])
+def test_an_fp32_gradient_past_bf16(M, K, N, big):
+    """Infinities and the largest numbers of an fp32 dy stay what they are in dx, v and dA, and large numbers in dB."""
+    c = still(M, K, N, 1, 3)
+    c.dy = c.dy.float()
+    c.dy[2, 5] = big
+    c.t[5, 0::2] = 1
+    c.t[5, 1::2] = -1
+    c.packed = pack(c.t)
+    c.gamma.fill_(0.125)
+    want = torch.full((K,), big * 0.125, device="cuda")
+    want[1::2] *= -1
+    if abs(big) == float("inf"):  # the sum of a row meets no zero of another output's weights
+        c.t[c.t == 0] = 1
+        c.packed = pack(c.t)
+    for out in (F32, BF):
+        dx = bl.grad_input(c.dy, c.packed, c.gamma, K, out_dtype=out)
+        assert torch.equal(dx[2], want.to(out))
+        assert not dx[:2].any() and not dx[3:].any()
+    c.xq[2, 7] = 16
+    c.eta.fill_(127)
+    c.A[0, 0, 7] = 2.0 ** -7  # u = 1 / 8
+    dB = bl.adapters_grad(c.dy, c.xq, c.eta, None, None, c.A, c.B, c.scale, c.ids, grad_dtype=F32, want_dx=False)[2]
+    if abs(big) == float("inf"):  # times the empty parts of u: an infinity here may come out as NaN
+        assert not dB[0, 5, 0].isfinite()
+    else:
+        assert float(dB[0, 5, 0]) == big * 0.125
+    assert not dB[0, :5].any() and not dB[0, 6:].any()
+    c.eta.fill_(127 / 1024.)  # x^ = 16 / 1024
+    c.B[0, 5, 1] = 1
+    dA = bl.adapters_grad(c.dy, c.xq, c.eta, None, None, c.A, c.B, c.scale, c.ids, grad_dtype=F32, want_dx=False)[1]
+    assert float(dA[0, 1, 7]) == big / 64

@@ -590,8 +590,10 @@ __global__ void __launch_bounds__(kUvThreads, 1) k_adapter_uv(const __grid_const
 //   out[j][c] += coef[m][j] x[m][c],   dA: coef = v eta / 127, x = x~;
 //                                      dB: coef = u,           x = dy
 // on mma.sync, both operands transposed out of shared memory by ldmatrix.
-// The coefficients go in as three bf16 parts; the next chunk's rows are loaded
-// while one is multiplied.
+// The coefficients go in as three bf16 parts.  The MMA cuts its sums off, which
+// would pull a long one towards zero: 16 tokens' terms are added to the running
+// sum by an addition that rounds.  The next chunk's rows are loaded while one is
+// multiplied.
 // Bound by the longest adapter's chain of chunks.  2048 tokens of 4 adapters,
 // K 4096, N 11008: 38 us (x~ and dy are 53 MB: 8 us).
 
@@ -747,16 +749,21 @@ __device__ __forceinline__ void dab_tile(const DabArgs& g, const DabSide& s, int
 #pragma unroll
       for (int t = 0; t < JT; ++t) {
         if (16 * t >= rows) continue;
+        float sum[2][4] = {};  // these 16 tokens' terms, the small parts first
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
+        for (int p = P - 1; p >= 0; --p) {
           uint32_t f[4];  // rows j 0-7, 8-15 at tokens 0-7, then at 8-15
           ldmatrix_x4_trans(f, s_coef + (p * kDabTokens + 16 * ks + kk + 8 * (mat >> 1)) * cpitch + 16 * t + 8 * (mat & 1));
 #pragma unroll
-          for (int px = 0; px < PX; ++px) {
-            mma_bf16_16816(acc[t][0], f[0], f[1], f[2], f[3], bx[px][0], bx[px][1]);
-            mma_bf16_16816(acc[t][1], f[0], f[1], f[2], f[3], bx[px][2], bx[px][3]);
+          for (int px = PX - 1; px >= 0; --px) {
+            mma_bf16_16816(sum[0], f[0], f[1], f[2], f[3], bx[px][0], bx[px][1]);
+            mma_bf16_16816(sum[1], f[0], f[1], f[2], f[3], bx[px][2], bx[px][3]);
           }
         }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][n][i] = __fadd_rn(acc[t][n][i], sum[n][i]);
       }
     }
     __syncthreads();

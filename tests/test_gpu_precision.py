@@ -125,3 +125,37 @@ def test_an_fp32_gradient_past_bf16(M, K, N, big):
     c.B[0, 5, 1] = 1
     dA = bl.adapters_grad(c.dy, c.xq, c.eta, None, None, c.A, c.B, c.scale, c.ids, grad_dtype=F32, want_dx=False)[1]
     assert float(dA[0, 1, 7]) == big / 64
+
+
+# A sum in fp32 that rounds to nearest is off by at most half a step for each
+# addition; one that cuts off, by a whole one.  Here a running sum of 2^24
+# (steps of 2) takes 63/32 once for each further 16 tokens: cut off, none of
+# them arrives.
+
+def additions(M):
+    return (M + 15) // 16
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("r", [2, 40, 128])
+def test_factors_gradients_round_to_nearest(dt, r):
+    M = 240  # one CTA's chain: clusters split 256 tokens and more
+    c = still(M, 64, 72, 1, r)
+    c.dy = c.dy.to(dt)
+    c.B[0, 3, 0] = 1
+    c.dy[0, 3] = 2.0 ** 24
+    c.dy[16::16, 3] = 63 / 32
+    c.xq[:, 7] = 1
+    want = 2.0 ** 24 + (additions(M) - 1) * 63 / 32
+    dA = bl.adapters_grad(c.dy, c.xq, c.eta, None, None, c.A, c.B, c.scale, c.ids, grad_dtype=F32, want_dx=False)[1]
+    assert abs(float(dA[0, 0, 7]) - want) <= additions(M) and dA.count_nonzero() == 1
+    c = still(M, 64, 72, 1, r)
+    c.dy = c.dy.to(dt)
+    c.A[0, 0, 5] = 1
+    c.xq[0, 5] = 1
+    c.xq[16::16, 5] = 63
+    c.eta[0] = 127 * 2.0 ** 24
+    c.eta[1:] = 127 / 32
+    c.dy[:, 3] = 1
+    dB = bl.adapters_grad(c.dy, c.xq, c.eta, None, None, c.A, c.B, c.scale, c.ids, grad_dtype=F32, want_dx=False)[2]
+    assert abs(float(dB[0, 3, 0]) - want) <= additions(M) and dB.count_nonzero() == 1

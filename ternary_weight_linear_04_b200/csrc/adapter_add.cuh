@@ -148,7 +148,9 @@ __device__ __forceinline__ void load_words(const void* p, uint32_t* o) {
 // Entries of the adapters' contraction in the tensor-core kernels: for each
 // adapter of a tile three parts of its r values, padded to rp (a multiple of 8,
 // or 1, 2 or 4), so that eight entries from a multiple of 8 on are whole
-// pairs (adapter, part), or lie inside one, and need one division.
+// pairs (adapter, part), or lie inside one, and need one division.  The small
+// part comes first: the MMA cuts its sums off, and would cut it off of a sum
+// that the large ones have made already.
 __host__ __device__ constexpr int padded_rank(int r) { return r > 4 ? (r + 7) / 8 * 8 : r == 3 ? 4 : r; }
 
 // Eight entries from e on of a token's row: its own adapter's begin at entry
@@ -158,7 +160,7 @@ __device__ __forceinline__ uint4 own_entries(int e, int own, int r, int rp, cons
   const int i0 = e - own, rs = rank_stride(r);
   float v[8];
   if (rp >= 8) {  // all of one part
-    const int p = i0 >= 2 * rp ? 2 : i0 >= rp ? 1 : 0, j = i0 - p * rp;
+    const int at = i0 >= 2 * rp ? 2 : i0 >= rp ? 1 : 0, p = P - 1 - at, j = i0 - at * rp;
     const float4 lo = *reinterpret_cast<const float4*>(x + j);
     const float4 hi = j + 4 < rs ? *reinterpret_cast<const float4*>(x + j + 4) : make_float4(0, 0, 0, 0);
     const float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -168,7 +170,7 @@ __device__ __forceinline__ uint4 own_entries(int e, int own, int r, int rp, cons
     const float4 y = *reinterpret_cast<const float4*>(x);
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
-      const int i = i0 + b, p = i >= 2 * rp ? 2 : i >= rp ? 1 : 0, j = i - p * rp;
+      const int i = i0 + b, at = i >= 2 * rp ? 2 : i >= rp ? 1 : 0, p = P - 1 - at, j = i - at * rp;
       const float w = j == 0 ? y.x : j == 1 ? y.y : j == 2 ? y.z : y.w;  // zero past r
       v[b] = i >= 0 && i < P * rp ? bf16_part(__fmul_rn(w, f), p) : 0.0f;
     }

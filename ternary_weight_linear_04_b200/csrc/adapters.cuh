@@ -271,14 +271,15 @@ __global__ void __launch_bounds__(kSortThreads)
 // One CTA per 16 tokens; its 16 warps take the contraction's steps of 64 in
 // turn and add their sums at the end (with few tokens a cluster splits the
 // contraction too).  Products on mma.sync m16n8k16: bf16 by bf16, fp32 sums;
-// x~ is exact in bf16, an fp32 dy goes in as three parts.  (tcgen05 would need
-// its operands in shared memory: the work is small beside reading dy, and
-// these fragments come straight from global memory.)  The order of the
-// contraction is free, so lane q of a row reads 16 consecutive codes, and A's
-// row the same 16; for v, B's rows lie across the contraction and pass
-// through shared memory (ldmatrix.trans).  A row's fragment is zeroed for the
-// adapters that are not its own.  The tokens' values of the next step are
-// loaded while this one's are multiplied: a warp's steps are a chain of
+// x~ is exact in bf16, an fp32 dy goes in as three parts.  The MMA cuts its
+// sums off: a step's is added to the running one by an addition that rounds.
+// (tcgen05 would need its operands in shared memory: the work is small beside
+// reading dy, and these fragments come straight from global memory.)  The
+// order of the contraction is free, so lane q of a row reads 16 consecutive
+// codes, and A's row the same 16; for v, B's rows lie across the contraction
+// and pass through shared memory (ldmatrix.trans).  A row's fragment is zeroed
+// for the adapters that are not its own.  The tokens' values of the next step
+// are loaded while this one's are multiplied: a warp's steps are a chain of
 // loads, and the time of the kernel: with the gradients behind it 76 us for u
 // and v of 2048 tokens (K 4096, N 11008, rank 16; reading dy takes 7).
 
@@ -428,6 +429,7 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
       } else {
         raw.load(row, k0, C, q, vec);
       }
+      float sum[NT][4] = {};  // this step's terms
       for (int lb = 0; lb < nad; lb += 4 / NT) {
         // slot x of the four: rank indices jb + 8 (x % NT) .. of adapter lb + x / NT
         uint4 w[4][2];
@@ -494,7 +496,7 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
               const uint32_t k0m = own[x / NT][0], k1m = own[x / NT][1];
               const uint4 f = w[x][i >> 1];
               const uint32_t lo = (i & 1) ? f.z : f.x, hi = (i & 1) ? f.w : f.y;
-              mma_bf16_16816(acc[x % NT], xf[0] & k0m, xf[1] & k1m, xf[2] & k0m, xf[3] & k1m,
+              mma_bf16_16816(sum[x % NT], xf[0] & k0m, xf[1] & k1m, xf[2] & k0m, xf[3] & k1m,
                              __byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
             }
           }
@@ -511,7 +513,7 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
           const int mat = lane >> 3, kk = lane & 7;
           const __nv_bfloat16* at = stage + (4 * (kk >> 1) + (kk & 1) + 2 * (mat & 1)) * kUvPitch + 8 * (mat >> 1);
 #pragma unroll 1
-          for (int part = 0; part < PX; ++part)
+          for (int part = PX - 1; part >= 0; --part)  // the small parts first
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t xf[4];
@@ -524,12 +526,16 @@ __device__ __forceinline__ void uv_tile(const UvArgs& g, const UvSide& s, uint8_
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                   const uint32_t k0m = own[(x + y) / NT][0], k1m = own[(x + y) / NT][1];
-                  mma_bf16_16816(acc[(x + y) % NT], xf[0] & k0m, xf[1] & k1m, xf[2] & k0m, xf[3] & k1m, d[2 * y], d[2 * y + 1]);
+                  mma_bf16_16816(sum[(x + y) % NT], xf[0] & k0m, xf[1] & k1m, xf[2] & k0m, xf[3] & k1m, d[2 * y], d[2 * y + 1]);
                 }
               }
             }
         }
       }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] = __fadd_rn(acc[n][i], sum[n][i]);
     }
     __syncthreads();  // the staged rows are read
 #pragma unroll

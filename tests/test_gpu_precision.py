@@ -159,3 +159,33 @@ def test_factors_gradients_round_to_nearest(dt, r):
     c.dy[:, 3] = 1
     dB = bl.adapters_grad(c.dy, c.xq, c.eta, None, None, c.A, c.B, c.scale, c.ids, grad_dtype=F32, want_dx=False)[2]
     assert abs(float(dB[0, 3, 0]) - want) <= additions(M) and dB.count_nonzero() == 1
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_v_rounds_to_nearest(dt):
+    """Steps of 64 outputs, 12 of them a warp: within the first step three MMAs may cut off (2 each), then eleven
+    additions of steps and fifteen of warps round (1 each)."""
+    M, K, N = 4800, 64, 64 * 16 * 12
+    c = still(M, K, N)
+    c.A[0, 0] = 1
+    c.B[0, :, 0] = 1
+    c.dy = c.dy.to(dt)
+    c.dy[:, 16::16] = 63 / 32
+    c.dy[:, 0] = 2.0 ** 24
+    want = 2.0 ** 24 + (N // 16 - 1) * 63 / 32
+    dx = bl.adapters_grad(c.dy, c.xq, c.eta, c.packed, c.gamma, c.A, c.B, c.scale, c.ids, out_dtype=F32, want_dab=False)[0]
+    assert float((dx.to(F64) - want).abs().max()) <= 3 * 2 + 11 + 15
+
+
+def test_u_rounds_to_nearest():
+    M, K, N = 4800, 64 * 16 * 12, 64
+    c = still(M, K, N)
+    for i in range(0, 16, 4):  # one for each MMA of a step: MMA i takes the codes 16 q + 4 i .. + 3 (q < 4)
+        c.A[0, 0, i::64] = 63 / 32
+    c.A[0, 0, 0] = 2.0 ** 24
+    c.xq.fill_(1)
+    c.xsum.fill_(K)
+    c.B[0, :, 0] = 1
+    want = 2.0 ** 24 + (K // 16 - 1) * 63 / 32
+    y = bl.forward_adapters(c.xq, c.eta, c.xsum, c.packed, c.gamma, N, c.A, c.B, c.scale, c.ids, out_dtype=F32)
+    assert float((y.to(F64) - want).abs().max()) <= 3 * 2 + 11 + 15

@@ -9,8 +9,11 @@
 // k_grad_input (here) contracts bf16 with bf16 values into fp32 accumulators
 // (tcgen05 kind::f16, accumulators in TMEM): W~ has the values -1, 0, +1,
 // exact in bf16, so the products are exact and only the sum rounds; gamma is
-// applied to the finished sum.  k_grad_weight (grad_weight.cuh) contracts
-// integers.
+// applied to the finished sum.  kind::f16 cuts its fp32 sums off instead of
+// rounding them, 16 terms at a time, so the planes of an fp32 dy come smallest
+// first: behind the tops, each of their steps would lose up to a last bit of
+// the whole sum (dx of 4096 x 4096 x 4096: 1.4e-5 off in the 2-norm that way,
+// 3e-7 this way).  k_grad_weight (grad_weight.cuh) contracts integers.
 #pragma once
 
 #include <cuda.h>
@@ -235,7 +238,8 @@ __global__ void __launch_bounds__(kGiThreads, 1)
   const int steps_n = (a.N + kGiBK - 1) / kGiBK;
   const int CS = H == 1 ? static_cast<int>(cluster_nctarank()) : 1;
   const int z = CS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  // this CTA's steps over n: [lo, lo + nst) of all planes'
+  // this CTA's steps over n: [lo, lo + nst) of all planes', the last plane's
+  // first
   const int64_t all = static_cast<int64_t>(steps_n) * a.planes;
   const int lo = static_cast<int>(all * z / CS), nst = static_cast<int>(all * (z + 1) / CS) - lo;
 
@@ -247,7 +251,7 @@ __global__ void __launch_bounds__(kGiThreads, 1)
   auto issue_a = [&](int i) {
     const int s = i % S;
     mbar_arrive_expect_tx(full_a + s, Cfg::kABytes);
-    tma_load_3d(sA + s * Cfg::kABytes, &tm_dy, full_a + s, ((lo + i) % steps_n) * kGiBK, m0, (lo + i) / steps_n);
+    tma_load_3d(sA + s * Cfg::kABytes, &tm_dy, full_a + s, ((lo + i) % steps_n) * kGiBK, m0, a.planes - 1 - (lo + i) / steps_n);
   };
   const int a_first = nst < S ? nst : S, p_first = nst < SP ? nst : SP;
   if (threadIdx.x == 0) {

@@ -189,3 +189,16 @@ def test_u_rounds_to_nearest():
     want = 2.0 ** 24 + (K // 16 - 1) * 63 / 32
     y = bl.forward_adapters(c.xq, c.eta, c.xsum, c.packed, c.gamma, N, c.A, c.B, c.scale, c.ids, out_dtype=F32)
     assert float((y.to(F64) - want).abs().max()) <= 3 * 2 + 11 + 15
+
+
+@pytest.mark.parametrize("M,K,N", [(100, 320, 4096), (1800, 4096, 4096), (300, 9000, 2048)])
+def test_the_low_planes_of_an_fp32_dy_are_not_cut_off(M, K, N):
+    """dy = 1 + 2^-22: the last bits add up to N 2^-22, which a running sum of the tops would lose."""
+    c = still(M, K, N)
+    c.dy = torch.full((M, N), 1 + 2.0 ** -22, device="cuda")
+    c.t.fill_(1)
+    c.packed = pack(c.t)
+    want = N + N * 2.0 ** -22
+    assert float(torch.tensor(want, dtype=F32)) == want
+    dx = bl.grad_input(c.dy, c.packed, c.gamma, K, out_dtype=F32)
+    assert (dx == want).all()

@@ -547,10 +547,10 @@ bl_status bitlinear_device_error(int32_t* code, void* stream);
  *
  * Conventions beside those above, for every call of this part:
  *   - dy, dn (gradients coming in) and the gradients going out are fp32 or
- *     bf16, row-major and dense.  Sums are held in fp32 (or finer); an
- *     output is rounded once.  Unlike the forward pass the results are
- *     floating-point sums: not bit-identical to an oracle's, but the same on
- *     every run (no atomics).
+ *     bf16, row-major and dense.  Sums are held in fp32 (bitlinear_grad_weight:
+ *     in fixed point, see there); an output is rounded once.  Unlike the
+ *     forward pass the results are floating-point sums: not bit-identical to
+ *     an oracle's, but the same on every run (no atomics).
  *   - Big operands are 16-byte aligned (BL_ERR_ALIGNMENT otherwise): dy,
  *     xq, packed, A, B, y, dx, dW, dA, dB; the workspace is 256-byte
  *     aligned.  Sizes are free (any M, N, K, r).
@@ -588,12 +588,15 @@ bl_status bitlinear_grad_input(const void* dy, bl_dtype dydt, int64_t M, int64_t
  *                  bitlinear_rmsnorm_quant_act (M x K, M).
  *   dw        out  N x K, fp32 or bf16.
  * The sum is one of integers: over each 1024 tokens the values dy eta / 127 of
- * an output n are rounded to 23 bits (fp32 dW) or 15 bits (bf16 dW) below the
- * largest of them, the products with x~ are then exact.  An error is thus
- * relative to that largest value: fp32 results of like-sized gradients come
- * out 2e-7 off in the 2-norm, and a token's gradients below 2^-23 (2^-15) of
- * the column's largest round to zero.  An infinity or a NaN in column n of dy
- * makes row n of dW NaN.
+ * an output n are rounded to a multiple of 2^-22 of the largest of them, the
+ * products with x~ are then exact, and the chunks' sums are added in fp32.
+ * Where the values of some output among 64 neighbours spread, the largest of
+ * them more than 2^4 (2^12) above the geometric mean of those that are not
+ * zero, all 64 are rounded to 2^-30 (2^-38) of their largest: a token's error
+ * is then at most 2^-17.9 of the geometric mean, up to a largest value 2^20
+ * above it (and 2^-39 of the largest beyond).  Results come out 1e-7 to 3e-7
+ * off in the 2-norm, also beside one token with far larger gradients.  An
+ * infinity or a NaN in column n of dy makes row n of dW NaN.
  */
 size_t bitlinear_grad_weight_workspace_bytes(int64_t M, int64_t N, int64_t K, bl_dtype dydt, bl_dtype dwdt);
 bl_status bitlinear_grad_weight(const void* dy, bl_dtype dydt, const int8_t* xq, const float* eta, int64_t M,

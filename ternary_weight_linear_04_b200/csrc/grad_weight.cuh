@@ -6,22 +6,32 @@
 //
 // The tokens are int8 already.  The other factor, g[m,n] = dy[m,n] f_m, is
 // held in fixed point: over each chunk of 1024 tokens a column n gets the
-// power of two that brings its largest |g| just below the top of ND signed
-// base-256 digits (k_gw_operands), q = round(g 2^e) = sum_j d_j 256^j with
-// d_j in [-128, 127].  The MMA sums d_j x~ over a chunk without any rounding
-// (at most 1024 * 128 * 127 < 2^24, so exact in fp32 too), and the epilogue adds D_j 256^j 2^-e to
-// fp32 accumulators in registers.  ND = 3 (23 bits beside the column's
-// largest value in the chunk) for fp32 results, ND = 2 (15 bits, against
-// the 8 of the result) for bf16 ones.
+// power of two that brings its largest |g| just below the top of three signed
+// base-256 digits (k_gw_operands), q = round(g 2^e) = sum_p d_p 256^(2-p) with
+// d_p in [-128, 127].  The MMA sums d_p x~ over a chunk without any rounding
+// (at most 1024 * 128 * 127 < 2^24, so exact in fp32 too), and the epilogue
+// adds D_p 256^(2-p) 2^-e to fp32 accumulators in registers.
+//
+// Three digits are 23 bits beside the column's largest value in the chunk.
+// That is finer than an fp32 sum while the values are of like size, but one
+// token with a large eta or a large gradient leaves the others few bits, and
+// outputs that it does not reach (its codes there are zero) would show it.  So
+// a block of 64 columns has a fourth and a fifth digit of g in a chunk where,
+// in some column, the largest |g| lies more than 2^4 and 2^12 above the
+// geometric mean of those that are not zero (in binary exponents): an error is
+// then at most 2^-17.9 of that mean for each token, while the largest is no more
+// than 2^20 above it.  Normal gradients are 2^2.5 to 2^3.5 above: three digits.
+// (One token 2^10 times the others: outputs without it were 5.8e-5 off in the
+// 2-norm with three digits.)
 //
 // Why integers: bf16 operands would need the token's value x~ f rounded to
 // 8 bits, or two such parts and two products (measured: 2.4e-6 off in the
-// 2-norm, and the fp32 accumulator of kind::f16 truncates, which pulls a
-// sum of 2048 tokens 4e-6 towards zero).  Two or three int8 products take
-// the time of 1 or 1.5 bf16 products and sum exactly.
+// 2-norm, and the fp32 accumulator of kind::f16 cuts off, which pulls a
+// sum of 2048 tokens 4e-6 towards zero).  Three int8 products take the time of
+// 1.5 bf16 products and sum exactly.
 //
-// Both operands are rewritten once with the tokens contiguous (K-major):
-// by k_gw_operands.
+// k_gw_operands rewrites both operands once with the tokens contiguous
+// (K-major).
 #pragma once
 
 #include <cuda.h>
@@ -39,11 +49,15 @@ constexpr int kGdTokens = 512;  // of a CTA that makes digits; two CTAs share a 
 // ---------------------------------------------------------------- operands
 
 // Digits of a 64-column, 512-token tile (a cluster of two CTAs makes a chunk's
-// and shares its maxima): lane = two neighbouring columns, a warp takes 32 tokens, held as they were read (two bf16 in a register)
-// between the column's maximum and the digits.  digits: ND planes of N x Mp
-// bytes (Mp a multiple of 16, zero past M); scale[chunk * N + n] = 2^-e, or
-// NaN where the column holds an infinity or a NaN (its whole gradient row is
-// then NaN, as it would be in floating point).
+// and shares its maxima): lane = two neighbouring columns, a warp takes 32
+// tokens, held as they were read (two bf16 in a register) between the column's
+// maximum and the digits.  digits: five planes of N x Mp
+// bytes (Mp a multiple of 16, zero past M), the largest digit first, the
+// fourth and fifth written where they are used; extra[chunk * groups + n / 64]
+// = 0, 1 or 2, how many of those are (groups: column blocks, rounded up to
+// four); scale[chunk * N + n] = 2^-e, or NaN where the column holds an
+// infinity or a NaN (its whole gradient row is then NaN, as it would be in
+// floating point).
 //
 // Rounding and splitting use no conversion instruction (a quarter of the
 // rate of an add): adding 1.5 2^23 rounds a value below 2^22 to an integer in
@@ -53,19 +67,28 @@ constexpr int kGdTokens = 512;  // of a CTA that makes digits; two CTAs share a 
 constexpr int kGdCols = 64;
 constexpr int kGdThreads = 512;
 
-// q + 0x808080 (ND = 3) or + 0x8080 (ND = 2), q = p rounded to an integer.
-template <int ND>
+constexpr int kGdPlanes = 5;
+
+// q + 0x808080, q = p rounded to an integer.
 __device__ __forceinline__ uint32_t biased_round(float p) {
   constexpr float kMagic = 12582912.0f;  // 1.5 2^23
   constexpr uint32_t kBits = 0x4B400000u;
-  if constexpr (ND == 2) {
-    return __float_as_uint(__fadd_rn(p, kMagic)) + (0x8080u - kBits);
-  } else {  // |p| passes 2^22: a multiple of 4096 first, the rest is exact
-    const float h = __fmaf_rn(p, 0x1p-12f, kMagic);
-    const float l = __fadd_rn(__fmaf_rn(__fsub_rn(h, kMagic), -4096.0f, p), kMagic);
-    return __float_as_uint(h) * 4096u + (__float_as_uint(l) + (0x808080u - 4097u * kBits));
-  }
+  // |p| passes 2^22: a multiple of 4096 first, the rest is exact
+  const float h = __fmaf_rn(p, 0x1p-12f, kMagic);
+  const float l = __fadd_rn(__fmaf_rn(__fsub_rn(h, kMagic), -4096.0f, p), kMagic);
+  return __float_as_uint(h) * 4096u + (__float_as_uint(l) + (0x808080u - 4097u * kBits));
 }
+
+// The same of p 2^16 with five digits: the upper three (PLANE 0) or the lower
+// two (PLANE 3) in the low bytes.
+template <int PLANE>
+__device__ __forceinline__ uint32_t biased_round_wide(float p) {
+  const long long q = __float2ll_rn(__fmul_rn(p, 65536.0f)) + 0x8080808080ll;
+  return static_cast<uint32_t>(PLANE == 0 ? q >> 16 : q & 0xFFFF);
+}
+
+// Digits of a tile's outputs in a chunk, from the four bytes of `extra`.
+__device__ __forceinline__ int gw_digits(uint32_t extra4) { return (extra4 & 0x02020202u) ? 5 : (extra4 & 0x01010101u) ? 4 : 3; }
 
 // The codes with the tokens contiguous: a tile of 64 inputs by 128 tokens of
 // xt (K x Mp) from xq (M x K), zero past M, transposed 4 x 4 bytes at a time
@@ -104,19 +127,20 @@ __device__ __forceinline__ void gw_codes_tile(const int8_t* __restrict__ xq, int
 
 // Both operands in one launch: blocks below digit_blocks make digits, the
 // others codes.
-template <typename DyT, int ND>
+template <typename DyT>
 __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
     k_gw_operands(unsigned digit_blocks, const int8_t* __restrict__ xq, int64_t K, uint8_t* __restrict__ xt,
                   const DyT* __restrict__ dy, const float* __restrict__ eta, int64_t M, int64_t N, int64_t Mp,
-                  int pairs, uint8_t* __restrict__ digits, float* __restrict__ scale) {
-  constexpr float kTop = ND == 3 ? 8355711.0f : 32639.0f;  // 127 (1 + 256 (+ 65536)): the largest q
-  constexpr int kBits = ND == 3 ? 22 : 14;
+                  int pairs, uint8_t* __restrict__ digits, float* __restrict__ scale, uint8_t* __restrict__ extra) {
+  constexpr float kTop = 8355711.0f;  // 127 (1 + 256 + 65536): the largest q
+  constexpr int kBits = 22;
   constexpr int kRegs = sizeof(DyT) == 2 ? 1 : 2;
-  extern __shared__ __align__(16) uint8_t smem[];  // ND x 64 columns x 512 bytes, words XORed with the lane
+  extern __shared__ __align__(16) uint8_t smem[];  // 3 x 64 columns x 512 bytes, words XORed with the lane
   __shared__ uint32_t s_max[16][kGdCols];
-  __shared__ uint32_t s_col[kGdCols];
+  __shared__ uint32_t s_col[2][kGdCols];
   __shared__ float s_f[kGdTokens];
   __shared__ uint32_t s_codes[64][33];
+  auto& s_exp = reinterpret_cast<uint32_t(&)[16][kGdCols]>(s_codes);  // (other blocks': two CTAs have to fit an SM)
   uint32_t* words = reinterpret_cast<uint32_t*>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t ntiles = (N + kGdCols - 1) / kGdCols;
@@ -167,25 +191,41 @@ __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
     const uint32_t u = kRegs == 2 ? raw[i][kRegs == 2 ? c : 0] : c ? raw[i][0] & 0xFFFF0000u : raw[i][0] << 16;
     return __fmul_rn(__uint_as_float(u), s_f[32 * warp + i]);
   };
-  uint32_t mx[2] = {0, 0};
+  // a column's largest magnitude, and of those that are not zero the number
+  // (from bit 20 on) and the sum of the exponents (at most 1024 * 255)
+  uint32_t mx[2] = {0, 0}, ex[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 32; i += 2)
 #pragma unroll
-    for (int c = 0; c < 2; ++c)  // orders magnitudes, infinities and NaN last
-      mx[c] = __vimax3_u32(mx[c], __float_as_uint(g_of(i, c)) & 0x7FFFFFFFu, __float_as_uint(g_of(i + 1, c)) & 0x7FFFFFFFu);
+    for (int c = 0; c < 2; ++c) {  // orders magnitudes, infinities and NaN last
+      const uint32_t a = __float_as_uint(g_of(i, c)) & 0x7FFFFFFFu, b = __float_as_uint(g_of(i + 1, c)) & 0x7FFFFFFFu;
+      mx[c] = __vimax3_u32(mx[c], a, b);
+      ex[c] += (a >> 23) + (b >> 23) + ((a ? 1u : 0u) << 20) + ((b ? 1u : 0u) << 20);
+    }
   *reinterpret_cast<uint2*>(&s_max[warp][2 * lane]) = make_uint2(mx[0], mx[1]);
+  *reinterpret_cast<uint2*>(&s_exp[warp][2 * lane]) = make_uint2(ex[0], ex[1]);
   __syncthreads();
   if (threadIdx.x < kGdCols) {
-    uint32_t t = 0;
+    uint32_t t = 0, x = 0;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) t = max(t, s_max[w][threadIdx.x]);
-    s_col[threadIdx.x] = t;
+    for (int w = 0; w < 16; ++w) {
+      t = max(t, s_max[w][threadIdx.x]);
+      x += s_exp[w][threadIdx.x];
+    }
+    s_col[0][threadIdx.x] = t;
+    s_col[1][threadIdx.x] = x;
   }
   cluster_sync_all();
   const uint32_t other = cluster_ctarank() ^ 1u;
+  int more = 0;  // digits beyond three that a column wants
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
-    mx[c] = max(s_col[2 * lane + c], __float_as_uint(ld_cluster_f32(cluster_map(&s_col[2 * lane + c], other))));
+  for (int c = 0; c < 2; ++c) {
+    mx[c] = max(s_col[0][2 * lane + c], __float_as_uint(ld_cluster_f32(cluster_map(&s_col[0][2 * lane + c], other))));
+    ex[c] = s_col[1][2 * lane + c] + __float_as_uint(ld_cluster_f32(cluster_map(&s_col[1][2 * lane + c], other)));
+    const uint32_t count = ex[c] >> 20, spread = (mx[c] >> 23) * count - (ex[c] & 0xFFFFFu);  // count times the distance
+    if (mx[c] < 0x7F800000u) more = max(more, spread <= 4 * count ? 0 : spread <= 12 * count ? 1 : 2);
+  }
+  more = __reduce_max_sync(0xFFFFFFFFu, more);  // the block's, the same in every warp
   cluster_sync_all();  // the other CTA has read this one's
   float up[2];
 #pragma unroll
@@ -200,32 +240,52 @@ __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
     if (warp == 0 && n + c < N && (blockIdx.x & 1) == 0)
       scale[chunk * N + n + c] = finite ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : __uint_as_float(0x7FC00000u);
   }
-#pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-#pragma unroll
-    for (int b = 0; b < 4; ++b) asm volatile("" : "+r"(raw[i + b][0]));  // keep dy, not the products
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t u[4], o[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) u[b] = biased_round<ND>(__fmul_rn(g_of(i + b, c), up[c]));
-      transpose4x4_bytes(u[0], u[1], u[2], u[3], o[0], o[1], o[2], o[3]);
-#pragma unroll
-      for (int j = 0; j < ND; ++j)
-        words[(j * kGdCols + 2 * lane + c) * 128 + ((8 * warp + i / 4) ^ lane)] = o[j] ^ 0x80808080u;
-    }
+  if (threadIdx.x == 0 && (blockIdx.x & 1) == 0) {
+    const int64_t groups = (ntiles + 3) / 4 * 4, g = n0 / kGdCols;
+    extra[chunk * groups + g] = static_cast<uint8_t>(more);
+    for (int64_t r = g + 1; g + 1 == ntiles && r < groups; ++r) extra[chunk * groups + r] = 0;
   }
-  __syncthreads();
-  // out: a warp writes one column's 512 bytes at a time
-  for (int r = warp; r < kGdCols * ND; r += 16) {
-    const int j = r / kGdCols, col = r % kGdCols, x = col >> 1;  // x: the lane that wrote the column
-    const int64_t m = mc + lane * 16;
-    if (n0 + col < N && m < Mp) {
-      uint4 v = *reinterpret_cast<const uint4*>(words + r * 128 + ((4 * lane) ^ (x & ~3)));
-      if (x & 1) v = make_uint4(v.y, v.x, v.w, v.z);
-      if (x & 2) v = make_uint4(v.z, v.w, v.x, v.y);
-      *reinterpret_cast<uint4*>(digits + (j * N + n0 + col) * Mp + m) = v;
+  // digits of four tokens at a time: byte j of `round`'s words into slot j
+  auto fill = [&](auto round) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) asm volatile("" : "+r"(raw[i + b][0]));  // keep dy, not the products
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t u[4], o[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) u[b] = round(__fmul_rn(g_of(i + b, c), up[c]));
+        transpose4x4_bytes(u[0], u[1], u[2], u[3], o[0], o[1], o[2], o[3]);
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          words[(j * kGdCols + 2 * lane + c) * 128 + ((8 * warp + i / 4) ^ lane)] = o[j] ^ 0x80808080u;
+      }
     }
+  };
+  // slots lo .. hi - 1 out, slot j as plane `top` - j: a warp writes one
+  // column's 512 bytes at a time
+  auto store = [&](int lo, int hi, int top) {
+    for (int r = lo * kGdCols + warp; r < hi * kGdCols; r += 16) {
+      const int j = r / kGdCols, col = r % kGdCols, x = col >> 1;  // x: the lane that wrote the column
+      const int64_t m = mc + lane * 16;
+      if (n0 + col < N && m < Mp) {
+        uint4 v = *reinterpret_cast<const uint4*>(words + r * 128 + ((4 * lane) ^ (x & ~3)));
+        if (x & 1) v = make_uint4(v.y, v.x, v.w, v.z);
+        if (x & 2) v = make_uint4(v.z, v.w, v.x, v.y);
+        *reinterpret_cast<uint4*>(digits + ((top - j) * N + n0 + col) * Mp + m) = v;
+      }
+    }
+  };
+  if (more == 0) fill([](float p) { return biased_round(p); });
+  else fill([](float p) { return biased_round_wide<0>(p); });
+  __syncthreads();
+  store(0, 3, 2);
+  if (more != 0) {
+    __syncthreads();
+    fill([](float p) { return biased_round_wide<3>(p); });
+    __syncthreads();
+    store(more == 1 ? 1 : 0, 2, 4);  // the fourth digit is slot 1, the fifth slot 0
   }
 }
 
@@ -234,7 +294,7 @@ __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
 // Persistent pairs of CTAs, tiles of 256 outputs n (128 TMEM lanes of each
 // CTA) by 256 inputs k (columns).  For each chunk of 1024 tokens the codes'
 // eight 256 x 128-token blocks (half in each CTA) stay in shared memory while
-// the ND digit planes pass through a ring of 128 x 128-token tiles against
+// the digit planes pass through a ring of 128 x 128-token tiles against
 // them: one digit of one chunk is a pass of eight steps into one of two TMEM
 // accumulators, and eight warps of each CTA add the finished pass to their
 // registers (128 values a thread) while the next one runs into the other.
@@ -274,10 +334,11 @@ struct Ring {
   }
 };
 
-template <int ND, typename OutT>
+template <typename OutT>
 __global__ void __launch_bounds__(kGwThreads, 1)
     k_grad_weight(const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_x,
-                  const float* __restrict__ scale, int M, int N, int K, void* __restrict__ dw) {
+                  const float* __restrict__ scale, const uint8_t* __restrict__ extra, int M, int N, int K,
+                  void* __restrict__ dw) {
   constexpr int S = kGwStages, SB = kGwSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -301,6 +362,10 @@ __global__ void __launch_bounds__(kGwThreads, 1)
   const int64_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
   const int chunks = (M + kGwChunk - 1) / kGwChunk;
   const int steps = (M + kGwBM - 1) / kGwBM;  // of 128 tokens
+  const int64_t groups = (static_cast<int64_t>(N) + kGwRows - 1) / kGwRows * 4;
+  auto extra_of = [&](int64_t t, int c) {  // of tile t's four blocks of 64 outputs
+    return __ldg(reinterpret_cast<const uint32_t*>(extra + c * groups + t / ktiles * 4));
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -337,14 +402,16 @@ __global__ void __launch_bounds__(kGwThreads, 1)
       bool ok = true;
       for (int64_t t = first; ok && t < tiles; t += stride) {
         const int n0 = static_cast<int>(t / ktiles) * kGwRows + 128 * rank;
-        for (int c = 0; ok && c < chunks; ++c)
-          for (int j = ND - 1; ok && j >= 0; --j)
+        for (int c = 0; ok && c < chunks; ++c) {
+          const int nd = gw_digits(extra_of(t, c));
+          for (int j = 0; ok && j < nd; ++j)
             for (int st = c * kGwPer; st < steps && st < (c + 1) * kGwPer; ++st, mine.next(S)) {
               ok = mbar_wait(empty_a + mine.s, mine.ph ^ 1u, abort_flag);
               if (!ok) break;
               if (rank == 0) mbar_arrive_expect_tx(full_a + mine.s, 2 * kGwABytes);
               tma2_load_3d(sA + mine.s * kGwABytes, &tm_d, full_a + mine.s, st * kGwBM, n0, j);
             }
+        }
       }
       // the other CTA's commits have arrived here before this one may exit
       for (int i = 0; ok && i < S; ++i, mine.next(S)) ok = mbar_wait(empty_a + mine.s, mine.ph ^ 1u, abort_flag);
@@ -370,14 +437,14 @@ __global__ void __launch_bounds__(kGwThreads, 1)
       bool ok = true;
       for (int64_t t = first; ok && t < tiles; t += stride)
         for (int c = 0; ok && c < chunks; ++c) {
-          const int nst = min(kGwPer, steps - c * kGwPer);
+          const int nst = min(kGwPer, steps - c * kGwPer), nd = gw_digits(extra_of(t, c));
           Ring b = rb;
-          for (int j = ND - 1; ok && j >= 0; --j, acc.next(2)) {
+          for (int j = 0; ok && j < nd; ++j, acc.next(2)) {
             ok = mbar_wait(acc_empty + acc.s, acc.ph ^ 1u, abort_flag);
             tc_fence_after();
             b = rb;
             for (int st = 0; ok && st < nst; ++st, ra.next(S), b.next(SB)) {
-              ok = (j != ND - 1 || mbar_wait(full_b + b.s, b.ph, abort_flag)) &&
+              ok = (j != 0 || mbar_wait(full_b + b.s, b.ph, abort_flag)) &&
                    mbar_wait(full_a + ra.s, ra.ph, abort_flag);
               if (!ok) break;
               tc_fence_after();
@@ -387,7 +454,7 @@ __global__ void __launch_bounds__(kGwThreads, 1)
               for (int kk = 0; kk < kGwBM / 32; ++kk)
                 tc2_mma_i8_ss(tmem_d + 256 * acc.s, ad + 2 * kk, bd + 2 * kk, idesc, st != 0 || kk != 0 ? 1u : 0u);
               tc2_commit_both(empty_a + ra.s);
-              if (j == 0) tc2_commit_both(empty_b + b.s);
+              if (j == nd - 1) tc2_commit_both(empty_b + b.s);
             }
             if (ok) tc2_commit_both(acc_full + acc.s);
           }
@@ -415,14 +482,17 @@ __global__ void __launch_bounds__(kGwThreads, 1)
       for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
 #pragma unroll 1
       for (int c = 0; ok && c < chunks; ++c, sp += N) {
-        float sc = __fmul_rn(__ldg(sp), ND == 3 ? 65536.0f : 256.0f);
+        float sc = __fmul_rn(__ldg(sp), 65536.0f);
+        const uint32_t ex = extra_of(t, c);
+        const int nd = gw_digits(ex), own = 3 + static_cast<int>((ex >> (8 * ((nw >> 6) & 3))) & 0xFFu);
 #pragma unroll 1
-        for (int j = 0; j < ND; ++j, pass.next(2)) {
+        for (int j = 0; j < nd; ++j, pass.next(2)) {
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full + pass.s, pass.ph, abort_flag));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int i = 0; i < 128; i += 16) {
+            if (j >= own) continue;  // a digit of other outputs in the tile, not written for these
             uint32_t v[16];
             tmem_ld_32x32b_x16(trow + 256 * pass.s + i, v);
             tmem_ld_wait();

@@ -194,46 +194,51 @@ bl_status launch_pdl_pairs(void (*kern)(KArgs...), unsigned blocks, int threads,
   return launch_status();
 }
 
-template <int ND, typename OutT>
-bl_status launch_gw(const CUtensorMap& td, const CUtensorMap& tx, const float* scale, int M, int N, int K, void* dw,
-                    int sms, cudaStream_t s) {
+template <typename OutT>
+bl_status launch_gw(const CUtensorMap& td, const CUtensorMap& tx, const float* scale, const uint8_t* extra, int M, int N,
+                    int K, void* dw, int sms, cudaStream_t s) {
   static int done[kMaxDevices] = {0};
-  auto kern = bl::k_grad_weight<ND, OutT>;
+  auto kern = bl::k_grad_weight<OutT>;
   if (!ensure_smem(kern, bl::kGwSmem, done)) return BL_ERR_CUDA;
   const int64_t tiles = ((int64_t{K} + bl::kGwBN - 1) / bl::kGwBN) * ((int64_t{N} + bl::kGwRows - 1) / bl::kGwRows);
   if (tiles > INT32_MAX / 2) return BL_ERR_UNSUPPORTED;
   const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
-  return launch_pdl_pairs(kern, static_cast<unsigned>(2 * pairs), bl::kGwThreads, bl::kGwSmem, s, td, tx, scale, M, N, K, dw);
+  return launch_pdl_pairs(kern, static_cast<unsigned>(2 * pairs), bl::kGwThreads, bl::kGwSmem, s, td, tx, scale, extra, M, N, K,
+                          dw);
 }
 
-// Workspace of grad_weight: the digit planes, their exponents, the codes.
+// Workspace of grad_weight: the digit planes, the codes, the planes' exponents
+// and which of them are used.
 struct GwScratch {
   int64_t Mp;
   uint8_t *digits, *codes;
   float* scale;
+  uint8_t* extra;
 };
 
-inline GwScratch gw_scratch(int64_t M, int64_t N, int64_t K, int nd, Scratch* ws) {
+inline GwScratch gw_scratch(int64_t M, int64_t N, int64_t K, Scratch* ws) {
   GwScratch g;
   g.Mp = round_up(M, 16);
-  g.digits = static_cast<uint8_t*>(ws->take(static_cast<size_t>(nd * N * g.Mp)));
+  g.digits = static_cast<uint8_t*>(ws->take(static_cast<size_t>(bl::kGdPlanes * N * g.Mp)));
   g.codes = static_cast<uint8_t*>(ws->take(static_cast<size_t>(K * g.Mp)));
-  g.scale = static_cast<float*>(ws->take(static_cast<size_t>((M + bl::kGwChunk - 1) / bl::kGwChunk * N * 4)));
+  const int64_t chunks = (M + bl::kGwChunk - 1) / bl::kGwChunk;
+  g.scale = static_cast<float*>(ws->take(static_cast<size_t>(chunks * N * 4)));
+  g.extra = static_cast<uint8_t*>(ws->take(static_cast<size_t>(chunks * (round_up(N, bl::kGwRows) / bl::kGdCols))));
   return g;
 }
 
-template <typename DyT, int ND>
+template <typename DyT>
 bl_status launch_gw_operands(const void* dy, const int8_t* xq, const float* eta, int64_t M, int64_t N, int64_t K,
                              const GwScratch& g, cudaStream_t s) {
   static int done[kMaxDevices] = {0};
-  auto kern = bl::k_gw_operands<DyT, ND>;
-  constexpr size_t smem = ND * bl::kGdCols * bl::kGdTokens;
+  auto kern = bl::k_gw_operands<DyT>;
+  constexpr size_t smem = 3 * bl::kGdCols * bl::kGdTokens;
   if (!ensure_smem(kern, smem, done)) return BL_ERR_CUDA;
   const int64_t digits = 2 * ((N + bl::kGdCols - 1) / bl::kGdCols) * ((M + bl::kGwChunk - 1) / bl::kGwChunk);
   const int64_t blocks = round_up(digits + ((K + 63) / 64) * ((M + 127) / 128), 2);
   if (blocks > INT32_MAX) return BL_ERR_UNSUPPORTED;
   return launch_pdl_pairs(kern, static_cast<unsigned>(blocks), bl::kGdThreads, smem, s, static_cast<unsigned>(digits), xq, K, g.codes, static_cast<const DyT*>(dy), eta, M, N, g.Mp,
-                    N % 2 == 0 ? 1 : 0, g.digits, g.scale);
+                    N % 2 == 0 ? 1 : 0, g.digits, g.scale, g.extra);
 }
 
 // One CTA per row, of as many warps as hold the row at kRgHeld chunks a thread.
@@ -486,7 +491,7 @@ bl_status bitlinear_grad_input(const void* dy, bl_dtype dydt, int64_t M, int64_t
 size_t bitlinear_grad_weight_workspace_bytes(int64_t M, int64_t N, int64_t K, bl_dtype dydt, bl_dtype dwdt) {
   if (train_sizes(M, N, K) != BL_OK || !dtype_ok(dydt) || !dtype_ok(dwdt)) return 0;
   Scratch ws(nullptr);
-  gw_scratch(M, N, K, dwdt == BL_F32 ? 3 : 2, &ws);
+  gw_scratch(M, N, K, &ws);
   return ws.used;
 }
 
@@ -511,24 +516,19 @@ bl_status bitlinear_grad_weight(const void* dy, bl_dtype dydt, const int8_t* xq,
     return BL_ERR_CUDA;
   }
   Scratch ws(workspace);
-  const int nd = dwdt == BL_F32 ? 3 : 2;
-  const GwScratch g = gw_scratch(M, N, K, nd, &ws);
-  if (dydt == BL_F32)
-    st = nd == 3 ? launch_gw_operands<float, 3>(dy, xq, eta, M, N, K, g, s)
-                 : launch_gw_operands<float, 2>(dy, xq, eta, M, N, K, g, s);
-  else
-    st = nd == 3 ? launch_gw_operands<__nv_bfloat16, 3>(dy, xq, eta, M, N, K, g, s)
-                 : launch_gw_operands<__nv_bfloat16, 2>(dy, xq, eta, M, N, K, g, s);
+  const GwScratch g = gw_scratch(M, N, K, &ws);
+  st = dydt == BL_F32 ? launch_gw_operands<float>(dy, xq, eta, M, N, K, g, s)
+                      : launch_gw_operands<__nv_bfloat16>(dy, xq, eta, M, N, K, g, s);
   if (st != BL_OK) return st;
   CUtensorMap td, tx;
-  if (!make_tmap(&td, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.digits, g.Mp, N, nd, g.Mp, bl::kGwBM, 128,
+  if (!make_tmap(&td, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.digits, g.Mp, N, bl::kGdPlanes, g.Mp, bl::kGwBM, 128,
                  CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.codes, g.Mp, K, 0, g.Mp, bl::kGwBM, bl::kGwBN / 2,
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return BL_ERR_CUDA;
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
-  return nd == 3 ? launch_gw<3, float>(td, tx, g.scale, m, n, k, dw, sms, s)
-                 : launch_gw<2, __nv_bfloat16>(td, tx, g.scale, m, n, k, dw, sms, s);
+  return dwdt == BL_F32 ? launch_gw<float>(td, tx, g.scale, g.extra, m, n, k, dw, sms, s)
+                        : launch_gw<__nv_bfloat16>(td, tx, g.scale, g.extra, m, n, k, dw, sms, s);
 }
 
 bl_status bitlinear_rmsnorm_grad(const void* dn, bl_dtype dndt, const int8_t* xq, const float* eta,

@@ -202,3 +202,76 @@ def test_the_low_planes_of_an_fp32_dy_are_not_cut_off(M, K, N):
     assert float(torch.tensor(want, dtype=F32)) == want
     dx = bl.grad_input(c.dy, c.packed, c.gamma, K, out_dtype=F32)
     assert (dx == want).all()
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+def test_weight_gradients_keep_all_of_a_column(out):
+    """dy eta / 127 of 1 + 2^-20 and -1: 2^-20 of the codes is left."""
+    c = still(70, 96, 40)
+    c.dy[3, :] = 1
+    c.dy[50, :] = -1
+    c.eta[3] = 127 * (1 + 2.0 ** -20)
+    c.xq[3] = c.xq[50] = torch.arange(-48, 48, device="cuda", dtype=torch.int8)
+    assert float(c.eta[3] / 127) == 1 + 2.0 ** -20
+    dw = bl.grad_weight(c.dy, c.xq, c.eta, out_dtype=out)
+    assert torch.equal(dw.float(), (c.xq[3].float() * 2.0 ** -20).expand(40, 96))
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("power", [6, 10, 14, 20, 26])
+@pytest.mark.parametrize("M,K,N", [(5, 40, 10), (700, 130, 300), (1100, 64, 70), (2500, 200, 513), (3000, 2100, 2500)])
+def test_a_column_with_one_large_token(M, K, N, power, dt, out):
+    """One token 2^power times the others, in some columns and one chunk: where its codes are zero the others' sum is
+    exact, as are the columns beside it."""
+    c = Case(M, K, N, dy_dtype=dt)
+    big = M - 2
+    cols = torch.arange(N, device="cuda") % 130 == 5
+    c.dy[big, cols] = 2.0 ** power
+    c.eta[big] = 127
+    c.xq[big, 1::2] = 0
+    val = c.dw()[0]
+    got = bl.grad_weight(c.dy, c.xq, c.eta, out_dtype=out)
+    assert torch.equal(val[:, 1::2], val[:, 1::2].to(F32).to(F64)) and torch.equal(val[~cols], val[~cols].to(F32).to(F64))
+    assert torch.equal(got[:, 1::2], val[:, 1::2].to(F32).to(out))
+    assert torch.equal(got[~cols], val[~cols].to(F32).to(out))
+
+
+def promised(c, out):
+    """Largest error the fixed point promises: in each chunk of 1024 tokens half a unit of the last digit for each
+    token's g: the largest is below 2^5 times the geometric mean for the digits taken (2^4, and the exponents' floors),
+    and half a unit at most 2^-22.99 of it (2^22 units, or half of 8355711); g
+    itself is rounded once (2^-24) and its factor once; each chunk adds up to five digits' sums in fp32."""
+    g = c.dy.to(F64).abs() * (c.eta.to(F64) / 127)[:, None]
+    bound, S = 0, g.t() @ c.xq.to(F64).abs()
+    for m in range(0, c.M, 1024):
+        part = g[m:m + 1024]
+        some = part > 0
+        mean = torch.exp2((torch.where(some, part, 1.0).log2().sum(0) / some.sum(0).clamp(min=1)))
+        bound = bound + (2.0 ** -17.9 * mean)[:, None] * c.xq[m:m + 1024].to(F64).abs().sum(0)[None, :]
+    adds = 5 * ((c.M + 1023) // 1024)
+    return bound + (2 + adds) * 2.0 ** -24 * S
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("kind", ["normal", "heavy", "tokens", "outlier"])
+@pytest.mark.parametrize("M,K,N", [(3, 64, 70), (200, 96, 300), (1024, 64, 64), (2500, 130, 72), (4100, 64, 513)])
+def test_weight_gradients_of_any_spread(M, K, N, kind, dt):
+    c = Case(M, K, N, whole=False)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    z = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    dy = z(M, N)
+    if kind == "heavy":
+        dy = dy.sign() * torch.exp(2 * z(M, N))
+    elif kind == "tokens":
+        dy = dy * torch.exp(3 * z(M, 1))
+    elif kind == "outlier":
+        c.eta[1] *= 2 ** 13
+        c.xq[1, 1:] = 0
+    c.dy = dy.to(dt)
+    val = c.dw()[0]
+    off = (bl.grad_weight(c.dy, c.xq, c.eta).to(F64) - val).abs()
+    assert (off <= promised(c, F32)).all(), float((off / promised(c, F32)).max())
+    off = (bl.grad_weight(c.dy, c.xq, c.eta, out_dtype=BF).to(F64) - val).abs()
+    assert (off <= promised(c, BF) + 2.0 ** -8 * (val.abs() + promised(c, BF))).all()

@@ -642,6 +642,8 @@ bl_status bitlinear_rmsnorm_grad(const void* dn, bl_dtype dndt, const int8_t* xq
  *   ids     in   int32, M, on the device; in any order.
  *   L, r    in   1 <= L <= 65535, 1 <= r <= 128 (adapters of smaller rank:
  *                zero rows of A); L r max(N, K) <= 2^40.
+ *   M       in   at most 65535 * 256 (BL_ERR_UNSUPPORTED beyond); K padded to
+ *                a multiple of 64 keeps 127 K < 2^31.
  *   y       out  M x N, fp32 or bf16; the sum is rounded once.
  * BL_FLAG_WEIGHTS_STATIC speaks of packed, gamma, A, B and scale.
  */

@@ -430,15 +430,22 @@ inline void la_scratch(int64_t M, int64_t K, Scratch* ws, LaScratch* q) {
   q->xsum = static_cast<int32_t*>(ws->take(static_cast<size_t>(M * 4)));
 }
 
+// Sizes of the forward pass with adapters: those above, K padded to 64 and
+// the projection's grid (65535 tiles of 256 tokens).
+inline bl_status fa_sizes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t r) {
+  const bl_status st = train_sizes(M, N, K), sa = adapter_sizes(L, r, N, K);
+  if (st == BL_ERR_INVALID_ARG || sa == BL_ERR_INVALID_ARG) return BL_ERR_INVALID_ARG;
+  if (st != BL_OK || sa != BL_OK || 127 * round_up(K, 64) >= (int64_t{1} << 31) || M > 65535 * 256) return BL_ERR_UNSUPPORTED;
+  return BL_OK;
+}
+
 // Checks that forward_adapters and linear_adapters share, in the order of
 // the other calls: arguments, sizes, then (after M = 0) the rest.
 bl_status fa_check(int64_t M, int64_t N, int64_t K, int64_t L, int64_t r, const uint8_t* packed, const float* gamma,
                    const void* A, const void* B, const float* scale, bl_dtype ydt) {
-  const bl_status st = train_sizes(M, N, K), sa = adapter_sizes(L, r, N, K);
-  if (st == BL_ERR_INVALID_ARG || sa == BL_ERR_INVALID_ARG) return BL_ERR_INVALID_ARG;
-  if (!dtype_ok(ydt) || !packed || !gamma || !A || !B || !scale) return BL_ERR_INVALID_ARG;
-  if (st != BL_OK || sa != BL_OK || 127 * round_up(K, 64) >= (int64_t{1} << 31)) return BL_ERR_UNSUPPORTED;
-  return BL_OK;
+  const bl_status st = fa_sizes(M, N, K, L, r);
+  if (st == BL_ERR_INVALID_ARG || !dtype_ok(ydt) || !packed || !gamma || !A || !B || !scale) return BL_ERR_INVALID_ARG;
+  return st;
 }
 
 inline bool adapters_aligned(const uint8_t* packed, const float* gamma, const void* A, const void* B, const float* scale,
@@ -552,7 +559,7 @@ bl_status bitlinear_rmsnorm_grad(const void* dn, bl_dtype dndt, const int8_t* xq
 }
 
 size_t bitlinear_forward_adapters_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r) {
-  if (train_sizes(M, N, K) != BL_OK || adapter_sizes(L, r, N, K) != BL_OK) return 0;
+  if (fa_sizes(M, N, K, L, r) != BL_OK) return 0;
   Scratch ws(nullptr);
   FaScratch f;
   fa_scratch(nullptr, nullptr, M, K, N, L, r, &ws, &f);

@@ -559,6 +559,8 @@ bl_status bitlinear_device_error(int32_t* code, void* stream);
  *     size is 0 takes NULL).  Overwritten; calls that may overlap on the
  *     GPU, captured graphs that may replay at the same time among them,
  *     need one each.
+ *   - An output shares no memory with an input (BL_ERR_INVALID_ARG), except
+ *     where a call says that it may.
  *   - M = 0 gives zero weight and adapter gradients and no other output.
  *   - Errors: BL_ERR_INVALID_ARG for null pointers, sizes below 1 (M below
  *     0), unknown dtypes or a workspace smaller than the query says;

@@ -3,6 +3,8 @@
 // bitlinear.cu after its own helpers.
 #pragma once
 
+#include <initializer_list>
+
 namespace {
 
 constexpr int64_t kTrainMaxDim = INT32_MAX / 2;
@@ -27,6 +29,21 @@ inline bl_status adapter_sizes(int64_t L, int64_t r, int64_t N, int64_t K) {
   if (r > kAdapterMaxRank || L > kAdapterMaxCount) return BL_ERR_UNSUPPORTED;
   if (L * r * (N > K ? N : K) > (int64_t{1} << 40)) return BL_ERR_UNSUPPORTED;
   return BL_OK;
+}
+
+// Whether an output shares memory with one of the inputs: kernels write while
+// other CTAs still read.
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+
+inline bool overlaps(const Span& out, std::initializer_list<Span> in) {
+  const auto at = [](const Span& s) { return reinterpret_cast<uintptr_t>(s.p); };
+  for (const Span& s : in)
+    if (out.p && s.p && at(out) < at(s) + static_cast<uint64_t>(s.bytes) && at(s) < at(out) + static_cast<uint64_t>(out.bytes))
+      return true;
+  return false;
 }
 
 // Device scratch handed out of the caller's workspace in 256-byte pieces.
@@ -483,6 +500,8 @@ bl_status bitlinear_grad_input(const void* dy, bl_dtype dydt, int64_t M, int64_t
   if (!dy || !dx || (need && !workspace) || workspace_bytes < need) return BL_ERR_INVALID_ARG;
   if (!aligned(dy, 16) || !aligned(packed, 16) || !aligned(dx, 16) || !aligned(gamma, 4) || !aligned(workspace, 256))
     return BL_ERR_ALIGNMENT;
+  if (overlaps({dx, M * K * dtype_bytes(dxdt)}, {{dy, M * N * dtype_bytes(dydt)}, {packed, N * ((K + 3) / 4)}, {gamma, 4}}))
+    return BL_ERR_INVALID_ARG;
   int sms = 148;
   if ((st = device_info(&sms)) != BL_OK) return st;
   const cudaStream_t s = as_stream(stream);
@@ -514,6 +533,8 @@ bl_status bitlinear_grad_weight(const void* dy, bl_dtype dydt, const int8_t* xq,
   if ((need && !workspace) || workspace_bytes < need) return BL_ERR_INVALID_ARG;
   if (!aligned(dy, 16) || !aligned(xq, 16) || !aligned(eta, 4) || !aligned(dw, 16) || !aligned(workspace, 256))
     return BL_ERR_ALIGNMENT;
+  if (overlaps({dw, N * K * dtype_bytes(dwdt)}, {{dy, M * N * dtype_bytes(dydt)}, {xq, M * K}, {eta, 4 * M}}))
+    return BL_ERR_INVALID_ARG;
   int sms = 148;
   if ((st = device_info(&sms)) != BL_OK) return st;
   const cudaStream_t s = as_stream(stream);
@@ -546,6 +567,10 @@ bl_status bitlinear_rmsnorm_grad(const void* dn, bl_dtype dndt, const int8_t* xq
   if (!dn || !xq || !eta || !rstd || !dx) return BL_ERR_INVALID_ARG;
   if (!aligned(dn, dtype_bytes(dndt)) || !aligned(dx, dtype_bytes(dxdt)) || !aligned(eta, 4) || !aligned(rstd, 4))
     return BL_ERR_ALIGNMENT;
+  const Span out = {dx, M * K * dtype_bytes(dxdt)};
+  const bool in_place = dx == dn && dxdt == dndt;  // a thread reads what it writes before
+  if (overlaps(out, {{xq, M * K}, {eta, 4 * M}, {rstd, 4 * M}}) || (!in_place && overlaps(out, {{dn, M * K * dtype_bytes(dndt)}})))
+    return BL_ERR_INVALID_ARG;
   int sms = 148;
   const bl_status st = device_info(&sms);
   if (st != BL_OK) return st;
@@ -578,6 +603,9 @@ bl_status bitlinear_forward_adapters(const int8_t* xq, const float* eta, const i
   if (!adapters_aligned(packed, gamma, A, B, scale, ids) || !aligned(xq, 16) || !aligned(y, 16) || !aligned(eta, 4) ||
       !aligned(xsum, 4) || !aligned(workspace, 256))
     return BL_ERR_ALIGNMENT;
+  if (overlaps({y, M * N * dtype_bytes(ydt)}, {{xq, M * K}, {eta, 4 * M}, {xsum, 4 * M}, {packed, N * ((K + 3) / 4)},
+                                              {gamma, 4}, {A, 2 * L * r * K}, {B, 2 * L * r * N}, {scale, 4 * L}, {ids, 4 * M}}))
+    return BL_ERR_INVALID_ARG;
   int sms = 148;
   if ((st = device_info(&sms)) != BL_OK) return st;
   const cudaStream_t s = as_stream(stream);
@@ -613,6 +641,9 @@ bl_status bitlinear_linear_adapters(const void* x, bl_dtype xdt, int64_t M, int6
   if (!adapters_aligned(packed, gamma, A, B, scale, ids) || !aligned(x, dtype_bytes(xdt)) || !aligned(y, 16) ||
       !aligned(workspace, 256))
     return BL_ERR_ALIGNMENT;
+  if (overlaps({y, M * N * dtype_bytes(ydt)}, {{x, M * K * dtype_bytes(xdt)}, {packed, N * ((K + 3) / 4)}, {gamma, 4},
+                                              {A, 2 * L * r * K}, {B, 2 * L * r * N}, {scale, 4 * L}, {ids, 4 * M}}))
+    return BL_ERR_INVALID_ARG;
   int sms = 148;
   if ((st = device_info(&sms)) != BL_OK) return st;
   const cudaStream_t s = as_stream(stream);
@@ -673,6 +704,11 @@ bl_status bitlinear_adapters_grad(const void* dy, bl_dtype dydt, const int8_t* x
   if (!adapters_aligned(packed, gamma, A, B, scale, ids) || !aligned(dy, 16) || !aligned(xq, 16) ||
       !aligned(dx, 16) || !aligned(dA, 16) || !aligned(dB, 16) || !aligned(eta, 4) || !aligned(workspace, 256))
     return BL_ERR_ALIGNMENT;
+  for (const Span& out : {Span{dx, M * K * dtype_bytes(dxdt)}, Span{dA, L * r * K * dtype_bytes(dabdt)},
+                          Span{dB, L * r * N * dtype_bytes(dabdt)}})
+    if (overlaps(out, {{dy, M * N * dtype_bytes(dydt)}, {xq, M * K}, {eta, 4 * M}, {packed, N * ((K + 3) / 4)}, {gamma, 4},
+                       {A, 2 * L * r * K}, {B, 2 * L * r * N}, {scale, 4 * L}, {ids, 4 * M}}))
+      return BL_ERR_INVALID_ARG;
   int sms = 148;
   if ((st = device_info(&sms)) != BL_OK) return st;
   const cudaStream_t s = as_stream(stream);

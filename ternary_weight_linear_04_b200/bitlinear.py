@@ -129,25 +129,25 @@ def rmsnorm_quant_act(x, stream=None, out=None, want_rstd=False):
     Activations (M x K, bf16, CUDA) -> (xq int8 M x K, eta fp32 M, xsum int32 M)
     of the normalised rows; with want_rstd also rstd (fp32 M), the factor each
     row was multiplied by (what rmsnorm_grad needs)."""
-    _require_cuda(x)
     if x.dim() != 2 or x.dtype != torch.bfloat16:
         raise ValueError("x must be a 2-D bfloat16 tensor")
     M, K = x.shape
     dev = x.device
-    if out is None:
-        out = (torch.empty((M, K), dtype=torch.int8, device=dev),
-               torch.empty(M, dtype=torch.float32, device=dev),
-               torch.empty(M, dtype=torch.int32, device=dev))
-    xq, eta, xsum = out
-    if want_rstd:
-        rstd = torch.empty(M, dtype=torch.float32, device=dev)
-        check(_lib.lib().bitlinear_rmsnorm_quant_act_rstd(
-            _ptr(x), _DTYPES[x.dtype], M, K, _ptr(xq), _ptr(eta), _ptr(xsum), _ptr(rstd),
-            _stream(stream)), "bitlinear_rmsnorm_quant_act_rstd")
-        return xq, eta, xsum, rstd
-    check(_lib.lib().bitlinear_rmsnorm_quant_act(_ptr(x), _DTYPES[x.dtype], M, K, _ptr(xq),
-                                                 _ptr(eta), _ptr(xsum), _stream(stream)),
-          "bitlinear_rmsnorm_quant_act")
+    with _place(stream, x):
+        if out is None:
+            out = (torch.empty((M, K), dtype=torch.int8, device=dev),
+                   torch.empty(M, dtype=torch.float32, device=dev),
+                   torch.empty(M, dtype=torch.int32, device=dev))
+        xq, eta, xsum = out
+        if want_rstd:
+            rstd = torch.empty(M, dtype=torch.float32, device=dev)
+            check(_lib.lib().bitlinear_rmsnorm_quant_act_rstd(
+                _ptr(x), _DTYPES[x.dtype], M, K, _ptr(xq), _ptr(eta), _ptr(xsum), _ptr(rstd),
+                _stream_of(x)), "bitlinear_rmsnorm_quant_act_rstd")
+            return xq, eta, xsum, rstd
+        check(_lib.lib().bitlinear_rmsnorm_quant_act(_ptr(x), _DTYPES[x.dtype], M, K, _ptr(xq),
+                                                     _ptr(eta), _ptr(xsum), _stream_of(x)),
+              "bitlinear_rmsnorm_quant_act")
     return xq, eta, xsum
 
 

@@ -21,9 +21,12 @@ namespace bl {
 __device__ int g_device_error;
 
 #ifdef BL_TEST_HOOKS
-// Fault-injection build used only by the timeout test: waits give up after
+// Fault-injection build used only by the timeout tests: waits give up after
 // 1 ms, and g_test_fault (set by bitlinear_test_set_fault) makes a kernel
-// withhold one barrier arrival so that a wait runs out.
+// withhold one barrier arrival so that a wait runs out: 1 the first unpacked
+// stage of k_gemm_tc, 2 the tile's adapters and 3 their first step there, 4 the
+// third expanded step of k_grad_input, 5 and 6 the first pass read by CTA 0 or
+// 1 of a pair of k_grad_weight.
 constexpr unsigned long long kWaitLimitNs = 1000000ull;  // 1 ms per wait
 __device__ int g_test_fault;
 #else

@@ -214,18 +214,13 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
       // 32 bytes.  Keeps the single issuing thread's work per stage short.
       const uint64_t a_desc0 = make_sw128_kmajor_desc(smem_u32(sA));
       const uint64_t b_desc0 = make_sw128_kmajor_desc(smem_u32(sB));
-      bool ok = true;
+      bool ok = true, some = false;  // some: MMAs may be in flight
       for (int i = 0; i < nkt; ++i) {
         const int s = i % S;
         const uint32_t par = static_cast<uint32_t>(i / S) & 1u;
         ok = mbar_wait(full_b + s, par, abort_flag) && mbar_wait(full_a + s, par, abort_flag);
-        if (!ok) {
-          if (i > 0) {  // MMAs are in flight: let them finish before TMEM is freed
-            tc_commit(drain);
-            mbar_drain(drain, 0);
-          }
-          break;
-        }
+        if (!ok) break;
+        some = true;
         tc_fence_after();
         const uint64_t ad = a_desc0 + static_cast<uint64_t>(s * (Cfg::kABytes >> 4));
         const uint64_t bd = b_desc0 + static_cast<uint64_t>(s * (Cfg::kBBytes >> 4));
@@ -242,11 +237,7 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
         for (int i = nkt; i < nkt + asteps; ++i) {
           const int s = i % S;
           ok = mbar_wait(full_a + s, static_cast<uint32_t>(i / S) & 1u, abort_flag);
-          if (!ok) {
-            tc_commit(drain);
-            mbar_drain(drain, 0);
-            break;
-          }
+          if (!ok) break;
           tc_fence_after();
           const uint64_t da = a_desc0 + static_cast<uint64_t>(s * (Cfg::kABytes >> 4));
           const uint64_t db = b_desc0 + static_cast<uint64_t>(s * (Cfg::kBBytes >> 4));
@@ -256,7 +247,12 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
           tc_commit(empty + s);
         }
       }
-      if (ok) tc_commit(accum_full);
+      if (ok) {
+        tc_commit(accum_full);
+      } else if (some) {  // whichever wait gave up: the MMAs finish before TMEM is freed
+        tc_commit(drain);
+        mbar_drain(drain, 0);
+      }
     }
   } else if (warp < 2 + kTcUnpackWarps) {
     // ---------------- unpack, then epilogue (warps 2..9)
@@ -313,7 +309,10 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
                               [] { asm volatile("bar.sync 1, 256;" ::: "memory"); }) * group;
     if (t == 0) {
       *s_entries = entries;
-      mbar_arrive(counted);
+#ifdef BL_TEST_HOOKS
+      if (g_test_fault != 2)
+#endif
+        mbar_arrive(counted);
     }
     const int asteps = (entries + 63) >> 6;
     // A thread takes the piece t % 8 (8 entries) of the rows t / 8 + 32 x, of
@@ -381,6 +380,9 @@ __global__ void __launch_bounds__(tc_threads(AD), BM <= 32 && !AD ? 2 : 1)
         if (row0 + 32 * y4 < BM) *reinterpret_cast<uint4*>(sB + s * Cfg::kBBytes + at + 4096 * y4) = vu[y4];
       fence_proxy_async_smem();
       __syncwarp();
+#ifdef BL_TEST_HOOKS
+      if (g_test_fault == 3 && t < 32 && i == nkt) continue;
+#endif
       if (lane == 0) mbar_arrive(full_a + s);
       if (i + 1 < nkt + asteps) load((i + 1 - nkt) * 64);
     }

@@ -378,6 +378,9 @@ __global__ void __launch_bounds__(kGiThreads, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
+#ifdef BL_TEST_HOOKS
+      if (g_test_fault == 4 && warp == 2 && i == 2) continue;  // behind two steps whose MMAs are in flight
+#endif
       if (lane == 0) mbar_arrive(full_b + s);
     }
     // ---------------- adapters

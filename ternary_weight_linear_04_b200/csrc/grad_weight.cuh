@@ -502,7 +502,11 @@ __global__ void __launch_bounds__(kGwThreads, 1)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_remote(acc_empty + pass.s, 0);
+#ifdef BL_TEST_HOOKS
+          const bool held = (g_test_fault == 5 && rank == 0 || g_test_fault == 6 && rank == 1) && warp == 2 && t == first && c == 0 && j == 0;
+          if (!held)
+#endif
+            if (lane == 0) mbar_arrive_remote(acc_empty + pass.s, 0);
           sc = __fmul_rn(sc, 0.00390625f);
         }
       }

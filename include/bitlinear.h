@@ -695,6 +695,15 @@ bl_status bitlinear_adapters_grad(const void* dy, bl_dtype dydt, const int8_t* x
                                   int64_t L, int64_t r, void* dx, bl_dtype dxdt, void* dA, void* dB,
                                   bl_dtype dabdt, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Tokens of a tile of the tensor-core kernels that a device of `sms` SMs runs
+ * for these sizes: of bitlinear_grad_input (and of dx in
+ * bitlinear_adapters_grad) with grad not 0, else of the projection with
+ * adapters where it takes the tensor cores (more than 16 tokens).  0 for sizes
+ * that the call refuses.  Host only: for inspection and tests.
+ */
+int32_t bitlinear_tile_tokens(int grad, int64_t M, int64_t K, int64_t N, int sms);
+
 /* Library version as "major.minor.patch" (static storage). */
 const char* bitlinear_version(void);
 

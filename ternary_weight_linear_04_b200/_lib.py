@@ -55,6 +55,7 @@ SIGNATURES = {
     "bitlinear_forward3": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _I64, _P, _I, _P, _P]),
     "bitlinear_grad_input_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I]),
     "bitlinear_grad_input": (_I, [_P, _I, _I64, _I64, _P, _P, _I64, _P, _I, _P, _SZ, _P]),
+    "bitlinear_tile_tokens": (ctypes.c_int32, [_I, _I64, _I64, _I64, _I]),
     "bitlinear_grad_weight_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I, _I]),
     "bitlinear_grad_weight": (_I, [_P, _I, _P, _P, _I64, _I64, _I64, _P, _I, _P, _SZ, _P]),
     "bitlinear_rmsnorm_quant_act_rstd": (_I, [_P, _I, _I64, _I64, _P, _P, _P, _P, _P]),

@@ -588,6 +588,15 @@ def adapters_grad(dy, xq, eta, packed, gamma, A, B, scale, ids, out_dtype=torch.
     return dx, dA, dB
 
 
+def tile_tokens(M, K, N, grad=False, sms=None):
+    """Tokens of a tile of the projection with adapters (more than 16 tokens),
+    or with grad of the input gradient (see bitlinear_tile_tokens).  sms
+    defaults to the current device's SM count."""
+    if sms is None:
+        sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    return int(_lib.lib().bitlinear_tile_tokens(1 if grad else 0, M, K, N, sms))
+
+
 def select_path(M, K, N, xq, packed, y, y_int=None):
     return PATH_NAMES[int(_lib.lib().bitlinear_select_path(M, K, N, _ptr(xq), _ptr(packed),
                                                            _ptr(y), _ptr(y_int)))]

@@ -166,12 +166,17 @@ bl_status gi_operands(const void* dy, bl_dtype dydt, const uint8_t* packed, int6
   return st;
 }
 
+// Tokens of an input gradient's tile: 256 where such tiles fill most of the
+// GPU, else 128.
+inline int gi_tokens(int64_t M, int64_t K, int sms) {
+  const int64_t ktiles = (K + bl::kGiBN - 1) / bl::kGiBN;
+  return M > 128 && ktiles * ((M + 255) / 256) * 4 > int64_t{3} * sms ? 256 : 128;
+}
+
 // dx = gamma dy W~ (+ v A where a.v is given), the copies made.
 bl_status run_grad_input(const GiOperands& o, bl_dtype dxdt, bl::GiArgs a, int sms, cudaStream_t s) {
   const Rows &dy = o.dy, &w = o.w;
-  // 256 tokens a tile where such tiles fill most of the GPU, else 128
-  const int64_t ktiles = (a.K + bl::kGiBN - 1) / bl::kGiBN;
-  const int H = a.M > 128 && ktiles * ((a.M + 255) / 256) * 4 > int64_t{3} * sms ? 2 : 1;
+  const int H = gi_tokens(a.M, a.K, sms) / 128;
   CUtensorMap tdy, tw;
   if (!make_tmap(&tdy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy.p, a.N, a.M, dy.planes, dy.stride, bl::kGiBK, 128 * H,
                  CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -512,6 +517,12 @@ bl_status bitlinear_grad_input(const void* dy, bl_dtype dydt, int64_t M, int64_t
   if ((st = gi_operands(dy, dydt, packed, M, N, K, &ws, &o, sms, s)) != BL_OK) return st;
   if ((st = run_pads(o.pads, sms, s)) != BL_OK) return st;
   return run_grad_input(o, dxdt, a, sms, s);
+}
+
+int32_t bitlinear_tile_tokens(int grad, int64_t M, int64_t K, int64_t N, int sms) {
+  if (M < 1 || sms < 1 || (grad ? train_sizes(M, N, K) : fa_sizes(M, N, K, 1, 1)) != BL_OK) return 0;
+  return grad ? gi_tokens(M, K, sms)
+              : tc_tokens<true>(static_cast<int>(M), static_cast<int>(round_up(K, 64)), static_cast<int>(N), sms);
 }
 
 size_t bitlinear_grad_weight_workspace_bytes(int64_t M, int64_t N, int64_t K, bl_dtype dydt, bl_dtype dwdt) {

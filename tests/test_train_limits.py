@@ -49,3 +49,10 @@ def test_an_output_on_an_input_is_refused(L, name, base, out, inputs):
     if name == "rmsnorm_grad":
         assert call(fn, spread, p_dx=spread["p_dn"], dxdt=0) == BAD  # of another type
         assert call(fn, spread, p_dx=spread["p_dn"] + 2) == BAD
+
+
+def test_tiles_of_refused_sizes(L):
+    tile = L.bitlinear_tile_tokens
+    assert tile(0, 300, 130, 11003, 148) == 256 and tile(1, 300, 3200, 70, 148) == 128
+    assert tile(0, 0, 64, 64, 148) == tile(0, 65535 * 256 + 1, 16, 8, 148) == tile(0, 4, 64, 64, 0) == 0
+    assert tile(1, 0, 64, 64, 148) == tile(1, 1 << 30, 64, 64, 148) == tile(1, 4, 0, 64, 148) == 0

@@ -1,4 +1,4 @@
-"""BitNet b1.58 BitLinear forward on one NVIDIA B200 (sm_100a).
+"""BitNet b1.58 BitLinear forward and backward on one NVIDIA B200 (sm_100a).
 
 The compute lives in ``libbitlinear.so`` (CUDA, C ABI in
 ``include/bitlinear.h``); this package is its thin Python binding.
@@ -10,7 +10,8 @@ __version__ = "0.1.0"
 
 def __getattr__(name):
     if name in ("pack_weights", "quant_act", "forward", "linear", "BitLinear", "packed_bytes",
-                "select_path", "device_error"):
+                "select_path", "device_error", "rmsnorm_quant_act", "grad_input", "grad_weight", "rmsnorm_grad",
+                "forward_adapters", "linear_adapters", "adapters_grad"):
         from . import bitlinear
         return getattr(bitlinear, name)
     raise AttributeError(name)

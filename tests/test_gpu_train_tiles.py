@@ -94,3 +94,35 @@ def test_input_gradient_keeps_what_is_not_finite_apart(tile, M, K, N, out, bad):
     rest = torch.arange(K, device="cuda") != K - 3
     assert torch.equal(got[:, rest], dx[:, rest])
     assert not got[own, K - 3].isfinite().any()
+
+
+@pytest.mark.parametrize("M", [1, 2, 8, 9, 16])
+@pytest.mark.parametrize("K,N,L,r", [(64, 40001, 3, 8), (4096, 11008, 2, 16), (256, 100000, 5, 5), (8192, 9000, 1, 40)])
+def test_few_tokens_on_the_tensor_cores(M, K, N, L, r):
+    """Layers that the register-resident kernels do not take: tiles of 16 tokens."""
+    assert bl.decode_regm_shape(max(M, 2), K, N, sms=148) is None and bl.decode_mma_shape(M, K, N, sms=148) is None
+    assert bl.tile_tokens(M, K, N, sms=148) == 16
+    c = Case(M, K, N, L, r)
+    for out in (BF, F32):
+        same(bl.forward_adapters(c.xq, c.eta, c.xsum, c.packed, c.gamma, N, c.A, c.B, c.scale, c.ids, out_dtype=out), c.y())
+    x = torch.randn(M, K, device="cuda").to(BF)
+    c.xq, c.eta, c.xsum = bl.quant_act(x)
+    y = bl.linear_adapters(x, c.packed, c.gamma, N, c.A, c.B, c.scale, c.ids, out_dtype=F32)
+    near(y, c.y(), K // 64 + 48)
+
+
+@pytest.mark.parametrize("M", [1, 5, 12])
+def test_the_register_kernels_switched_off(M):
+    c = Case(M, 320, 200, 3, 8)
+    args = (c.xq, c.eta, c.xsum, c.packed, c.gamma, 200, c.A, c.B, c.scale, c.ids)
+    try:
+        bl.set_decode_reg(False)
+        bl.set_decode_mma(False)
+        same(bl.forward_adapters(*args, out_dtype=F32), c.y())
+        x = torch.randn(M, 320, device="cuda").to(BF)
+        off = bl.linear_adapters(x, *args[3:5], 200, *args[6:], out_dtype=F32)
+    finally:
+        bl.set_decode_reg(True)
+        bl.set_decode_mma(True)
+    c.xq, c.eta, c.xsum = bl.quant_act(x)
+    near(off, c.y(), 320 // 8 + 48)

@@ -573,9 +573,14 @@ bl_status bitlinear_device_error(int32_t* code, void* stream);
  *   dy      in   M x N, fp32 or bf16.
  *   packed, gamma   in   as written by bitlinear_pack_weights for N x K.
  *   dx      out  M x K, fp32 or bf16.
- * bf16 products (an fp32 dy as three parts that hold all of it) summed in
- * fp32.  K of a multiple of 64 and N of 8 are read in place; other sizes are
- * copied once into the workspace.
+ * bf16 products (an fp32 dy as three parts that hold all of it, the smallest
+ * summed first) summed by the tensor core in fp32, which cuts a sum off every
+ * 16 terms where other sums round: fp32 results of like-sized gradients come
+ * out 1e-7 to 2e-7 off in the 2-norm (N = 11008), of magnitudes that spread
+ * over five decades 2e-6 (bf16 dy) to 1e-5 (fp32 dy), where sums that round
+ * are 1e-6 off.  An infinity in dy gives infinities, and NaN where it meets a
+ * zero weight.  K of a multiple of 64 and N of 8 are read in place; other
+ * sizes are copied once into the workspace.
  */
 size_t bitlinear_grad_input_workspace_bytes(int64_t M, int64_t N, int64_t K, bl_dtype dydt);
 bl_status bitlinear_grad_input(const void* dy, bl_dtype dydt, int64_t M, int64_t N, const uint8_t* packed,
@@ -634,9 +639,10 @@ bl_status bitlinear_rmsnorm_grad(const void* dn, bl_dtype dndt, const int8_t* xq
  * (the projection alone where ids[m] is outside [0, L), -1 by convention).
  * The adapters read the same 8-bit tokens as the projection; x^ A^T is
  * summed in fp32 and enters the second product as it is or as three bf16
- * parts that hold all of it.  A token's output depends on no other token's
- * adapter, whatever that one holds (infinities and NaN too).  No counterpart
- * on the pages.
+ * parts that hold all of it.  A token's output is made of its own adapter's
+ * values alone, whatever another one holds (infinities and NaN too); which
+ * adapters share its tile may change the order of its sum, and so its last
+ * bit.  No counterpart on the pages.
  *   xq, eta, xsum, packed, gamma, flags   in   as for bitlinear_forward_path.
  *   A       in   bf16, L x r x K.
  *   B       in   bf16, L x N x r.
@@ -680,8 +686,8 @@ bl_status bitlinear_linear_adapters(const void* x, bl_dtype xdt, int64_t M, int6
  *   dB_a = sum over the tokens of a: dy^T u   L x N x r
  * v and u enter their products as three bf16 parts that hold all of them.
  * What an adapter's factors hold, infinities and NaN too, reaches its own
- * tokens and its own gradients only.  An adapter that no token uses gets
- * zeros.  dx may be NULL (not computed; packed and gamma may then be NULL
+ * tokens and its own gradients only; an infinity in dy may come out of dB as
+ * NaN.  An adapter that no token uses gets zeros.  dx may be NULL (not computed; packed and gamma may then be NULL
  * too), and so may dA and dB together.
  *   dabdt   in   type of dA and dB, fp32 or bf16.
  *   other arguments as for bitlinear_forward_adapters and

@@ -185,8 +185,9 @@ __global__ void __launch_bounds__(kAuThreads)
 // where those without one do.  One CTA: a stable counting sort by the adapter's
 // low and (L > 255) high eight bits.  Each of 32 warps counts and places its
 // own stretch of the tokens, ranks within a step of 32 by matching keys, so
-// the order needs no atomics.  About 4 us for 2048 tokens, all latency.  With it the kernels behind read one or two
-// adapters a tile whatever the order of the requests.
+// the order needs no atomics.  7 us for 2048 tokens (cold caches), all latency.
+// With it u, v, dA and dB read one or two adapters a tile whatever the order of
+// the requests.
 
 constexpr int kSortThreads = 1024;
 
@@ -280,8 +281,8 @@ __global__ void __launch_bounds__(kSortThreads)
 // and pass through shared memory (ldmatrix.trans).  A row's fragment is zeroed
 // for the adapters that are not its own.  The tokens' values of the next step
 // are loaded while this one's are multiplied: a warp's steps are a chain of
-// loads, and the time of the kernel: with the gradients behind it 76 us for u
-// and v of 2048 tokens (K 4096, N 11008, rank 16; reading dy takes 7).
+// loads, and the time of the kernel: 36 us for u and v of 2048 tokens (K 4096,
+// N 11008, rank 16, cold caches; reading dy takes 7).
 
 struct UvSide {
   int is_v;                // u: x = codes, F = A; v: x = dy, F = B
@@ -601,7 +602,7 @@ __global__ void __launch_bounds__(kUvThreads, 1) k_adapter_uv(const __grid_const
 // sum by an addition that rounds.  The next chunk's rows are loaded while one is
 // multiplied.
 // Bound by the longest adapter's chain of chunks.  2048 tokens of 4 adapters,
-// K 4096, N 11008: 38 us (x~ and dy are 53 MB: 8 us).
+// K 4096, N 11008: 47 us with cold caches (x~ and dy are 53 MB: 8 us).
 
 struct DabSide {
   const void* x;     // M x C: codes (dA) or dy (dB)

@@ -91,7 +91,8 @@ struct TcCfg {
 // the unpack warps behind the loop, 16 us a tile of 256 tokens were left
 // open), and take half of the epilogue.  Entries of several adapters share a
 // step, so small ranks hardly pad.  2048 x 4096 x 11008, 8 adapters of rank 16
-// packed: 133 us (cold) against 111 for the projection alone.  Of a K split only CTA 0 has these steps.
+// packed (two or three steps a tile): 145 us against 111 for the projection
+// alone, cold caches.  Of a K split only CTA 0 has these steps.
 constexpr int kTcAdWarps = 8;
 constexpr int tc_threads(bool ad) { return kTcThreads + (ad ? 32 * kTcAdWarps : 0); }
 

@@ -63,7 +63,8 @@ constexpr int kGdTokens = 512;  // of a CTA that makes digits; two CTAs share a 
 // rate of an add): adding 1.5 2^23 rounds a value below 2^22 to an integer in
 // the low bits, and the bytes of q + 0x808080 with their top bits flipped
 // are the signed digits.  2048 x 11008, three digits, cold: 101 us with
-// conversions, bound by their pipe, 45 us so (41 instructions a value).
+// conversions, bound by their pipe, 46 us so (44 instructions a value, three
+// of them for the spread).
 constexpr int kGdCols = 64;
 constexpr int kGdThreads = 512;
 
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
 // Digits go from high to low.  One CTA a tile (128 x 256) reads 12 KB of
 // shared memory for each MMA of 128 cycles beside 4 KB that TMA writes, all
 // that it can; a pair reads 8 KB in each.  2048 x 4096 x 11008, three digits:
-// about 235 us, 2.4e15 integer operations a second; the tensor pipe waits for
+// about 240 us, 2.3e15 integer operations a second; the tensor pipe waits for
 // the passes to be added (a TMEM load and its use follow one another in two
 // warps a scheduler), which is also why a chunk is 1024 tokens and not 512
 // (322 -> 264 us for the whole call).

@@ -143,8 +143,8 @@ bl_status launch_gi(const CUtensorMap& tdy, const CUtensorMap& tw, const bl::GiA
   if (H == 1) {
     // as many CTAs along the contraction, up to 8, as the GPU has room for
     // beside the tiles, four steps each at least.  77 x 3200 x 8640, 34 tiles:
-    // 32 us with one CTA a tile, 21 with two, 27 with four, which do not all
-    // fit
+    // 32 us with one CTA a tile, 21 with two, 17 with three, 27 with four, which
+    // do not all fit
     const int64_t steps = (int64_t{a.N} + bl::kGiBK - 1) / bl::kGiBK * a.planes;
     split = steps >= 32 ? 8 : steps >= 8 ? static_cast<int>(steps / 4) : 1;
     while (split > 1 && tiles > cluster_room(kern, bl::kGiThreads, smem, split, room)) --split;

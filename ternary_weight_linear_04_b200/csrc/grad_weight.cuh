@@ -51,13 +51,12 @@ constexpr int kGdTokens = 512;  // of a CTA that makes digits; two CTAs share a 
 // Digits of a 64-column, 512-token tile (a cluster of two CTAs makes a chunk's
 // and shares its maxima): lane = two neighbouring columns, a warp takes 32
 // tokens, held as they were read (two bf16 in a register) between the column's
-// maximum and the digits.  digits: five planes of N x Mp
-// bytes (Mp a multiple of 16, zero past M), the largest digit first, the
-// fourth and fifth written where they are used; extra[chunk * groups + n / 64]
-// = 0, 1 or 2, how many of those are (groups: column blocks, rounded up to
-// four); scale[chunk * N + n] = 2^-e, or NaN where the column holds an
-// infinity or a NaN (its whole gradient row is then NaN, as it would be in
-// floating point).
+// maximum and the digits.  digits: five planes of N x Mp bytes (Mp a multiple
+// of 16, zero past M), the largest digit first, the fourth and fifth written
+// where they are used; extra[chunk * groups + n / 64] = 0, 1 or 2, how many of
+// those are (groups: column blocks, rounded up to four); scale[chunk * N + n] =
+// 2^-e, or NaN where the column holds an infinity or a NaN (its whole gradient
+// row is then NaN).
 //
 // Rounding and splitting use no conversion instruction (a quarter of the
 // rate of an add): adding 1.5 2^23 rounds a value below 2^22 to an integer in
@@ -137,10 +136,10 @@ __global__ void __launch_bounds__(kGdThreads, sizeof(DyT) == 2 ? 2 : 1)
   constexpr int kBits = 22;
   constexpr int kRegs = sizeof(DyT) == 2 ? 1 : 2;
   extern __shared__ __align__(16) uint8_t smem[];  // 3 x 64 columns x 512 bytes, words XORed with the lane
-  __shared__ uint32_t s_max[16][kGdCols];
+  __shared__ __align__(16) uint32_t s_max[16][kGdCols];
   __shared__ uint32_t s_col[2][kGdCols];
   __shared__ float s_f[kGdTokens];
-  __shared__ uint32_t s_codes[64][33];
+  __shared__ __align__(16) uint32_t s_codes[64][33];
   auto& s_exp = reinterpret_cast<uint32_t(&)[16][kGdCols]>(s_codes);  // (other blocks': two CTAs have to fit an SM)
   uint32_t* words = reinterpret_cast<uint32_t*>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
